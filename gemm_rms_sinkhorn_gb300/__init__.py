@@ -70,6 +70,23 @@ _SIGS = {
     "mhc_forward_host": ([_vp, _vp, _vp, _f32, _f32, _f32, _vp, _i32, _i64, _i32, _i64,
                           _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "mhc_gemm_rms_noalloc": ([_vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp], _i32),
+    "mhc_embed": ([_vp, _vp, _f32, _i64, _i64, _i32, _i64, _vp, _vp], _i32),
+    "mhc_embed_f32": ([_vp, _vp, _f32, _i64, _i64, _i32, _i64, _vp, _vp], _i32),
+    "mhc_embed_backward_workspace_bytes": ([_i64, _i64, _i32, _i64], _sz),
+    "mhc_embed_backward": ([_vp, _vp, _f32, _i32, _i64, _i64, _i32, _i64, _vp, _vp, _sz, _vp],
+                           _i32),
+    "mhc_ckpt_pack": ([_vp, _i64, _i32, _i64, _vp, _vp, _vp], _i32),
+    "mhc_ckpt_unpack": ([_vp, _vp, _i64, _i32, _i64, _vp, _vp], _i32),
+    "mhc_post_res_apply_ckpt": ([_vp, _vp, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp], _i32),
+    "mhc_post_res_apply_ckpt_f32": ([_vp, _vp, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _vp],
+                                    _i32),
+    "mhc_post_res_apply_backward": ([_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp,
+                                     _vp], _i32),
+    "mhc_post_res_apply_backward_f32": ([_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp,
+                                         _vp], _i32),
+    "mhc_pre_backward_workspace_bytes": ([_i64, _i32, _i64, _i32], _sz),
+    "mhc_pre_backward": ([_vp, _vp, _vp, _vp, _vp, _f32, _f32, _f32, _vp, _i32] + [_vp] * 7 +
+                         [_i32, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     # test hook (include/mhc_testing.h), not part of the stable API
     "mhc_testing_gemm_rms_stalled": ([_vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _sz, _i64,
                                       ctypes.c_uint64, _vp], _i32),
@@ -424,6 +441,128 @@ def mhc_gemm_rms_noalloc(X, phi_t, B, n, C, Y, r, stream=None):
     _check(_lib.mhc_gemm_rms_noalloc(_ptr(X, bf, "X"), _ptr(phi_t, bf, "phi_t"), B, n, C,
                                      _ptr(Y, f, "Y"), _ptr(r, f, "r"), _stream(stream)),
            "mhc_gemm_rms_noalloc")
+
+
+# ------------------------------------------------------------------ training
+
+
+def kept_blocks(C: int) -> int:
+    """Scales of a stream of C channels in the 8-bit form of X: one per 32 channels."""
+    return -(-C // 32)
+
+
+def alloc_kept(B: int, n: int, C: int, device=None) -> tuple:
+    """Buffers (Xq, Xs) for X [B, n, C] in 8 bits."""
+    dev = device or "cuda"
+    return (torch.empty(B, n, C, dtype=torch.uint8, device=dev),
+            torch.empty(B, n, kept_blocks(C), dtype=torch.uint8, device=dev))
+
+
+def mhc_embed(table, ids, scale, V, B, n, C, X, stream=None):
+    """X[b, i] = scale * table[ids[b]] for every stream i; table bf16 [V, C], ids int64 [B]."""
+    _check(_lib.mhc_embed(_ptr(table, torch.bfloat16, "table"), _ptr(ids, torch.int64, "ids"),
+                          scale, V, B, n, C, _ptr(X, torch.bfloat16, "X"), _stream(stream)),
+           "mhc_embed")
+
+
+def mhc_embed_f32(table, ids, scale, V, B, n, C, X, stream=None):
+    """mhc_embed from an fp32 table."""
+    _check(_lib.mhc_embed_f32(_ptr(table, torch.float32, "table"), _ptr(ids, torch.int64, "ids"),
+                              scale, V, B, n, C, _ptr(X, torch.bfloat16, "X"), _stream(stream)),
+           "mhc_embed_f32")
+
+
+def embed_backward_workspace(V: int, B: int, n: int, C: int, device=None) -> torch.Tensor:
+    """Workspace of ``mhc_embed_backward`` for (V, B, n, C)."""
+    nbytes = int(_lib.mhc_embed_backward_workspace_bytes(V, B, n, C))
+    return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device or "cuda")
+
+
+def mhc_embed_backward(dX, ids, scale, accumulate, V, B, n, C, dtable, ws, stream=None):
+    """dtable[v] (+)= scale * sum of dX over the positions of id v and the streams, fp32 [V, C]."""
+    p, nb = _ws(ws)
+    _check(_lib.mhc_embed_backward(_ptr(dX, torch.bfloat16, "dX"), _ptr(ids, torch.int64, "ids"),
+                                   scale, int(accumulate), V, B, n, C,
+                                   _ptr(dtable, torch.float32, "dtable"), p, nb, _stream(stream)),
+           "mhc_embed_backward")
+
+
+def mhc_ckpt_pack(X, B, n, C, Xq, Xs, stream=None):
+    """X (bf16) to codes Xq and scales Xs (uint8; ``alloc_kept``)."""
+    _check(_lib.mhc_ckpt_pack(_ptr(X, torch.bfloat16, "X"), B, n, C, _ptr8(Xq, "Xq"),
+                              _ptr(Xs, torch.uint8, "Xs"), _stream(stream)), "mhc_ckpt_pack")
+
+
+def mhc_ckpt_unpack(Xq, Xs, B, n, C, X, stream=None):
+    """The values that (Xq, Xs) stand for, exact in bf16."""
+    _check(_lib.mhc_ckpt_unpack(_ptr8(Xq, "Xq"), _ptr(Xs, torch.uint8, "Xs"), B, n, C,
+                                _ptr(X, torch.bfloat16, "X"), _stream(stream)), "mhc_ckpt_unpack")
+
+
+def _post_ckpt(name, ft, X, F_out, H_res, H_post, B, n, C, X_next, Xq, Xs, stream):
+    bf, f = torch.bfloat16, torch.float32
+    _check(getattr(_lib, name)(_ptr(X, bf, "X"), _ptr(F_out, ft, "F_out"),
+                               _ptr(H_res, f, "H_res"), _ptr(H_post, f, "H_post"), B, n, C,
+                               _ptr(X_next, bf, "X_next"), _ptr8(Xq, "Xq"),
+                               _ptr(Xs, torch.uint8, "Xs"), _stream(stream)), name)
+
+
+def mhc_post_res_apply_ckpt(X, F_out, H_res, H_post, B, n, C, X_next, Xq, Xs, stream=None):
+    """mhc_post_res_apply that also keeps X in 8 bits; X_next may be X."""
+    _post_ckpt("mhc_post_res_apply_ckpt", torch.bfloat16, X, F_out, H_res, H_post, B, n, C, X_next,
+               Xq, Xs, stream)
+
+
+def mhc_post_res_apply_ckpt_f32(X, F_out, H_res, H_post, B, n, C, X_next, Xq, Xs, stream=None):
+    """mhc_post_res_apply_f32 that also keeps X in 8 bits; X_next may be X."""
+    _post_ckpt("mhc_post_res_apply_ckpt_f32", torch.float32, X, F_out, H_res, H_post, B, n, C,
+               X_next, Xq, Xs, stream)
+
+
+def _post_backward(name, ft, dX_next, Xq, Xs, F_out, H_post, B, n, C, dF_out, dH_res, dH_post,
+                   stream):
+    f = torch.float32
+    _check(getattr(_lib, name)(_ptr(dX_next, torch.bfloat16, "dX_next"), _ptr8(Xq, "Xq"),
+                               _ptr(Xs, torch.uint8, "Xs"), _ptr(F_out, ft, "F_out"),
+                               _ptr(H_post, f, "H_post"), B, n, C, _ptr(dF_out, ft, "dF_out"),
+                               _ptr(dH_res, f, "dH_res"), _ptr(dH_post, f, "dH_post"),
+                               _stream(stream)), name)
+
+
+def mhc_post_res_apply_backward(dX_next, Xq, Xs, F_out, H_post, B, n, C, dF_out, dH_res, dH_post,
+                                stream=None):
+    """dF_out, dH_res and dH_post of X_next = H_res·X + H_post ⊗ F_out."""
+    _post_backward("mhc_post_res_apply_backward", torch.bfloat16, dX_next, Xq, Xs, F_out, H_post,
+                   B, n, C, dF_out, dH_res, dH_post, stream)
+
+
+def mhc_post_res_apply_backward_f32(dX_next, Xq, Xs, F_out, H_post, B, n, C, dF_out, dH_res,
+                                    dH_post, stream=None):
+    """The same with F_out and dF_out in fp32."""
+    _post_backward("mhc_post_res_apply_backward_f32", torch.float32, dX_next, Xq, Xs, F_out,
+                   H_post, B, n, C, dF_out, dH_res, dH_post, stream)
+
+
+def pre_backward_workspace(B: int, n: int, C: int, iters: int, device=None) -> torch.Tensor:
+    """Workspace of ``mhc_pre_backward`` for (B, n, C, iters)."""
+    nbytes = int(_lib.mhc_pre_backward_workspace_bytes(B, n, C, iters))
+    return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device or "cuda")
+
+
+def mhc_pre_backward(dX_next, dF_pre, Xq, Xs, phi_t, alpha_pre, alpha_post, alpha_res, bias, iters,
+                     Y, r, H_pre, H_post, H_res, dH_res, dH_post, accumulate, B, n, C, dX, dphi_t,
+                     dbias, dalpha, ws, stream=None):
+    """dX (may be dX_next), dphi_t, dbias and dalpha [3] of steps 1-4a and of the residual path."""
+    bf, f = torch.bfloat16, torch.float32
+    p, nb = _ws(ws)
+    _check(_lib.mhc_pre_backward(
+        _ptr(dX_next, bf, "dX_next"), _ptr(dF_pre, bf, "dF_pre"), _ptr8(Xq, "Xq"),
+        _ptr(Xs, torch.uint8, "Xs"), _ptr(phi_t, bf, "phi_t"), alpha_pre, alpha_post, alpha_res,
+        _ptr(bias, f, "bias"), iters, _ptr(Y, f, "Y"), _ptr(r, f, "r"), _ptr(H_pre, f, "H_pre"),
+        _ptr(H_post, f, "H_post"), _ptr(H_res, f, "H_res"), _ptr(dH_res, f, "dH_res"),
+        _ptr(dH_post, f, "dH_post"), int(accumulate), B, n, C, _ptr(dX, bf, "dX"),
+        _ptr(dphi_t, f, "dphi_t"), _ptr(dbias, f, "dbias"), _ptr(dalpha, f, "dalpha"), p, nb,
+        _stream(stream)), "mhc_pre_backward")
 
 
 def mhc_device_status() -> int:

@@ -1,6 +1,6 @@
 """In-tree build of ``libmhc_gb300.so`` for sm_103a (GB300).
 
-Each ``csrc/*.cu`` file is compiled by its own ``nvcc`` process (in parallel)
+Each ``.cu`` file under ``csrc/`` is compiled by its own ``nvcc`` process (in parallel)
 with ``-gencode arch=compute_103a,code=sm_103a``, then the objects are linked
 into one shared library next to this file.  Only sources newer than their
 object are recompiled.  Run ``python gemm_rms_sinkhorn_gb300/build.py``
@@ -38,7 +38,8 @@ def _nvcc() -> str:
 
 
 def _headers():
-    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True) + \
+        glob.glob(os.path.join(CSRC, "**", "*.h"), recursive=True) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
@@ -60,7 +61,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     nvcc = _nvcc()
     build_dir, lib = (BUILD_CHECK, LIB_CHECK) if check else (BUILD, LIB)
     os.makedirs(build_dir, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    srcs = sorted(glob.glob(os.path.join(CSRC, "**", "*.cu"), recursive=True))
     newest_hdr = max((os.path.getmtime(h) for h in _headers()), default=0.0)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     if check:

@@ -9,9 +9,11 @@
 #include <mutex>
 
 #include "check.cuh"
+#include "host/args.h"
 #include "mhc.h"
 #include "mhc_internal.h"
 #include "mhc_testing.h"
+#include "train/train.h"
 
 namespace mhc {
 
@@ -92,119 +94,6 @@ cudaError_t current_device_info(DeviceInfo *info)
 }
 
 namespace {
-
-struct Buf {
-    const void *p;
-    size_t bytes;
-};
-
-bool overlaps(const Buf &a, const Buf &b)
-{
-    if (a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Shape rules shared by every call.  Returns MHC_OK or the error.
-int check_shape(int64_t B, int n, int64_t C, bool needs_c)
-{
-    if (B < 0) return MHC_ERR_INVALID;
-    if (n < 1 || n > 8) return MHC_ERR_UNSUPPORTED;
-    if (needs_c) {
-        if (C < 8 || C % 8 != 0) return MHC_ERR_UNSUPPORTED;
-        // K = n*C is addressed with 32-bit TMA coordinates and int kernel arguments
-        if (static_cast<int64_t>(n) * C > (int64_t{1} << 30)) return MHC_ERR_UNSUPPORTED;
-    }
-    // token rows are TMA coordinates, 32-bit signed
-    if (B >= (int64_t{1} << 31)) return MHC_ERR_UNSUPPORTED;
-    return MHC_OK;
-}
-
-int check_ptrs(const Buf *bufs, int count)
-{
-    for (int i = 0; i < count; ++i)
-        if (bufs[i].p == nullptr) return MHC_ERR_INVALID;
-    for (int i = 0; i < count; ++i)
-        if (!aligned16(bufs[i].p)) return MHC_ERR_ALIGN;
-    return MHC_OK;
-}
-
-// Outputs must not overlap inputs or each other.  `alias_ok` names one
-// (output, input) pair that may be exactly equal.
-int check_overlap(const Buf *outs, int n_out, const Buf *ins, int n_in, const void *alias_out,
-                  const void *alias_in)
-{
-    for (int i = 0; i < n_out; ++i) {
-        for (int j = 0; j < n_in; ++j) {
-            if (outs[i].p == alias_out && ins[j].p == alias_in && alias_out == alias_in &&
-                outs[i].bytes == ins[j].bytes)
-                continue;
-            if (overlaps(outs[i], ins[j])) return MHC_ERR_INVALID;
-        }
-        for (int j = i + 1; j < n_out; ++j)
-            if (overlaps(outs[i], outs[j])) return MHC_ERR_INVALID;
-    }
-    return MHC_OK;
-}
-
-// Whether the pointer checks of the device-memory entry points run (on unless a
-// test turns them off to time their cost).
-std::atomic<int> g_memory_checks{1};
-
-// Every buffer must be device memory of the current device (cudaMalloc,
-// stream-ordered pools or mapped VMM ranges): a host pointer, managed memory
-// or another GPU's memory reached over peer access is MHC_ERR_INVALID, before
-// anything is launched.  The kernels' TMA descriptors and stores assume local
-// device memory.
-int check_on_device(const Buf *bufs, int count, const DeviceInfo &info)
-{
-    if (!g_memory_checks.load(std::memory_order_relaxed)) return MHC_OK;
-    for (int i = 0; i < count; ++i) {
-        cudaPointerAttributes a{};
-        if (cudaPointerGetAttributes(&a, bufs[i].p) != cudaSuccess) {
-            cudaGetLastError();  // not sticky; clear it
-            return MHC_ERR_INVALID;
-        }
-        if (a.type != cudaMemoryTypeDevice || a.device != info.device) return MHC_ERR_INVALID;
-    }
-    return MHC_OK;
-}
-
-// Every buffer must be host memory (page-locked or pageable), as the runtime
-// records it: device or managed memory is MHC_ERR_INVALID.
-int check_on_host(const Buf *bufs, int count)
-{
-    for (int i = 0; i < count; ++i) {
-        cudaPointerAttributes a{};
-        if (cudaPointerGetAttributes(&a, bufs[i].p) != cudaSuccess) {
-            cudaGetLastError();  // not sticky; clear it
-            return MHC_ERR_INVALID;
-        }
-        if (a.type != cudaMemoryTypeHost && a.type != cudaMemoryTypeUnregistered)
-            return MHC_ERR_INVALID;
-    }
-    return MHC_OK;
-}
-
-int check_device(DeviceInfo *info)
-{
-    if (current_device_info(info) != cudaSuccess) return MHC_ERR_CUDA;
-    if (info->cc_major != 10 || info->cc_minor != 3) return MHC_ERR_UNSUPPORTED;
-    return MHC_OK;
-}
-
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? MHC_OK : MHC_ERR_CUDA; }
-
-size_t bf16_bytes(int64_t count) { return static_cast<size_t>(count) * 2; }
-size_t f32_bytes(int64_t count) { return static_cast<size_t>(count) * 4; }
-
-#define MHC_TRY(expr)                   \
-    do {                                \
-        const int st_ = (expr);         \
-        if (st_ != MHC_OK) return st_;  \
-    } while (0)
 
 // Batches up to this size take the one-launch steps 1-4a kernel.  Measured on
 // GB300 against the kernel chain (µs per forward in a CUDA graph): 1.6-2.7x
@@ -952,11 +841,12 @@ int mhc_testing_check_selftest(void)
 int mhc_device_status(int *status)
 {
     if (status == nullptr) return MHC_ERR_INVALID;
-    int st[5] = {0, 0, 0, 0, 0};
+    int st[6] = {0, 0, 0, 0, 0, 0};
     if (read_and_clear_device_status(&st[0]) != cudaSuccess) return MHC_ERR_CUDA;
     if (read_and_clear_fused_status(&st[1]) != cudaSuccess) return MHC_ERR_CUDA;
     if (read_and_clear_decode_status(&st[2]) != cudaSuccess) return MHC_ERR_CUDA;
     if (read_and_clear_rmsnorm_gemm_status(&st[3]) != cudaSuccess) return MHC_ERR_CUDA;
+    if (read_and_clear_phi_grad_status(&st[5]) != cudaSuccess) return MHC_ERR_CUDA;
     if (kCheckBuild) {
         // the records stay readable through mhc_testing_check_record
         std::lock_guard<std::mutex> lock(g_check_status_mu);

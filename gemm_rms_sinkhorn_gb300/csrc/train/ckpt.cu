@@ -1,0 +1,178 @@
+// Keeping the n residual streams in 8 bits for the backward pass (the form is
+// kept.cuh's), alone and together with the update that consumes them:
+//
+//   X_next[b][i][c] = Σ_j H_res[b][i][j]·X[b][j][c] + H_post[b][i]·F_out[b][c]
+//   (codes, scales) = X as kept
+//
+// The update has X in registers anyway, so keeping it there costs the bytes of
+// the codes and no second read of X; and X_next may then overwrite X.
+//
+// A thread owns 8 channels of one token in all n streams (128-bit accesses),
+// so four neighbouring lanes hold a block of 32 channels and find its largest
+// magnitude with two shuffles.  All kernels are bound by memory.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "check.cuh"
+#include "kept.cuh"
+#include "mix.cuh"
+#include "ptx.cuh"
+#include "train.h"
+
+namespace mhc {
+namespace {
+
+constexpr int kMaxGridY = 65535;
+
+// The largest magnitude over the four lanes of a block.
+__device__ __forceinline__ uint32_t block_amax(uint32_t a)
+{
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+}
+
+// Codes and scale of 8 channels (chunk c8) of one stream row.  Every lane of
+// the warp calls it; a lane without channels passes zeros and live = false.
+__device__ __forceinline__ void keep8(const uint4 &x, bool live, int64_t row, int64_t c8,
+                                      int64_t C, int64_t nb, uint8_t *Xq, uint8_t *Xs)
+{
+    const uint32_t E = kept::scale_code(block_amax(kept::amax8(x)));
+    if (!live) return;
+    kept::st_stream_v2(Xq + row * C + c8 * 8, kept::encode8(x, E));
+    if ((c8 & 3) == 0) Xs[row * nb + (c8 >> 2)] = static_cast<uint8_t>(E);
+}
+
+template <int n, typename FT>
+__global__ void __launch_bounds__(256, n <= 4 ? 4 : 2)
+post_res_ckpt_kernel(const uint16_t *X, const FT *__restrict__ F_out,
+                     const float *__restrict__ H_res, const float *__restrict__ H_post, int64_t B,
+                     int64_t C, uint16_t *X_next, uint8_t *__restrict__ Xq,
+                     uint8_t *__restrict__ Xs)
+{
+    __shared__ float hs[n * n + n];
+    const int64_t C8 = C >> 3, nb = kept_blocks(C);
+    const int64_t c8 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    for (int64_t b = blockIdx.y; b < B; b += gridDim.y) {
+        const bool tok_ok = in_range(1001, b, 1, B);
+        const bool ok = c8 < C8 && tok_ok && in_range(1002, c8 * 8, 8, C);
+        uint4 xv[n];
+        float f[8];
+        if (ok) {
+#pragma unroll
+            for (int j = 0; j < n; ++j) xv[j] = ptx::ld_stream_v4(X + (b * n + j) * C + c8 * 8);
+            kept::load_f8(F_out + b * C + c8 * 8, f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < n; ++j) xv[j] = make_uint4(0, 0, 0, 0);
+        }
+        __syncthreads();  // the previous token's coefficients are no longer read
+        for (int t = threadIdx.x; t < n * n + n; t += blockDim.x)
+            if (tok_ok)
+                hs[t] = t < n * n ? __ldg(H_res + b * n * n + t) : __ldg(H_post + b * n + (t - n * n));
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < n; ++j) keep8(xv[j], ok, b * n + j, c8, C, nb, Xq, Xs);
+        if (ok) {
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                ptx::st_stream_v4(X_next + (b * n + i) * C + c8 * 8, post_mix8<n>(hs, i, xv, f));
+        }
+    }
+}
+
+// Packing alone: the rows of all tokens and streams are alike.
+__global__ void __launch_bounds__(256)
+ckpt_pack_kernel(const uint16_t *__restrict__ X, int64_t rows, int64_t C,
+                 uint8_t *__restrict__ Xq, uint8_t *__restrict__ Xs)
+{
+    const int64_t C8 = C >> 3, nb = kept_blocks(C);
+    const int64_t c8 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        const bool ok = c8 < C8 && in_range(1011, row, 1, rows);
+        const uint4 x = ok ? ptx::ld_stream_v4(X + row * C + c8 * 8) : make_uint4(0, 0, 0, 0);
+        keep8(x, ok, row, c8, C, nb, Xq, Xs);
+    }
+}
+
+__global__ void __launch_bounds__(256)
+ckpt_unpack_kernel(const uint8_t *__restrict__ Xq, const uint8_t *__restrict__ Xs, int64_t rows,
+                   int64_t C, uint16_t *__restrict__ X)
+{
+    const int64_t C8 = C >> 3, nb = kept_blocks(C);
+    const int64_t c8 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    if (c8 >= C8) return;
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        if (!in_range(1021, row, 1, rows)) continue;
+        const uint2 q = kept::ld_stream_v2(Xq + row * C + c8 * 8);
+        const float s = kept::scale_value(__ldg(Xs + row * nb + (c8 >> 2)));
+        ptx::st_stream_v4(X + row * C + c8 * 8, kept::decode8_bf16(q, s));
+    }
+}
+
+// Threads per block: a power of two that divides C/8 when one exists, otherwise 128.
+int block_threads(int64_t C8)
+{
+    for (int t : {256, 128, 64, 32})
+        if (C8 % t == 0) return t;
+    return 128;
+}
+
+dim3 row_grid(int64_t rows, int64_t C8, int threads)
+{
+    const int64_t gx = (C8 + threads - 1) / threads;
+    return dim3(static_cast<unsigned>(gx),
+                static_cast<unsigned>(rows < kMaxGridY ? rows : kMaxGridY), 1);
+}
+
+}  // namespace
+
+template <typename FT>
+cudaError_t launch_post_res_ckpt(const uint16_t *X, const FT *F_out, const float *H_res,
+                                 const float *H_post, int64_t B, int n, int64_t C,
+                                 uint16_t *X_next, uint8_t *Xq, uint8_t *Xs, cudaStream_t stream)
+{
+    const int threads = block_threads(C / 8);
+    const dim3 grid = row_grid(B, C / 8, threads);
+    switch (n) {
+#define MHC_CASE(k)                                                                            \
+    case k:                                                                                    \
+        return launch_pdl(post_res_ckpt_kernel<k, FT>, grid, dim3(threads), 0, stream, X,      \
+                          F_out, H_res, H_post, B, C, X_next, Xq, Xs);
+        MHC_CASE(1) MHC_CASE(2) MHC_CASE(3) MHC_CASE(4) MHC_CASE(5) MHC_CASE(6) MHC_CASE(7)
+        MHC_CASE(8)
+#undef MHC_CASE
+    default: return cudaErrorInvalidValue;
+    }
+}
+template cudaError_t launch_post_res_ckpt<uint16_t>(const uint16_t *, const uint16_t *,
+                                                    const float *, const float *, int64_t, int,
+                                                    int64_t, uint16_t *, uint8_t *, uint8_t *,
+                                                    cudaStream_t);
+template cudaError_t launch_post_res_ckpt<float>(const uint16_t *, const float *, const float *,
+                                                 const float *, int64_t, int, int64_t, uint16_t *,
+                                                 uint8_t *, uint8_t *, cudaStream_t);
+
+cudaError_t launch_ckpt_pack(const uint16_t *X, int64_t B, int n, int64_t C, uint8_t *Xq,
+                             uint8_t *Xs, cudaStream_t stream)
+{
+    const int threads = block_threads(C / 8);
+    return launch_pdl(ckpt_pack_kernel, row_grid(B * n, C / 8, threads), dim3(threads), 0, stream,
+                      X, B * n, C, Xq, Xs);
+}
+
+cudaError_t launch_ckpt_unpack(const uint8_t *Xq, const uint8_t *Xs, int64_t B, int n, int64_t C,
+                               uint16_t *X, cudaStream_t stream)
+{
+    const int threads = block_threads(C / 8);
+    return launch_pdl(ckpt_unpack_kernel, row_grid(B * n, C / 8, threads), dim3(threads), 0,
+                      stream, Xq, Xs, B * n, C, X);
+}
+
+}  // namespace mhc

@@ -1,0 +1,385 @@
+// Token ids to the n residual streams, and the table's gradient.
+//
+//   X[b][i][c]   = scale·T[ids[b]][c]                         for every stream i
+//   dT[v][c]     = scale·Σ_{b: ids[b] = v} Σ_i dX[b][i][c]    fp32
+//
+// An id outside [0, V) is padding: its row of X is zero and it adds to no row
+// of dT.
+//
+// The gradient is a sum by token id, and token counts are very uneven (a few
+// ids make up much of a batch, most of the table does not occur), so it runs
+// over the positions sorted by id, in three launches:
+//
+//   sort   CTA k owns a range of table rows.  It reads all ids, keeps those of
+//          its range in their order, and counts those below it, which is where
+//          its part of the sorted list starts: a stable counting sort with no
+//          exchange between CTAs.  (Reading B ids per CTA is L2 traffic, a few
+//          percent of the time of the rows of dX that follow.)  Rows of its range that do not
+//          occur it sets to zero, so the table is written once.
+//   sum    the sorted list is cut into chunks of kChunk positions, whatever the
+//          ids, so every CTA has the same work.  A run of one id that lies in a
+//          chunk is written; a run that a chunk's edge cuts leaves its sums in
+//          the workspace (one before the edge, one after).
+//   join   adds the pieces of the cut runs, in the order of the chunks.
+//
+// All sums are fp32 in the order of the positions, so results do not depend on
+// timing.  There are no atomics on sums.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "check.cuh"
+#include "kept.cuh"
+#include "mix.cuh"
+#include "ptx.cuh"
+#include "train.h"
+
+namespace mhc {
+namespace {
+
+constexpr int kMaxGridY = 65535;
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxRange = 512;  // table rows of a sorting CTA, at most
+constexpr int kChunk = 16;      // sorted positions of a summing CTA
+
+__device__ __forceinline__ uint4 scaled8(const uint16_t *p, float scale)
+{
+    float f[8];
+    unpack8(__ldg(reinterpret_cast<const uint4 *>(p)), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= scale;
+    return pack8(f);
+}
+__device__ __forceinline__ uint4 scaled8(const float *p, float scale)
+{
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    const float f[8] = {a.x * scale, a.y * scale, a.z * scale, a.w * scale,
+                        b.x * scale, b.y * scale, b.z * scale, b.w * scale};
+    return pack8(f);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+embed_kernel(const T *__restrict__ table, const int64_t *__restrict__ ids, float scale, int64_t V,
+             int64_t B, int n, int64_t C, uint16_t *__restrict__ X)
+{
+    const int64_t C8 = C >> 3;
+    const int64_t c8 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    if (c8 >= C8) return;
+    for (int64_t b = blockIdx.y; b < B; b += gridDim.y) {
+        if (!in_range(1401, b, 1, B)) continue;
+        const int64_t id = __ldg(ids + b);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (id >= 0 && id < V) v = scaled8(table + id * C + c8 * 8, scale);
+        uint16_t *x = X + b * n * C + c8 * 8;
+        for (int i = 0; i < n; ++i) ptx::st_stream_v4(x + i * C, v);
+    }
+}
+
+// Workspace of the gradient: the number of positions that are not padding,
+// the sorted positions and their rows, and two rows of sums per chunk.
+struct GradWs {
+    int *count, *pos, *row;
+    float *part;  // [chunks][2][C]: the run cut by the chunk's start, then by its end
+};
+
+__host__ __device__ inline int64_t chunks_of(int64_t positions)
+{
+    return (positions + kChunk - 1) / kChunk;
+}
+
+size_t carve(GradWs &w, void *base, int64_t B, int64_t C)
+{
+    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    uint8_t *p = static_cast<uint8_t *>(base);
+    size_t at = 0;
+    w.count = reinterpret_cast<int *>(p + at);
+    at += 256;
+    w.pos = reinterpret_cast<int *>(p + at);
+    at += up(static_cast<size_t>(B) * 4);
+    w.row = reinterpret_cast<int *>(p + at);
+    at += up(static_cast<size_t>(B) * 4);
+    w.part = reinterpret_cast<float *>(p + at);
+    at += up(static_cast<size_t>(chunks_of(B)) * 2 * static_cast<size_t>(C) * 4);
+    return at;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 2)
+embed_sort_kernel(const int64_t *__restrict__ ids, int64_t V, int64_t B, int64_t C, int range,
+                  int accumulate, GradWs ws, float *__restrict__ dtable)
+{
+    __shared__ int hist[kSortWarps][kMaxRange];  // counts, then where each warp's next one goes
+    __shared__ int total[kMaxRange];
+    __shared__ int sums[kSortWarps], below_w[kSortWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x) * range;
+    const int64_t v1 = v0 + range < V ? v0 + range : V;
+    const int rows = static_cast<int>(v1 - v0);
+    for (int r = threadIdx.x; r < kSortWarps * kMaxRange; r += kSortThreads) (&hist[0][0])[r] = 0;
+    __syncthreads();
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+
+    // each warp counts a stretch of the positions
+    const int64_t per = ((B + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int64_t lo = per * warp < B ? per * warp : B;
+    const int64_t hi = lo + per < B ? lo + per : B;
+    int below = 0, mine = 0;
+#pragma unroll 4
+    for (int64_t b = lo + lane; b < hi; b += 32) {
+        const int64_t id = __ldg(ids + b);
+        below += id >= 0 && id < v0;
+        if (id >= v0 && id < v1) {
+            atomicAdd(&hist[warp][static_cast<int>(id - v0)], 1);
+            ++mine;
+        }
+    }
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    below = __reduce_add_sync(0xffffffffu, below);
+    if (lane == 0) below_w[warp] = below;
+    __syncthreads();
+
+    // where each (row, warp) starts: rows in order, the warps' stretches in order
+    const int r = threadIdx.x;  // kMaxRange == kSortThreads: a thread per row
+    int cnt = 0;
+    if (r < rows)
+        for (int w = 0; w < kSortWarps; ++w) cnt += hist[w][r];
+    total[r] = cnt;
+    int incl = cnt;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += up;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int base = 0, all = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+        base += below_w[w] + (w < warp ? sums[w] : 0);
+        all += below_w[w] + sums[w];
+    }
+    if (r < rows) {
+        int at = base + incl - cnt;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = hist[w][r];
+            hist[w][r] = at;
+            at += c;
+        }
+    }
+    if (v1 == V && threadIdx.x == 0) *ws.count = all;
+    __syncthreads();
+
+    if (mine > 0) {
+        for (int64_t b0 = lo; b0 < hi; b0 += 32) {
+            const int64_t b = b0 + lane;
+            const int64_t id = b < hi ? __ldg(ids + b) : -1;
+            const bool in = id >= v0 && id < v1;
+            if (__ballot_sync(0xffffffffu, in) == 0) continue;
+            const int key = in ? static_cast<int>(id - v0) : -1;
+            const unsigned same = __match_any_sync(0xffffffffu, key);
+            const int rank = __popc(same & ((1u << lane) - 1u));
+            const int at = in ? hist[warp][key] + rank : 0;
+            __syncwarp();
+            if (in && rank == 0) hist[warp][key] += __popc(same);
+            __syncwarp();
+            if (in && in_range(1411, at, 1, B)) {
+                ws.pos[at] = static_cast<int>(b);
+                ws.row[at] = static_cast<int>(id);
+            }
+        }
+    }
+    if (!accumulate) {
+        const int64_t c4 = C >> 2;
+        for (int k = warp; k < rows; k += kSortWarps) {
+            if (total[k] != 0 || !in_range(1412, v0 + k, 1, V)) continue;
+            float *dst = dtable + (v0 + k) * C;
+            for (int64_t e = lane; e < c4; e += 32)
+                ptx::st_stream_v4(dst + e * 4, make_uint4(0, 0, 0, 0));
+        }
+    }
+}
+
+__device__ __forceinline__ void put8(float *dst, const float (&v)[8], float scale, int accumulate)
+{
+    float4 *d = reinterpret_cast<float4 *>(dst);
+    float4 a = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+    float4 b = make_float4(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale);
+    if (accumulate) {
+        const float4 x = d[0], y = d[1];
+        a = make_float4(x.x + a.x, x.y + a.y, x.z + a.z, x.w + a.w);
+        b = make_float4(y.x + b.x, y.y + b.y, y.z + b.z, y.w + b.w);
+    }
+    __stcs(d, a);
+    __stcs(d + 1, b);
+}
+
+template <int n>
+__global__ void __launch_bounds__(256)
+embed_sum_kernel(const uint16_t *__restrict__ dX, float scale, int accumulate, int64_t V,
+                 int64_t B, int64_t C, GradWs ws, float *__restrict__ dtable)
+{
+    __shared__ int pos[kChunk], row[kChunk + 2];  // row: one before and one after too
+    const int64_t C8 = C >> 3;
+    const int64_t c8 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    const int count = *ws.count;
+    for (int64_t k = blockIdx.y; k * kChunk < count; k += gridDim.y) {
+        const int first = static_cast<int>(k * kChunk);
+        const int len = count - first < kChunk ? count - first : kChunk;
+        __syncthreads();
+        if (threadIdx.x < kChunk + 2) {
+            const int p = first + static_cast<int>(threadIdx.x) - 1;
+            row[threadIdx.x] = p >= 0 && p < count ? ws.row[p] : -1;
+            if (threadIdx.x < len) pos[threadIdx.x] = ws.pos[first + threadIdx.x];
+        }
+        __syncthreads();
+        if (c8 >= C8) continue;
+        float acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        uint4 x[n];
+        const auto load = [&](int p) {
+            if (!in_range(1421, pos[p], 1, B)) return;
+            const uint16_t *src = dX + static_cast<int64_t>(pos[p]) * n * C + c8 * 8;
+#pragma unroll
+            for (int i = 0; i < n; ++i) x[i] = ptx::ld_stream_v4(src + i * C);
+        };
+        load(0);
+        bool begins = row[0] != row[1];  // the current run starts in this chunk
+        for (int p = 0; p < len; ++p) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                float f[8];
+                unpack8(x[i], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] += f[e];
+            }
+            if (p + 1 < len) load(p + 1);
+            const int v = row[p + 1];
+            const bool ends = row[p + 2] != v;
+            if (!ends && p + 1 < len) continue;
+            if (begins && ends) {
+                if (in_range(1422, v, 1, V))
+                    put8(dtable + static_cast<int64_t>(v) * C + c8 * 8, acc, scale, accumulate);
+            } else if (in_range(1423, 2 * k + 1, 1, 2 * chunks_of(B))) {
+                put8(ws.part + (2 * k + (begins ? 1 : 0)) * C + c8 * 8, acc, 1.f, 0);
+            }
+            begins = true;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256)
+embed_join_kernel(float scale, int accumulate, int64_t V, int64_t B, int64_t C, GradWs ws,
+                  float *__restrict__ dtable)
+{
+    const int64_t C8 = C >> 3;
+    const int64_t c8 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    const int count = *ws.count;
+    for (int64_t k = blockIdx.y; (k + 1) * kChunk < count; k += gridDim.y) {
+        // the run that chunk k's end cuts, if it starts in chunk k
+        const int first = static_cast<int>(k * kChunk), next = first + kChunk;
+        const int v = ws.row[next - 1];
+        if (ws.row[next] != v) continue;
+        if (ws.row[first] == v && first > 0 && ws.row[first - 1] == v) continue;
+        int lo = next, hi = count;  // the first position after the run
+        while (lo < hi) {
+            const int mid = lo + (hi - lo) / 2;
+            if (ws.row[mid] <= v) lo = mid + 1; else hi = mid;
+        }
+        const int64_t last = (lo - 1) / kChunk;
+        if (c8 >= C8 || !in_range(1431, v, 1, V) || !in_range(1432, last, 1, chunks_of(B))) continue;
+        float acc[8];
+        const float4 *src = reinterpret_cast<const float4 *>(ws.part + (2 * k + 1) * C + c8 * 8);
+        float4 a = __ldcs(src), b = __ldcs(src + 1);
+        acc[0] = a.x; acc[1] = a.y; acc[2] = a.z; acc[3] = a.w;
+        acc[4] = b.x; acc[5] = b.y; acc[6] = b.z; acc[7] = b.w;
+#pragma unroll 8
+        for (int64_t kk = k + 1; kk <= last; ++kk) {
+            src = reinterpret_cast<const float4 *>(ws.part + 2 * kk * C + c8 * 8);
+            a = __ldcs(src);
+            b = __ldcs(src + 1);
+            acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
+            acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
+        }
+        put8(dtable + static_cast<int64_t>(v) * C + c8 * 8, acc, scale, accumulate);
+    }
+}
+
+int block_threads(int64_t C8)
+{
+    for (int t : {256, 128, 64, 32})
+        if (C8 % t == 0) return t;
+    return 128;
+}
+
+dim3 col_grid(int64_t rows, int64_t C8, int threads)
+{
+    return dim3(static_cast<unsigned>((C8 + threads - 1) / threads),
+                static_cast<unsigned>(rows < kMaxGridY ? rows : kMaxGridY), 1);
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_embed(const T *table, const int64_t *ids, float scale, int64_t V, int64_t B,
+                         int n, int64_t C, uint16_t *X, cudaStream_t stream)
+{
+    const int threads = block_threads(C / 8);
+    return launch_pdl(embed_kernel<T>, col_grid(B, C / 8, threads), dim3(threads), 0, stream,
+                      table, ids, scale, V, B, n, C, X);
+}
+template cudaError_t launch_embed<uint16_t>(const uint16_t *, const int64_t *, float, int64_t,
+                                            int64_t, int, int64_t, uint16_t *, cudaStream_t);
+template cudaError_t launch_embed<float>(const float *, const int64_t *, float, int64_t, int64_t,
+                                         int, int64_t, uint16_t *, cudaStream_t);
+
+size_t embed_backward_workspace_bytes(int64_t, int64_t B, int, int64_t C)
+{
+    GradWs w;
+    return carve(w, nullptr, B, C);
+}
+
+cudaError_t launch_embed_backward(const uint16_t *dX, const int64_t *ids, float scale,
+                                  int accumulate, int64_t V, int64_t B, int n, int64_t C,
+                                  float *dtable, void *workspace, int num_sms,
+                                  cudaStream_t stream)
+{
+    static_assert(kMaxRange == kSortThreads, "a thread per row of the range");
+    GradWs ws;
+    carve(ws, workspace, B, C);
+    int64_t range = (V + 2 * num_sms - 1) / (2 * num_sms);  // two CTAs an SM, in one wave
+    if (range > kMaxRange) range = kMaxRange;
+    cudaError_t e = launch_pdl(embed_sort_kernel,
+                               dim3(static_cast<unsigned>((V + range - 1) / range)),
+                               dim3(kSortThreads), 0, stream, ids, V, B, C,
+                               static_cast<int>(range), accumulate, ws, dtable);
+    if (e != cudaSuccess) return e;
+    const int threads = block_threads(C / 8);
+    const dim3 grid = col_grid(chunks_of(B), C / 8, threads);
+    switch (n) {
+#define MHC_CASE(k)                                                                           \
+    case k:                                                                                   \
+        e = launch_pdl(embed_sum_kernel<k>, grid, dim3(threads), 0, stream, dX, scale,        \
+                       accumulate, V, B, C, ws, dtable);                                      \
+        break;
+        MHC_CASE(1) MHC_CASE(2) MHC_CASE(3) MHC_CASE(4) MHC_CASE(5) MHC_CASE(6) MHC_CASE(7)
+        MHC_CASE(8)
+#undef MHC_CASE
+    default: return cudaErrorInvalidValue;
+    }
+    if (e != cudaSuccess || B <= kChunk) return e;  // one chunk cuts no run
+    return launch_pdl(embed_join_kernel, grid, dim3(threads), 0, stream, scale, accumulate, V, B,
+                      C, ws, dtable);
+}
+
+}  // namespace mhc

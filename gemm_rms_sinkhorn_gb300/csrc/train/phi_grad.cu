@@ -1,0 +1,382 @@
+// dφ_t[k][q] = Σ_b dY[b][k]·X[b][q] on the tensor cores, X read as it was kept
+// (kept.cuh) and dY given as three bf16 terms (train.h): the products of bf16
+// values are exact, so with fp32 accumulation dφ has fp32's accuracy, which
+// one bf16 rounding of dY (2^-9) would not have.
+//
+// A tall, skinny product: K = nC rows (the channels), 3N columns, summed over
+// the tokens.  Bound by the bytes of the codes while N is small; at n = 8 (240
+// columns) by the tensor cores.  A CTA takes strips of 256 channels and blocks
+// of 64 tokens, the (strip, block) units dealt out in equal contiguous ranges,
+// one CTA per SM:
+//
+//   warps 0-7  load codes and scales two units ahead into registers, write the
+//              bf16 values to the stage's A tile and hand it over; after a
+//              strip's last unit they read the accumulators (tcgen05.ld), add
+//              the three terms and store the sums to the workspace;
+//   warp 8     TMA: the dY terms of the block (B tile);
+//   warp 9     tcgen05.mma, M = 128 channels (two accumulators), N = 3n² + 6n
+//              columns padded to 48, K = 16 tokens.
+//
+// Channels are contiguous in the codes, so A is written MN-major: a unit's tile
+// is [4 × 64 channels][8 × 8 tokens], each 64 × 8 part 1 KB with the 128-byte
+// swizzle.  A second launch adds the strips' parts in the order of the tokens.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "check.cuh"
+#include "kept.cuh"
+#include "mhc_internal.h"
+#include "ptx.cuh"
+#include "train.h"
+
+namespace mhc {
+namespace {
+
+constexpr int kStrip = 256;
+constexpr int kTok = kPhiTokens;
+constexpr int kLoadWarps = 8;
+constexpr int kThreads = (kLoadWarps + 2) * 32;
+constexpr int kABytes = kStrip * kTok * 2;  // 32 KB
+constexpr int kStatusTimeout = -5;          // MHC_ERR_TIMEOUT
+
+__device__ int g_phi_status;
+
+template <int n>
+struct Cfg {
+    static constexpr int N = n * n + 2 * n;
+    static constexpr int NT = (kPhiTerms * N + 47) / 48 * 48;  // columns: three terms × 16 k at a time
+    static constexpr int kBBytes = NT * kTok * 2;
+    static constexpr int kStage = kABytes + kBBytes;
+    static constexpr int kStages = n <= 4 ? 4 : 3;
+    static constexpr int kSmem = 1024 + kStages * kStage + 256;
+    static constexpr int kTmemCols = 2 * NT <= 128 ? 128 : 2 * NT <= 256 ? 256 : 512;
+    static_assert(NT <= 256 && NT % 16 == 0, "MMA N for M = 128");
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+// The units (strip, token block), strip-major, in `grid` equal ranges.
+struct Units {
+    int64_t total, blocks;  // units; token blocks of a strip
+    int grid;
+    __host__ __device__ int64_t lo(int c) const { return total * c / grid; }
+    __host__ __device__ int owner(int64_t u) const
+    {
+        return static_cast<int>(((u + 1) * grid - 1) / total);
+    }
+};
+
+// MN-major operand with the 128-byte swizzle: 64 elements × 8 per 1 KB part;
+// parts along M/N `lead` bytes apart, along K `stride` bytes.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead, uint32_t stride)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(lead >> 4) << 16;
+    d |= static_cast<uint64_t>(stride >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+struct Tile {  // a thread's codes of one unit: 8 channels of 8 tokens
+    uint2 q[8];
+    uint32_t E[8];
+};
+
+template <int n>
+__global__ void __launch_bounds__(kThreads, 1)
+phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restrict__ Xq,
+                const uint8_t *__restrict__ Xs, int64_t B, int64_t C, Units un,
+                float *__restrict__ part, uint64_t limit_ns)
+{
+    using Cf = Cfg<n>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cf::kStages * Cf::kStage);
+    uint64_t *empty = full + Cf::kStages;
+    uint64_t *acc_full = empty + Cf::kStages, *acc_empty = acc_full + 1, *drain = acc_empty + 1;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+    const int64_t K = n * C, nb = kept_blocks(C);
+    const int64_t u0 = un.lo(cta), u1 = un.lo(cta + 1);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cf::kStages; ++s) {
+            ptx::mbar_init(&full[s], kLoadWarps + 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        ptx::mbar_init(acc_full, 1);
+        ptx::mbar_init(acc_empty, kLoadWarps);
+        ptx::mbar_init(drain, 1);
+        *abort = 0;
+        ptx::fence_barrier_init();
+        ptx::prefetch_tensormap(&tm_y);
+    }
+    if (warp == 9) ptx::tmem_alloc<Cf::kTmemCols>(tmem_holder);
+    ptx::tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    ptx::pdl_wait();
+
+    const auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ptx::mbar_wait_bounded(bar, parity, abort, limit_ns)) return true;
+        *abort = 1;
+        atomicExch(&g_phi_status, kStatusTimeout);
+        return false;
+    };
+
+    if (warp < kLoadWarps) {
+        // lane: 8 channels of the strip; warp: tokens warp, warp + 8, ... of the block
+        const auto load = [&](int64_t u, Tile &x) {
+            const int64_t strip = u / un.blocks, b0 = (u - strip * un.blocks) * kTok + warp;
+            const int64_t q = strip * kStrip + lane * 8;
+            const int64_t i = q / C, c = q - i * C;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t b = b0 + 8 * e;
+                if (u < u1 && q < K && b < B && in_range(1301, b * K + q, 8, B * K)) {
+                    x.q[e] = kept::ld_stream_v2(Xq + b * K + q);
+                    x.E[e] = __ldg(Xs + (b * n + i) * nb + (c >> 5));
+                } else {
+                    x.q[e] = make_uint2(0, 0);
+                    x.E[e] = kept::kScaleMin;
+                }
+            }
+        };
+        const uint32_t at = static_cast<uint32_t>((lane >> 3) * 8192 + warp * 128 +
+                                                  (((lane & 7) ^ warp) << 4));
+        int stage = 0, seg = 0;
+        uint32_t phase = 0;
+        // the tile of one unit into its stage, then the unit after next into x
+        const auto step = [&](int64_t u, Tile &x) {
+            if (!wait(&empty[stage], phase ^ 1)) return false;
+            uint8_t *dst = smem + stage * Cf::kStage + at;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4 *>(dst + e * 1024) =
+                    kept::decode8_bf16(x.q[e], kept::scale_value(x.E[e]));
+            load(u + 2, x);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&full[stage]);
+            if (++stage == Cf::kStages) { stage = 0; phase ^= 1; }
+            const int64_t strip = u / un.blocks;
+            if (u + 1 < u1 && (u + 1) / un.blocks == strip) return true;
+            // the strip's (part of the) sum is complete: channel h·128 + 32·quarter + lane
+            if (!wait(acc_full, seg & 1)) return false;
+            ptx::tc_fence_after();
+            const int h = warp >> 2, quarter = warp & 3;
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                   static_cast<uint32_t>(h * Cf::NT);
+            float *dst_p = part + (cta + strip) * static_cast<int64_t>(Cf::N) * kStrip + h * 128 +
+                           quarter * 32 + lane;
+            const bool ok = in_range(1302, cta + strip, 1, un.grid + un.total / un.blocks);
+#pragma unroll
+            for (int m = 0; m < Cf::NT / 48; ++m) {
+                float v[3][16];
+#pragma unroll
+                for (int w = 0; w < 3; ++w) ptx::tmem_ld_16(taddr + m * 48 + w * 16, v[w]);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (m * 16 + e < Cf::N && ok)
+                        dst_p[(m * 16 + e) * kStrip] =
+                            (v[(3 * e) / 16][(3 * e) % 16] + v[(3 * e + 1) / 16][(3 * e + 1) % 16]) +
+                            v[(3 * e + 2) / 16][(3 * e + 2) % 16];
+                __syncwarp();
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(acc_empty);
+            ++seg;
+            return true;
+        };
+        Tile x0, x1;
+        load(u0, x0);
+        load(u0 + 1, x1);
+        for (int64_t u = u0; u < u1; u += 2) {
+            if (!step(u, x0)) break;
+            if (u + 1 < u1 && !step(u + 1, x1)) break;
+        }
+    } else if (warp == kLoadWarps) {
+        if (lane == 0) {
+            const uint64_t pol = ptx::policy_evict_last();  // every strip reads them
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, parity = 0;
+            bool ok = true;
+            for (int64_t u = u0; u < u1 && ok; ++u) {
+                ok = wait(&empty[stage], phase ^ 1);
+                if (!ok) break;
+                ptx::mbar_arrive_expect_tx(&full[stage], Cf::kBBytes);
+                ptx::tma_load_2d(smem + stage * Cf::kStage + kABytes, &tm_y,
+                                 static_cast<int32_t>(u % un.blocks * kTok), 0, &full[stage], pol);
+                issued |= 1u << stage;
+                parity = (parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == Cf::kStages) { stage = 0; phase ^= 1; }
+            }
+            // after an abort a stage's other arrivals may be missing, so its
+            // barrier cannot tell that the copy has landed: wait by the clock, far
+            // longer than any copy takes
+            if (*abort) {
+                const uint64_t t0 = ptx::globaltimer_ns();
+                for (int polls = 0; polls < (1 << 20) && ptx::globaltimer_ns() - t0 < 1000000; ++polls)
+                    __nanosleep(200);
+            }
+        }
+    } else {
+        if (lane == 0) {
+            constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, Cf::NT) | (1u << 15);  // A MN-major
+            int stage = 0, seg = 0;
+            uint32_t phase = 0;
+            bool ok = true, first = true;
+            for (int64_t u = u0; u < u1; ++u) {
+                if (first && !(ok = wait(acc_empty, (seg & 1) ^ 1))) break;
+                if (!(ok = wait(&full[stage], phase))) break;
+                ptx::tc_fence_after();
+                const uint32_t a = ptx::smem_u32(smem + stage * Cf::kStage);
+                const uint64_t b_desc = ptx::smem_desc_sw128(a + kABytes);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int ks = 0; ks < kTok / 16; ++ks)
+                        ptx::mma_bf16(tmem + static_cast<uint32_t>(h * Cf::NT),
+                                      desc_mn_sw128(a + h * 16384 + ks * 2048, 8192, 1024),
+                                      b_desc + 2 * ks, idesc, first && ks == 0 ? 0u : 1u);
+                ptx::mma_commit(&empty[stage]);
+                if (++stage == Cf::kStages) { stage = 0; phase ^= 1; }
+                first = u + 1 < u1 && (u + 1) / un.blocks != u / un.blocks;
+                if (first || u + 1 == u1) {
+                    ptx::mma_commit(acc_full);
+                    ++seg;
+                }
+            }
+            if (!ok || *abort) {  // every MMA issued has to end before TMEM is freed
+                ptx::mma_commit(drain);
+                volatile int never = 0;
+                ptx::mbar_wait_bounded(drain, 0, &never, limit_ns);
+            }
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::pdl_trigger();
+    if (warp == 9) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc<Cf::kTmemCols>(tmem);
+    }
+}
+
+// Adds each strip's parts in the order of the CTAs, which is that of the tokens.
+__global__ void __launch_bounds__(64)
+phi_join_kernel(const float *__restrict__ part, int N, int64_t K, Units un, int accumulate,
+                float *__restrict__ dphi_t)
+{
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    const int64_t strip = blockIdx.x;
+    const int first = un.owner(strip * un.blocks), last = un.owner((strip + 1) * un.blocks - 1);
+    const int64_t q = strip * kStrip + threadIdx.x * 4;
+    if (q >= K) return;
+    for (int k = blockIdx.y; k < N; k += gridDim.y) {
+        if (!in_range(1311, k * K + q, 4, N * K) ||
+            !in_range(1312, first + strip, last - first + 1, un.grid + un.total / un.blocks))
+            continue;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int c = first; c <= last; ++c) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                part + ((c + strip) * N + k) * kStrip + threadIdx.x * 4));
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        float4 *dst = reinterpret_cast<float4 *>(dphi_t + k * K + q);
+        if (accumulate) {
+            const float4 o = *dst;
+            s = make_float4(o.x + s.x, o.y + s.y, o.z + s.z, o.w + s.w);
+        }
+        *dst = s;
+    }
+}
+
+Units make_units(int64_t B, int n, int64_t C, int num_sms)
+{
+    Units u;
+    u.blocks = (B + kTok - 1) / kTok;
+    const int64_t strips = (n * C + kStrip - 1) / kStrip;
+    u.total = strips * u.blocks;
+    u.grid = static_cast<int>(u.total < num_sms ? u.total : num_sms);
+    return u;
+}
+
+template <int n>
+cudaError_t launch_n(const CUtensorMap &tm, const uint8_t *Xq, const uint8_t *Xs, int64_t B,
+                     int64_t C, const Units &un, int accumulate, float *dphi_t, float *part,
+                     cudaStream_t stream)
+{
+    static std::atomic<bool> set{false};
+    if (!set.load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            phi_grad_kernel<n>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<n>::kSmem);
+        if (e != cudaSuccess) return e;
+        set.store(true, std::memory_order_release);
+    }
+    cudaError_t e = launch_pdl(phi_grad_kernel<n>, dim3(un.grid), dim3(kThreads), Cfg<n>::kSmem,
+                               stream, tm, Xq, Xs, B, C, un, part, kWaitLimitNs);
+    if (e != cudaSuccess) return e;
+    const int64_t K = n * C;
+    return launch_pdl(phi_join_kernel,
+                      dim3(static_cast<unsigned>((K + kStrip - 1) / kStrip), Cfg<n>::N), dim3(64),
+                      0, stream, part, Cfg<n>::N, K, un, accumulate, dphi_t);
+}
+
+}  // namespace
+
+size_t phi_grad_workspace_bytes(int64_t B, int n, int64_t C, int num_sms)
+{
+    const Units u = make_units(B, n, C, num_sms);
+    return static_cast<size_t>(u.grid + u.total / u.blocks) * num_coeffs(n) * kStrip * 4;
+}
+
+cudaError_t launch_phi_grad(const uint8_t *Xq, const uint8_t *Xs, const uint16_t *dY_terms,
+                            int64_t B, int n, int64_t C, int accumulate, float *dphi_t,
+                            void *workspace, int num_sms, cudaStream_t stream)
+{
+    const Units un = make_units(B, n, C, num_sms);
+    CUtensorMap tm;
+    const int N = num_coeffs(n);
+    const uint32_t box = static_cast<uint32_t>((kPhiTerms * N + 47) / 48 * 48);
+    if (!make_tmap(&tm, dY_terms, static_cast<uint64_t>(phi_grad_padded_tokens(B)),
+                   static_cast<uint64_t>(kPhiTerms * N), box))
+        return cudaErrorInvalidValue;
+    float *part = static_cast<float *>(workspace);
+    switch (n) {
+#define MHC_CASE(k) \
+    case k: return launch_n<k>(tm, Xq, Xs, B, C, un, accumulate, dphi_t, part, stream);
+        MHC_CASE(1) MHC_CASE(2) MHC_CASE(3) MHC_CASE(4) MHC_CASE(5) MHC_CASE(6) MHC_CASE(7)
+        MHC_CASE(8)
+#undef MHC_CASE
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t read_and_clear_phi_grad_status(int *status)
+{
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return e;
+    int v = 0, zero = 0;
+    if ((e = cudaMemcpyFromSymbol(&v, g_phi_status, sizeof v)) != cudaSuccess) return e;
+    if ((e = cudaMemcpyToSymbol(g_phi_status, &zero, sizeof zero)) != cudaSuccess) return e;
+    *status = v;
+    return cudaSuccess;
+}
+
+}  // namespace mhc

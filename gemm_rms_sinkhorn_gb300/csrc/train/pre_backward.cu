@@ -1,0 +1,615 @@
+// Backward of everything before the layer function F: F_pre (§2.5 (1)), the
+// coefficients with their Sinkhorn iteration (§2.3, §2.4) and the projection
+// with its RMS (§2.1, §2.2), page "mHC 算法分析 & cutile 高效实现", and of the
+// residual path of X_next.  G = dX_next, dF = dF_pre, X read as it was kept
+// (kept.cuh), K = nC, N = n² + 2n:
+//
+//   dots    dH_pre[i] = Σ_c dF[c]·X[i][c]
+//   coefs   dH̃_pre  = dH_pre·H_pre·(1 − H_pre)
+//           dH̃_post = dH_post·H_post·(1 − H_post/2)
+//           dH̃_res  = the Sinkhorn iteration's (below)
+//           dbias = Σ_b dH̃,  dα_seg = Σ_b Σ_{k in seg} dH̃·Y/r
+//           dY = α·dH̃/r,     s = −Σ_k dY·Y/(K·r²)       (r = sqrt(Σx²/K))
+//   streams dX[j] = Σ_i H_res[i][j]·G[i] + H_pre[j]·dF + Σ_k dY[k]·φ[k] + s·X[j]
+//   phi     dφ_t[k] = Σ_b dY[b][k]·X[b]                  (phi_grad.cu)
+//
+// The sum over all channels in `dots` stands between F's gradient and dX, so
+// the codes are read by dots and again by streams.
+//
+// Sinkhorn.  With A = exp(H̃_res) (rows shifted by their maximum, which changes
+// no iterate), the iteration is u_t = 1/(A·v_{t−1}), v_t = 1/(Aᵀ·u_t), v_0 = 1,
+// H_res = diag(u_T)·A·diag(v_T).  The forward is run again, keeping the u_t and
+// v_t (2n values a step, not the n² of the iterate), and each step is undone:
+//
+//   dA = u·v·dH_res,  ū_i = Σ_j A·v·dH_res,  v̄_j = Σ_i u·A·dH_res
+//   for t = T … 1:  c̄ = −v̄·v_t²,            dA += u_t ⊗ c̄
+//                   r̄ = −(ū + A·c̄)·u_t²,    dA += r̄ ⊗ v_{t−1}
+//                   v̄ = Aᵀ·r̄,  ū = 0
+//   dH̃_res = dA·A                            (T = 0: dA = dH_res)
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "check.cuh"
+#include "kept.cuh"
+#include "mix.cuh"
+#include "ptx.cuh"
+#include "slots.cuh"
+#include "train.h"
+
+namespace mhc {
+namespace {
+
+// ------------------------------------------------------------------ dots
+
+constexpr int kDotWarps = 8;
+
+// A CTA per group of tokens, lanes as in slots.cuh, warps over the channels.
+template <int n>
+__global__ void __launch_bounds__(kDotWarps * 32)
+dots_kernel(const uint16_t *__restrict__ dF, const uint8_t *__restrict__ Xq,
+            const uint8_t *__restrict__ Xs, int64_t B, int64_t C, float *__restrict__ dH_pre)
+{
+    using S = Slots<n>;
+    __shared__ float part[kDotWarps][8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = lane & 3, slot = (lane >> 2) & (S::n2 - 1), tok = (lane >> 2) / S::n2;
+    const int64_t nb = kept_blocks(C);
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    const int64_t b = static_cast<int64_t>(blockIdx.x) * S::tokens + tok;
+    const bool have = b < B && slot < n && in_range(1201, b, 1, B);
+    const int64_t row = b * n + slot;
+    uint2 q;
+    uint4 f;
+    uint32_t E;
+    const auto load = [&](int64_t cg) {
+        const int64_t c = cg * 32 + t * 8;
+        if (have && cg < nb && c < C && in_range(1202, c, 8, C)) {
+            q = kept::ld_stream_v2(Xq + row * C + c);
+            f = ptx::ld_stream_v4(dF + b * C + c);
+            E = __ldg(Xs + row * nb + cg);
+        } else {
+            q = make_uint2(0, 0);
+            f = make_uint4(0, 0, 0, 0);
+            E = kept::kScaleMin;
+        }
+    };
+    float s = 0.f;
+    load(warp);
+    for (int64_t cg = warp; cg < nb; cg += kDotWarps) {
+        float x[8], v[8];
+        kept::decode8(q, kept::scale_value(E), x);
+        unpack8(f, v);
+        load(cg + kDotWarps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(x[e], v[e], s);
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    if (t == 0) part[warp][lane >> 2] = s;
+    __syncthreads();
+    if (warp == 0 && have && t == 0) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDotWarps; ++w) sum += part[w][lane >> 2];
+        dH_pre[row] = sum;
+    }
+}
+
+// ----------------------------------------------------------------- coefs
+
+constexpr int kCoefThreads = 64;
+constexpr int kCoefWarps = kCoefThreads / 32;
+constexpr int kHistSmem = 96 * 1024;  // u_t and v_t of a CTA's tokens, where they fit
+
+__host__ __device__ constexpr int dy_cols(int n) { return (n * n + 2 * n + 15) / 16 * 16; }  // dY rows, padded
+
+struct CoefOut {
+    uint16_t *dY_rows;   // [B][dy_cols] bf16, zero-padded
+    uint16_t *dY_terms;  // [3N][padded tokens] bf16 (train.h)
+    float *sx;           // [B]
+    float *part;         // [CTAs][N + 3]: Σ dH̃ by column, then by α
+    float *hist;         // [CTAs][iters][2n][threads], or NULL: in shared memory
+};
+
+template <int n>
+__global__ void __launch_bounds__(kCoefThreads)
+coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, CoefOut o)
+{
+    constexpr int N = n * n + 2 * n, kCols = dy_cols(n);
+    extern __shared__ float smem_hist[];
+    __shared__ float bsum[kCoefWarps][N + 3];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float *hist = o.hist ? o.hist + static_cast<int64_t>(blockIdx.x) * a.iters * 2 * n * kCoefThreads
+                         : smem_hist;
+    hist += threadIdx.x;
+    const auto u_at = [&](int t, int i) -> float & { return hist[(t * 2 * n + i) * kCoefThreads]; };
+    const auto v_at = [&](int t, int j) -> float & { return hist[(t * 2 * n + n + j) * kCoefThreads]; };
+    for (int k = lane; k < N + 3; k += 32) bsum[warp][k] = 0.f;
+    __syncwarp();
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+
+    const float inv_K = 1.0f / (static_cast<float>(n) * static_cast<float>(a.C));
+    for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * kCoefThreads; b0 < Bp;
+         b0 += static_cast<int64_t>(gridDim.x) * kCoefThreads) {
+        const int64_t b = b0 + threadIdx.x;
+        const bool live = b < a.B && in_range(1211, b, 1, a.B);
+        const float *y = a.Y + b * N;
+        const float inv_r = live ? 1.0f / __ldg(a.r + b) : 0.f;
+        float A[n][n], dA[n][n];
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+#pragma unroll
+                for (int j = 0; j < n; ++j) {
+                    const int k = 2 * n + i * n + j;
+                    A[i][j] = a.a_res * __ldg(y + k) * inv_r + __ldg(a.bias + k);
+                    dA[i][j] = __ldg(a.dH_res + b * n * n + i * n + j);
+                }
+            if (a.iters > 0) {
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    float mx = A[i][0];
+#pragma unroll
+                    for (int j = 1; j < n; ++j) mx = fmaxf(mx, A[i][j]);
+#pragma unroll
+                    for (int j = 0; j < n; ++j) A[i][j] = expf(A[i][j] - mx);
+                }
+                float u[n], v[n], bu[n], bv[n];
+#pragma unroll
+                for (int j = 0; j < n; ++j) v[j] = 1.0f;
+                for (int t = 0; t < a.iters; ++t) {
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        float p[n];
+#pragma unroll
+                        for (int j = 0; j < n; ++j) p[j] = A[i][j] * v[j];
+                        u[i] = recip_approx(tree_sum<n>(p));
+                        u_at(t, i) = u[i];
+                    }
+#pragma unroll
+                    for (int j = 0; j < n; ++j) {
+                        float p[n];
+#pragma unroll
+                        for (int i = 0; i < n; ++i) p[i] = u[i] * A[i][j];
+                        v[j] = recip_approx(tree_sum<n>(p));
+                        v_at(t, j) = v[j];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < n; ++i) bu[i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < n; ++j) bv[j] = 0.f;
+#pragma unroll
+                for (int i = 0; i < n; ++i)
+#pragma unroll
+                    for (int j = 0; j < n; ++j) {
+                        const float d = dA[i][j], av = A[i][j] * v[j];
+                        bu[i] = fmaf(av, d, bu[i]);
+                        bv[j] = fmaf(u[i] * A[i][j], d, bv[j]);
+                        dA[i][j] = u[i] * v[j] * d;
+                    }
+                for (int t = a.iters - 1; t >= 0; --t) {
+                    float c[n];
+#pragma unroll
+                    for (int j = 0; j < n; ++j) {
+                        const float vj = v_at(t, j);
+                        c[j] = -bv[j] * vj * vj;
+                    }
+#pragma unroll
+                    for (int j = 0; j < n; ++j) v[j] = t > 0 ? v_at(t - 1, j) : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const float ui = u_at(t, i);
+                        float p[n];
+#pragma unroll
+                        for (int j = 0; j < n; ++j) {
+                            p[j] = A[i][j] * c[j];
+                            dA[i][j] = fmaf(ui, c[j], dA[i][j]);
+                        }
+                        u[i] = -(bu[i] + tree_sum<n>(p)) * ui * ui;  // r̄
+                        bu[i] = 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < n; ++j) {
+                        float p[n];
+#pragma unroll
+                        for (int i = 0; i < n; ++i) {
+                            p[i] = A[i][j] * u[i];
+                            dA[i][j] = fmaf(u[i], v[j], dA[i][j]);
+                        }
+                        bv[j] = tree_sum<n>(p);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < n; ++i)
+#pragma unroll
+                    for (int j = 0; j < n; ++j) A[i][j] = expf(A[i][j]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+#pragma unroll
+                for (int j = 0; j < n; ++j) A[i][j] = dA[i][j] = 0.f;
+        }
+
+        float sx = 0.f, da[3] = {0.f, 0.f, 0.f};
+        uint32_t packed = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            float d = 0.f;  // dH̃ of column k
+            if (k < n) {
+                if (live) {
+                    const float h = __ldg(a.H_pre + b * n + k);
+                    d = __ldg(dH_pre + b * n + k) * h * (1.0f - h);
+                }
+            } else if (k < 2 * n) {
+                if (live) {
+                    const float h = __ldg(a.H_post + b * n + (k - n));
+                    d = __ldg(a.dH_post + b * n + (k - n)) * h * (1.0f - 0.5f * h);
+                }
+            } else {
+                d = dA[(k - 2 * n) / n][(k - 2 * n) % n] * A[(k - 2 * n) / n][(k - 2 * n) % n];
+            }
+            const float yk = live ? __ldg(y + k) : 0.f;
+            const float alpha = k < n ? a.a_pre : k < 2 * n ? a.a_post : a.a_res;
+            da[k < n ? 0 : k < 2 * n ? 1 : 2] += d * (yk * inv_r);
+            const float dy = alpha * d * inv_r;
+            sx = fmaf(-dy, yk, sx);
+            float s = d;
+#pragma unroll
+            for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
+            if (lane == 0) bsum[warp][k] += s;
+            // dY as one bf16 for dX, whose own rounding is as large, and as three
+            // for dφ, which is kept in fp32
+            const uint32_t hi = pack_bf16_rn(dy, 0.f) & 0xFFFFu;
+            const float rest = dy - bf16_lo(hi);
+            const uint32_t mid = pack_bf16_rn(rest, 0.f) & 0xFFFFu;
+            const uint32_t low = pack_bf16_rn(rest - bf16_lo(mid), 0.f) & 0xFFFFu;
+            if (b < Bp && in_range(1212, (3 * k + 2) * Bp + b, 1, 3 * N * Bp)) {
+                uint16_t *dst = o.dY_terms + static_cast<int64_t>(3 * k) * Bp + b;
+                dst[0] = static_cast<uint16_t>(hi);
+                dst[Bp] = static_cast<uint16_t>(mid);
+                dst[2 * Bp] = static_cast<uint16_t>(low);
+            }
+            if (k % 2 == 0) {
+                packed = hi;
+            } else if (live) {
+                reinterpret_cast<uint32_t *>(o.dY_rows + b * kCols)[k / 2] = packed | (hi << 16);
+            }
+        }
+        if (live) {
+            if constexpr (N % 2 == 1) reinterpret_cast<uint32_t *>(o.dY_rows + b * kCols)[N / 2] = packed;
+#pragma unroll
+            for (int k = (N + 1) / 2; k < kCols / 2; ++k)
+                reinterpret_cast<uint32_t *>(o.dY_rows + b * kCols)[k] = 0;
+            o.sx[b] = sx * inv_r * inv_r * inv_K;
+        }
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            float s = da[e];
+#pragma unroll
+            for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
+            if (lane == 0) bsum[warp][N + e] += s;
+        }
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < N + 3; k += kCoefThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kCoefWarps; ++w) s += bsum[w][k];
+        o.part[static_cast<int64_t>(blockIdx.x) * (N + 3) + k] = s;
+    }
+}
+
+// dbias and dα from the CTAs' sums: a warp per value.
+__global__ void __launch_bounds__(32)
+bias_join_kernel(const float *__restrict__ part, int ctas, int N, int accumulate,
+                 float *__restrict__ dbias, float *__restrict__ dalpha)
+{
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    const int k = blockIdx.x, lane = threadIdx.x;
+    float s = 0.f;
+    for (int c = lane; c < ctas; c += 32) s += __ldcg(part + static_cast<int64_t>(c) * (N + 3) + k);
+#pragma unroll
+    for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
+    if (lane != 0) return;
+    float *dst = k < N ? dbias + k : dalpha + (k - N);
+    *dst = accumulate ? *dst + s : s;
+}
+
+// --------------------------------------------------------------- streams
+//
+// Bound by memory (G, the codes and dF in, dX out).  A CTA holds φ for a strip
+// of channels in shared memory, in the order of the tensor product's operand,
+// and walks token tiles; a warp mixes 16 tokens × 32 channels of all streams.
+// dY·φ runs as mma.m16n8k16 (16 tokens, N padded to 16 as k) into the very
+// registers in which the other terms are added: with the four column tiles of a
+// warp taken as channels 8t + 2q, 8t + 2q + 1 (t: lane, q: tile), a lane ends up
+// with 8 neighbouring channels of two tokens, its 128-bit accesses.  The product
+// is a rank-N update of a streamed matrix; tcgen05 would bring it through TMEM
+// and shared memory to where these lanes have it already.
+
+constexpr int kStreamWarps = 8;
+constexpr int kStreamThreads = kStreamWarps * 32;
+
+template <int n>
+struct DX {
+    static constexpr int N = n * n + 2 * n;
+    static constexpr int kCols = dy_cols(n);
+    static constexpr int KS = kCols / 16;
+    static constexpr int CG = n <= 4 ? 8 : n <= 6 ? 4 : 2;  // groups of 32 channels in a strip
+    static constexpr int S = CG * 32;
+    static constexpr int TS = kStreamWarps / CG * 16;       // tokens of a step
+    static constexpr int P = n * n + n + 1;                 // H_resᵀ, H_pre, s of a token
+    static constexpr int kPhiBytes = n * CG * KS * 2 * 32 * 16;
+    static constexpr int kSmem = kPhiBytes + 2 * TS * P * 4;
+};
+
+template <int n>
+__global__ void __launch_bounds__(kStreamThreads, n <= 4 ? 2 : 1)
+streams_kernel(const uint16_t *dX_next, const uint16_t *__restrict__ dF,
+               const uint8_t *__restrict__ Xq, const uint8_t *__restrict__ Xs,
+               const uint16_t *__restrict__ phi_t, const float *__restrict__ H_res,
+               const float *__restrict__ H_pre, const float *__restrict__ sx,
+               const uint16_t *__restrict__ dY_rows, int64_t B, int64_t C, int64_t steps,
+               int64_t units, uint16_t *dX)
+{
+    using D = DX<n>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint4 *phi_s = reinterpret_cast<uint4 *>(smem);
+    float *co = reinterpret_cast<float *>(smem + D::kPhiBytes);  // [2][TS][P]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int cg = warp % D::CG, tt = warp / D::CG;
+    const int64_t nb = kept_blocks(C), K = n * C;
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+
+    const auto stage = [&](int64_t u, int buf) {
+        if (u < u1) {
+            const int64_t b0 = u % steps * D::TS;
+            for (int x = threadIdx.x; x < D::TS * D::P; x += kStreamThreads) {
+                const int tk = x / D::P, e = x - tk * D::P;
+                const int64_t b = b0 + tk;
+                if (b >= B || !in_range(1221, b, 1, B)) continue;
+                const float *src = e < n * n ? H_res + b * n * n + (e % n) * n + e / n
+                                   : e < n * n + n ? H_pre + b * n + (e - n * n) : sx + b;
+                ptx::cp_async4(co + (buf * D::TS + tk) * D::P + e, src);
+            }
+        }
+        ptx::cp_async_commit();
+    };
+    // φ of a strip, rows k and k + 1 of 8 channels at a time: lane (gg, tk) of
+    // k step ks holds, for column tile q, k = 16·ks + 2·tk (+1, +8, +9) at channel
+    // 8·(gg / 2) + 2q + gg % 2
+    const auto load_phi = [&](int64_t strip) {
+        constexpr int kPairs = D::kCols / 2, kOct = D::S / 8;
+        for (int x = threadIdx.x; x < n * kPairs * kOct; x += kStreamThreads) {
+            const int oct = x % kOct, pair = x / kOct % kPairs, j = x / (kOct * kPairs);
+            const int64_t c = strip * D::S + oct * 8;
+            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+            if (c < C && in_range(1222, c, 8, C)) {
+                const uint16_t *src = phi_t + 2 * pair * K + j * C + c;
+                if (2 * pair < D::N) lo = __ldg(reinterpret_cast<const uint4 *>(src));
+                if (2 * pair + 1 < D::N) hi = __ldg(reinterpret_cast<const uint4 *>(src + K));
+            }
+            const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
+            const int ks = pair / 8, half = pair % 8 / 4, tk = pair % 4, toct = oct % 4;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(phi_s) +
+                            (((j * D::CG + oct / 4) * D::KS + ks) * 2) * 128;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t *d = dst + (q / 2) * 128 + (q % 2) * 2 + half;
+                d[((2 * toct) * 4 + tk) * 4] = __byte_perm(l[q], h[q], 0x5410);
+                d[((2 * toct + 1) * 4 + tk) * 4] = __byte_perm(l[q], h[q], 0x7632);
+            }
+        }
+    };
+
+    int64_t have_strip = -1;
+    stage(u0, 0);
+    for (int64_t u = u0; u < u1; ++u) {
+        const int buf = static_cast<int>((u - u0) & 1);
+        const int64_t strip = u / steps;
+        const int64_t bA = u % steps * D::TS + tt * 16 + g, bB = bA + 8;
+        const int64_t c = strip * D::S + cg * 32 + t * 8;
+        const bool okc = c < C && in_range(1223, c, 8, C);
+        const bool ok[2] = {okc && bA < B, okc && bB < B};
+        const int64_t bb[2] = {bA, bB};
+        uint4 gv[2][n], fv[2];
+        uint2 q[2][n];
+        uint32_t E[2][n];
+        uint32_t ya[D::KS][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t b = bb[h];
+            if (ok[h]) {
+#pragma unroll
+                for (int i = 0; i < n; ++i) gv[h][i] = ptx::ld_stream_v4(dX_next + (b * n + i) * C + c);
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    q[h][i] = kept::ld_stream_v2(Xq + (b * n + i) * C + c);
+                    E[h][i] = __ldg(Xs + (b * n + i) * nb + (c >> 5));
+                }
+                fv[h] = ptx::ld_stream_v4(dF + b * C + c);
+            } else {
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    gv[h][i] = make_uint4(0, 0, 0, 0);
+                    q[h][i] = make_uint2(0, 0);
+                    E[h][i] = kept::kScaleMin;
+                }
+                fv[h] = make_uint4(0, 0, 0, 0);
+            }
+            const uint32_t *yr = reinterpret_cast<const uint32_t *>(dY_rows + b * D::kCols);
+#pragma unroll
+            for (int ks = 0; ks < D::KS; ++ks) {
+                ya[ks][h] = b < B ? __ldg(yr + ks * 8 + t) : 0u;
+                ya[ks][h + 2] = b < B ? __ldg(yr + ks * 8 + t + 4) : 0u;
+            }
+        }
+        if (strip != have_strip) {
+            __syncthreads();
+            load_phi(strip);
+            have_strip = strip;
+        }
+        ptx::cp_async_wait_all();
+        __syncthreads();
+        stage(u + 1, buf ^ 1);
+        const float *cA = co + (buf * D::TS + tt * 16 + g) * D::P;
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            float d[4][4];
+            const uint4 *ph = phi_s + ((j * D::CG + cg) * D::KS) * 2 * 32 + lane;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) d[x][0] = d[x][1] = d[x][2] = d[x][3] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < D::KS; ++ks) {
+                const uint4 p0 = ph[ks * 64], p1 = ph[ks * 64 + 32];
+                mma_16816(d[0], ya[ks][0], ya[ks][1], ya[ks][2], ya[ks][3], p0.x, p0.y);
+                mma_16816(d[1], ya[ks][0], ya[ks][1], ya[ks][2], ya[ks][3], p0.z, p0.w);
+                mma_16816(d[2], ya[ks][0], ya[ks][1], ya[ks][2], ya[ks][3], p1.x, p1.y);
+                mma_16816(d[3], ya[ks][0], ya[ks][1], ya[ks][2], ya[ks][3], p1.z, p1.w);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float *cf = cA + h * 8 * D::P;
+                uint64_t acc[4], w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[x] = f2_pack(d[x][2 * h], d[x][2 * h + 1]);
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const uint64_t hh = f2_pack(cf[j * n + i], cf[j * n + i]);
+                    unpack8_pairs(gv[h][i], w);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[x] = f2_fma(hh, w[x], acc[x]);
+                }
+                const uint64_t hp = f2_pack(cf[n * n + j], cf[n * n + j]);
+                unpack8_pairs(fv[h], w);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[x] = f2_fma(hp, w[x], acc[x]);
+                float xf[8];
+                kept::decode8(q[h][j], kept::scale_value(E[h][j]), xf);
+                const uint64_t ss = f2_pack(cf[n * n + n], cf[n * n + n]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    acc[x] = f2_fma(ss, f2_pack(xf[2 * x], xf[2 * x + 1]), acc[x]);
+                if (ok[h] && in_range(1224, bb[h], 1, B))
+                    ptx::st_stream_v4(dX + (bb[h] * n + j) * C + c, pack8_pairs(acc));
+            }
+        }
+    }
+    ptx::cp_async_wait_all();
+}
+
+// -------------------------------------------------------------- launches
+
+struct Ws {
+    float *dH_pre, *sx, *part, *hist;
+    uint16_t *dY_rows, *dY_terms;
+    void *phi;
+    int64_t ctas;      // of coefs_kernel
+    size_t hist_smem;  // its dynamic shared memory
+    size_t total;
+};
+
+Ws carve(void *base, int64_t B, int n, int64_t C, int iters, int num_sms)
+{
+    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const int N = num_coeffs(n);
+    const int64_t Bp = phi_grad_padded_tokens(B);
+    Ws w{};
+    uint8_t *p = static_cast<uint8_t *>(base);
+    size_t at = 0;
+    const auto take = [&](size_t bytes) { uint8_t *r = p + at; at += up(bytes); return r; };
+    const size_t hist = static_cast<size_t>(iters) * 2 * n * kCoefThreads * sizeof(float);
+    w.hist_smem = hist <= static_cast<size_t>(kHistSmem) ? hist : 0;
+    const int64_t most = (w.hist_smem != 0 || iters == 0 ? 16 : 2) * static_cast<int64_t>(num_sms);
+    const int64_t need = (Bp + kCoefThreads - 1) / kCoefThreads;
+    w.ctas = need < most ? need : most;
+    w.dH_pre = reinterpret_cast<float *>(take(static_cast<size_t>(B) * n * 4));
+    w.sx = reinterpret_cast<float *>(take(static_cast<size_t>(B) * 4));
+    w.part = reinterpret_cast<float *>(take(static_cast<size_t>(w.ctas) * (N + 3) * 4));
+    w.dY_rows = reinterpret_cast<uint16_t *>(take(static_cast<size_t>(B) * dy_cols(n) * 2));
+    w.dY_terms = reinterpret_cast<uint16_t *>(take(static_cast<size_t>(Bp) * kPhiTerms * N * 2));
+    w.hist = nullptr;
+    if (w.hist_smem == 0 && iters > 0)
+        w.hist = reinterpret_cast<float *>(take(static_cast<size_t>(w.ctas) * hist));
+    w.phi = take(phi_grad_workspace_bytes(B, n, C, num_sms));
+    w.total = at;
+    return w;
+}
+
+template <int n>
+cudaError_t launch_n(const PreBackwardArgs &a, const Ws &w, int num_sms, cudaStream_t stream)
+{
+    using D = DX<n>;
+    constexpr int N = D::N;
+    const int64_t Bp = phi_grad_padded_tokens(a.B);
+    const int64_t groups = (a.B + Slots<n>::tokens - 1) / Slots<n>::tokens;
+    cudaError_t e = launch_pdl(dots_kernel<n>, dim3(static_cast<unsigned>(groups)),
+                               dim3(kDotWarps * 32), 0, stream, a.dF_pre, a.Xq, a.Xs, a.B, a.C,
+                               w.dH_pre);
+    if (e != cudaSuccess) return e;
+    const CoefOut o{w.dY_rows, w.dY_terms, w.sx, w.part, w.hist};
+    static std::atomic<int> per_sm{0};
+    int resident = per_sm.load(std::memory_order_acquire);
+    if (resident == 0) {
+        e = cudaFuncSetAttribute(coefs_kernel<n>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kHistSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(streams_kernel<n>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, D::kSmem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, streams_kernel<n>,
+                                                              kStreamThreads, D::kSmem);
+        if (e != cudaSuccess) return e;
+        if (resident < 1) resident = 1;
+        per_sm.store(resident, std::memory_order_release);
+    }
+    e = launch_pdl(coefs_kernel<n>, dim3(static_cast<unsigned>(w.ctas)), dim3(kCoefThreads),
+                   w.hist_smem, stream, a, w.dH_pre, Bp, o);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(bias_join_kernel, dim3(N + 3), dim3(32), 0, stream, w.part,
+                   static_cast<int>(w.ctas), N, a.accumulate, a.dbias, a.dalpha);
+    if (e != cudaSuccess) return e;
+    const int64_t steps = (a.B + D::TS - 1) / D::TS;
+    const int64_t units = (a.C + D::S - 1) / D::S * steps;
+    const int64_t wave = static_cast<int64_t>(num_sms) * resident;
+    e = launch_pdl(streams_kernel<n>, dim3(static_cast<unsigned>(units < wave ? units : wave)),
+                   dim3(kStreamThreads), D::kSmem, stream, a.dX_next, a.dF_pre, a.Xq, a.Xs,
+                   a.phi_t, a.H_res, a.H_pre, w.sx, w.dY_rows, a.B, a.C, steps, units, a.dX);
+    if (e != cudaSuccess) return e;
+    return launch_phi_grad(a.Xq, a.Xs, w.dY_terms, a.B, n, a.C, a.accumulate, a.dphi_t, w.phi,
+                           num_sms, stream);
+}
+
+}  // namespace
+
+size_t pre_backward_workspace_bytes(int64_t B, int n, int64_t C, int iters, int num_sms)
+{
+    return B > 0 ? carve(nullptr, B, n, C, iters, num_sms).total : 0;
+}
+
+cudaError_t launch_pre_backward(const PreBackwardArgs &a, void *workspace, int num_sms,
+                                cudaStream_t stream)
+{
+    const Ws w = carve(workspace, a.B, a.n, a.C, a.iters, num_sms);
+    switch (a.n) {
+#define MHC_CASE(k) \
+    case k: return launch_n<k>(a, w, num_sms, stream);
+        MHC_CASE(1) MHC_CASE(2) MHC_CASE(3) MHC_CASE(4) MHC_CASE(5) MHC_CASE(6) MHC_CASE(7)
+        MHC_CASE(8)
+#undef MHC_CASE
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace mhc

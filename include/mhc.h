@@ -3,7 +3,8 @@
  *
  * Manifold-constrained hyper-connections (mHC) widen the residual stream of a
  * transformer into n parallel streams and mix them with per-token
- * coefficients.  This library computes the forward pass of that mixing as
+ * coefficients.  This library computes the forward pass of that mixing (and,
+ * for training, its backward pass) as
  * analysed on the page "mHC 算法分析 & cutile 高效实现" (mHC algorithm
  * analysis and an efficient cuTile implementation), §2.1–§2.5 and §3:
  *
@@ -20,6 +21,8 @@
  *   mhc_rmsnorm_gemm    C = rmsnorm(A) @ B for any N (Lazy Pre-Norm, second page §2)
  *   mhc_*_f32w / _split / _f32   the fp32-weight, fp32-F_out precision variant (§5)
  *   mhc_*_e4m3          the fp8 e4m3 precision variant (§4)
+ *   mhc_embed*, mhc_ckpt_*, mhc_post_res_apply_ckpt*, mhc_*_backward*
+ *                       training: token ids to streams, X kept in 8 bits, gradients
  *
  * Shapes: B tokens (batch × sequence), expansion n, hidden size C,
  * K = n·C, N = n² + 2n.
@@ -342,6 +345,111 @@ int mhc_rmsnorm_gemm(const mhc_bf16 *A, const mhc_bf16 *B_t, int64_t M, int64_t 
  */
 int mhc_gemm_rms_noalloc(const mhc_bf16 *X, const mhc_bf16 *phi_t, int64_t B, int n, int64_t C,
                          float *Y, float *r, mhc_stream_t stream);
+
+/*
+ * Training.  The calls below are the forward's way in (token ids to streams),
+ * the update that keeps X for the backward pass, and that pass.  A training
+ * step of one layer runs
+ *
+ *   forward   mhc_gemm_rms_coeffs, mhc_pre_apply, [F], mhc_post_res_apply_ckpt
+ *   backward  mhc_post_res_apply_backward, [F's backward], mhc_pre_backward
+ *
+ * and keeps between the two Y, r, the H, F_out and X, which is n times as wide
+ * as an ordinary residual, in 8 bits:
+ *   Xq [B][n][C] uint8                one OCP e4m3 code per value
+ *   Xs [B][n][ceil(C/32)] uint8       one byte E per 32 channels of a stream
+ * A value stands for code·2^(E-127); E is the smallest in [10, 247] with
+ * amax <= 448·2^(E-127) over its block, so nothing saturates (but magnitudes over
+ * 240·2^120, next to the end of bf16's range, which are kept as that) and every
+ * value stood for is finite and exact in bf16.  Codes round to nearest even (relative 2^-4 at
+ * most, for values within 2^-15 of the block's largest).  A block that holds an
+ * infinity or a NaN is kept as NaN throughout (E = 255).
+ *
+ * Rules, layouts and status codes are those of the forward calls.  Gradients
+ * have the types of what they are the gradients of, those of weights (dtable,
+ * dphi_t, dbias, dalpha) fp32: with accumulate == 0 they are written whole,
+ * otherwise added to.  B == 0 launches no kernel; it sets the weights'
+ * gradients to zero when accumulate == 0.  All sums are fp32 in a fixed order:
+ * results are bitwise reproducible for a given device and shape.
+ */
+
+/*
+ * Token ids to the n streams: X[b][i][c] = scale·table[ids[b]][c] for every i,
+ * rounded to bf16.
+ *   table [V][C] bf16 (mhc_embed_f32: fp32), ids [B] int64, X [B][n][C] bf16
+ * An id outside [0, V) is padding: its streams are zero.  scale finite and
+ * V >= 1 (MHC_ERR_INVALID), V < 2^31 (MHC_ERR_UNSUPPORTED).
+ */
+int mhc_embed(const mhc_bf16 *table, const int64_t *ids, float scale, int64_t V, int64_t B, int n,
+              int64_t C, mhc_bf16 *X, mhc_stream_t stream);
+int mhc_embed_f32(const float *table, const int64_t *ids, float scale, int64_t V, int64_t B,
+                  int n, int64_t C, mhc_bf16 *X, mhc_stream_t stream);
+
+/*
+ * Its gradient: dtable[v][c] (+)= scale·Σ_{b: ids[b]=v} Σ_i dX[b][i][c], fp32
+ * [V][C], summed over the positions sorted by id (no atomics).  Padding adds
+ * to no row.  workspace: mhc_embed_backward_workspace_bytes.
+ */
+size_t mhc_embed_backward_workspace_bytes(int64_t V, int64_t B, int n, int64_t C);
+int mhc_embed_backward(const mhc_bf16 *dX, const int64_t *ids, float scale, int accumulate,
+                       int64_t V, int64_t B, int n, int64_t C, float *dtable, void *workspace,
+                       size_t workspace_bytes, mhc_stream_t stream);
+
+/* X to its 8-bit form, and the values that the 8-bit form stands for (exact in bf16). */
+int mhc_ckpt_pack(const mhc_bf16 *X, int64_t B, int n, int64_t C, uint8_t *Xq, uint8_t *Xs,
+                  mhc_stream_t stream);
+int mhc_ckpt_unpack(const uint8_t *Xq, const uint8_t *Xs, int64_t B, int n, int64_t C,
+                    mhc_bf16 *X, mhc_stream_t stream);
+
+/*
+ * mhc_post_res_apply (or _f32) that keeps X in 8 bits in the same pass.
+ * X_next may be exactly X: what the backward needs of X is kept.
+ */
+int mhc_post_res_apply_ckpt(const mhc_bf16 *X, const mhc_bf16 *F_out, const float *H_res,
+                            const float *H_post, int64_t B, int n, int64_t C, mhc_bf16 *X_next,
+                            uint8_t *Xq, uint8_t *Xs, mhc_stream_t stream);
+int mhc_post_res_apply_ckpt_f32(const mhc_bf16 *X, const float *F_out, const float *H_res,
+                                const float *H_post, int64_t B, int n, int64_t C,
+                                mhc_bf16 *X_next, uint8_t *Xq, uint8_t *Xs, mhc_stream_t stream);
+
+/*
+ * Backward of step 4b, but for its dX (which mhc_pre_backward forms):
+ *   dF_out[b][c]    = Σ_i H_post[b][i]·dX_next[b][i][c]       (F_out's type)
+ *   dH_res[b][i][j] = Σ_c dX_next[b][i][c]·X[b][j][c]         fp32
+ *   dH_post[b][i]   = Σ_c dX_next[b][i][c]·F_out[b][c]        fp32
+ * with X as it was kept.
+ */
+int mhc_post_res_apply_backward(const mhc_bf16 *dX_next, const uint8_t *Xq, const uint8_t *Xs,
+                                const mhc_bf16 *F_out, const float *H_post, int64_t B, int n,
+                                int64_t C, mhc_bf16 *dF_out, float *dH_res, float *dH_post,
+                                mhc_stream_t stream);
+int mhc_post_res_apply_backward_f32(const mhc_bf16 *dX_next, const uint8_t *Xq, const uint8_t *Xs,
+                                    const float *F_out, const float *H_post, int64_t B, int n,
+                                    int64_t C, float *dF_out, float *dH_res, float *dH_post,
+                                    mhc_stream_t stream);
+
+/*
+ * Backward of steps 1-4a and of X's way through step 4b, after F's backward has
+ * turned dF_out into dF_pre:
+ *   dH_pre[i] = Σ_c dF_pre[c]·X[i][c]
+ *   dH̃        = through the sigmoids and the `iters` Sinkhorn steps
+ *   dY        = α·dH̃/r,   s = -Σ_k dY[k]·Y[k]/(K·r²)
+ *   dX[j]     = Σ_i H_res[i][j]·dX_next[i] + H_pre[j]·dF_pre + Σ_k dY[k]·φ[k] + s·X[j]
+ *   dphi_t[k] = Σ_b dY[b][k]·X[b],  dbias = Σ_b dH̃,  dalpha = Σ_b Σ_seg dH̃·Y/r
+ * with X as it was kept, and Y, r, H_* as the forward wrote them for the same
+ * phi_t, alphas, bias and iters.  dalpha is [3]: pre, post, res.  dX may be
+ * exactly dX_next.  A token with r = 0 has gradients that are not finite, as
+ * its coefficients are.  workspace: mhc_pre_backward_workspace_bytes on the
+ * current device.
+ */
+size_t mhc_pre_backward_workspace_bytes(int64_t B, int n, int64_t C, int iters);
+int mhc_pre_backward(const mhc_bf16 *dX_next, const mhc_bf16 *dF_pre, const uint8_t *Xq,
+                     const uint8_t *Xs, const mhc_bf16 *phi_t, float alpha_pre, float alpha_post,
+                     float alpha_res, const float *bias, int iters, const float *Y, const float *r,
+                     const float *H_pre, const float *H_post, const float *H_res,
+                     const float *dH_res, const float *dH_post, int accumulate, int64_t B, int n,
+                     int64_t C, mhc_bf16 *dX, float *dphi_t, float *dbias, float *dalpha,
+                     void *workspace, size_t workspace_bytes, mhc_stream_t stream);
 
 /*
  * Reads and clears the device status word of the current device: MHC_OK, or
