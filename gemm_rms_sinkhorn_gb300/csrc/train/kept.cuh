@@ -82,7 +82,34 @@ __device__ __forceinline__ void decode8(const uint2 &q, float scale, float (&f)[
     }
 }
 
-// The same as bf16 (exact too).
+// Eight codes to the fp32 values of the codes alone, as four channel pairs:
+// where sums run over one block, its scale is applied to the sum.
+__device__ __forceinline__ void codes8_pairs(const uint2 &q, uint64_t (&t)[4])
+{
+    const uint32_t w[4] = {q.x, q.x >> 16, q.y, q.y >> 16};
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        float lo, hi;
+        f16x2_to_f32(e4m3x2_to_f16x2(w[p]), lo, hi);
+        t[p] = f2_pack(lo, hi);
+    }
+}
+
+// The same as bf16 pairs (exact).
+__device__ __forceinline__ uint4 codes8_bf16(const uint2 &q)
+{
+    const uint32_t w[4] = {q.x, q.x >> 16, q.y, q.y >> 16};
+    uint32_t r[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        float lo, hi;
+        f16x2_to_f32(e4m3x2_to_f16x2(w[p]), lo, hi);
+        r[p] = pack_bf16_rn(lo, hi);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// The values that eight codes stand for, as bf16 (exact).
 __device__ __forceinline__ uint4 decode8_bf16(const uint2 &q, float scale)
 {
     float f[8];

@@ -43,58 +43,81 @@ namespace {
 
 // ------------------------------------------------------------------ dots
 
+// Bound by the codes' bytes.  A lane takes 8 channels of all n streams, so dF is
+// widened once for them; a block's scale multiplies its partial sum, not its
+// values.  W warps share a token.
 constexpr int kDotWarps = 8;
 
-// A CTA per group of tokens, lanes as in slots.cuh, warps over the channels.
-template <int n>
+template <int n, int W>
 __global__ void __launch_bounds__(kDotWarps * 32)
 dots_kernel(const uint16_t *__restrict__ dF, const uint8_t *__restrict__ Xq,
             const uint8_t *__restrict__ Xs, int64_t B, int64_t C, float *__restrict__ dH_pre)
 {
-    using S = Slots<n>;
-    __shared__ float part[kDotWarps][8];
+    __shared__ float part[kDotWarps][n];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = lane & 3, slot = (lane >> 2) & (S::n2 - 1), tok = (lane >> 2) / S::n2;
     const int64_t nb = kept_blocks(C);
     ptx::pdl_wait();
     ptx::pdl_trigger();
-    const int64_t b = static_cast<int64_t>(blockIdx.x) * S::tokens + tok;
-    const bool have = b < B && slot < n && in_range(1201, b, 1, B);
-    const int64_t row = b * n + slot;
-    uint2 q;
+    const int64_t b = static_cast<int64_t>(blockIdx.x) * (kDotWarps / W) + warp / W;
+    const bool have = b < B && in_range(1201, b, 1, B);
+    const uint16_t *f_row = dF + b * C;
+    const uint8_t *q_row = Xq + b * n * C, *s_row = Xs + b * n * nb;
+    const int C8 = static_cast<int>(C >> 3);
+    uint2 q[n];
     uint4 f;
-    uint32_t E;
-    const auto load = [&](int64_t cg) {
-        const int64_t c = cg * 32 + t * 8;
-        if (have && cg < nb && c < C && in_range(1202, c, 8, C)) {
-            q = kept::ld_stream_v2(Xq + row * C + c);
-            f = ptx::ld_stream_v4(dF + b * C + c);
-            E = __ldg(Xs + row * nb + cg);
-        } else {
-            q = make_uint2(0, 0);
-            f = make_uint4(0, 0, 0, 0);
-            E = kept::kScaleMin;
+    uint32_t E[n];
+    const auto load = [&](int c8) {
+        const bool in = have && c8 < C8 && in_range(1202, c8 * 8, 8, C);
+        f = in ? ptx::ld_stream_v4(f_row + c8 * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            q[i] = in ? kept::ld_stream_v2(q_row + i * C + c8 * 8) : make_uint2(0, 0);
+            E[i] = in ? __ldg(s_row + i * nb + (c8 >> 2)) : kept::kScaleMin;
         }
     };
-    float s = 0.f;
-    load(warp);
-    for (int64_t cg = warp; cg < nb; cg += kDotWarps) {
-        float x[8], v[8];
-        kept::decode8(q, kept::scale_value(E), x);
-        unpack8(f, v);
-        load(cg + kDotWarps);
+    float s[n];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(x[e], v[e], s);
+    for (int i = 0; i < n; ++i) s[i] = 0.f;
+    const int c0 = (warp % W) * 32 + lane;
+    load(c0);
+    for (int c8 = c0; c8 - lane < C8; c8 += W * 32) {
+        uint64_t v[4], x[4];
+        unpack8_pairs(f, v);
+        float d[n], scale[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            kept::codes8_pairs(q[i], x);
+            uint64_t a = 0;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) a = f2_fma(x[p], v[p], a);
+            float lo, hi;
+            f2_unpack(a, lo, hi);
+            d[i] = lo + hi;
+            scale[i] = kept::scale_value(E[i]);
+        }
+        load(c8 + W * 32);
+#pragma unroll
+        for (int i = 0; i < n; ++i) s[i] = fmaf(d[i], scale[i], s[i]);
     }
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    s += __shfl_xor_sync(0xffffffffu, s, 2);
-    if (t == 0) part[warp][lane >> 2] = s;
-    __syncthreads();
-    if (warp == 0 && have && t == 0) {
-        float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kDotWarps; ++w) sum += part[w][lane >> 2];
-        dH_pre[row] = sum;
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) s[i] += __shfl_xor_sync(0xffffffffu, s[i], x);
+    if constexpr (W == 1) {
+        if (have && lane == 0)
+#pragma unroll
+            for (int i = 0; i < n; ++i) dH_pre[b * n + i] = s[i];
+    } else {
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < n; ++i) part[warp][i] = s[i];
+        __syncthreads();
+        if (have && warp % W == 0 && lane < n) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) sum += part[warp + w][lane];
+            dH_pre[b * n + lane] = sum;
+        }
     }
 }
 
@@ -553,10 +576,12 @@ cudaError_t launch_n(const PreBackwardArgs &a, const Ws &w, int num_sms, cudaStr
     using D = DX<n>;
     constexpr int N = D::N;
     const int64_t Bp = phi_grad_padded_tokens(a.B);
-    const int64_t groups = (a.B + Slots<n>::tokens - 1) / Slots<n>::tokens;
-    cudaError_t e = launch_pdl(dots_kernel<n>, dim3(static_cast<unsigned>(groups)),
-                               dim3(kDotWarps * 32), 0, stream, a.dF_pre, a.Xq, a.Xs, a.B, a.C,
-                               w.dH_pre);
+    // a warp a token once there are tokens for some warps on every SM, else a CTA a token
+    const bool many = a.B >= 16 * static_cast<int64_t>(num_sms);
+    const int64_t dot_ctas = many ? (a.B + kDotWarps - 1) / kDotWarps : a.B;
+    cudaError_t e = launch_pdl(many ? dots_kernel<n, 1> : dots_kernel<n, kDotWarps>,
+                               dim3(static_cast<unsigned>(dot_ctas)), dim3(kDotWarps * 32), 0,
+                               stream, a.dF_pre, a.Xq, a.Xs, a.B, a.C, w.dH_pre);
     if (e != cudaSuccess) return e;
     const CoefOut o{w.dY_rows, w.dY_terms, w.sx, w.part, w.hist};
     static std::atomic<int> per_sm{0};
