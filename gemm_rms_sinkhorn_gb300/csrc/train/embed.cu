@@ -84,6 +84,8 @@ embed_kernel(const T *__restrict__ table, const int64_t *__restrict__ ids, float
 // the sorted positions and their rows, and two rows of sums per chunk.
 struct GradWs {
     int *count, *pos, *row;
+    int *last;    // [chunks]: where the run that starts in a chunk and is cut by its end, ends
+                  // (a chunk), or -1 where there is none
     float *part;  // [chunks][2][C]: the run cut by the chunk's start, then by its end
 };
 
@@ -103,6 +105,8 @@ size_t carve(GradWs &w, void *base, int64_t B, int64_t C)
     at += up(static_cast<size_t>(B) * 4);
     w.row = reinterpret_cast<int *>(p + at);
     at += up(static_cast<size_t>(B) * 4);
+    w.last = reinterpret_cast<int *>(p + at);
+    at += up(static_cast<size_t>(chunks_of(B)) * 4);
     w.part = reinterpret_cast<float *>(p + at);
     at += up(static_cast<size_t>(chunks_of(B)) * 2 * static_cast<size_t>(C) * 4);
     return at;
@@ -164,6 +168,11 @@ embed_sort_kernel(const int64_t *__restrict__ ids, int64_t V, int64_t B, int64_t
     }
     if (r < rows) {
         int at = base + incl - cnt;
+        // this row's positions are [at, at + cnt): each chunk whose end lies among them
+        const int k1 = (at + cnt - 1) / kChunk;
+        for (int k = at / kChunk; cnt > 0 && k <= k1; ++k)
+            if ((k + 1) * static_cast<int64_t>(kChunk) <= at + cnt && in_range(1413, k, 1, chunks_of(B)))
+                ws.last[k] = k == at / kChunk && k < k1 ? k1 : -1;
         for (int w = 0; w < kSortWarps; ++w) {
             const int c = hist[w][r];
             hist[w][r] = at;
@@ -287,16 +296,9 @@ embed_join_kernel(float scale, int accumulate, int64_t V, int64_t B, int64_t C, 
     const int count = *ws.count;
     for (int64_t k = blockIdx.y; (k + 1) * kChunk < count; k += gridDim.y) {
         // the run that chunk k's end cuts, if it starts in chunk k
-        const int first = static_cast<int>(k * kChunk), next = first + kChunk;
-        const int v = ws.row[next - 1];
-        if (ws.row[next] != v) continue;
-        if (ws.row[first] == v && first > 0 && ws.row[first - 1] == v) continue;
-        int lo = next, hi = count;  // the first position after the run
-        while (lo < hi) {
-            const int mid = lo + (hi - lo) / 2;
-            if (ws.row[mid] <= v) lo = mid + 1; else hi = mid;
-        }
-        const int64_t last = (lo - 1) / kChunk;
+        const int64_t last = ws.last[k];
+        if (last < 0) continue;
+        const int v = ws.row[(k + 1) * kChunk];
         if (c8 >= C8 || !in_range(1431, v, 1, V) || !in_range(1432, last, 1, chunks_of(B))) continue;
         float acc[8];
         const float4 *src = reinterpret_cast<const float4 *>(ws.part + (2 * k + 1) * C + c8 * 8);
