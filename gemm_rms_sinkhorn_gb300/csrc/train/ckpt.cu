@@ -138,7 +138,7 @@ ckpt_unpack_kernel(const uint8_t *__restrict__ Xq, const uint8_t *__restrict__ X
         for (int k = 0; k < kRows; ++k)
             if (ok[k])
                 ptx::st_stream_v4(X + (row + k) * C + c8 * 8,
-                                  kept::decode8_bf16(q[k], kept::scale_value(E[k])));
+                                  kept::decode8_bf16(q[k], E[k]));
     }
 }
 

@@ -285,35 +285,69 @@ embed_sum_kernel(const uint16_t *__restrict__ dX, float scale, int accumulate, i
     }
 }
 
-__global__ void __launch_bounds__(256)
+// 32 lanes take 128 columns, and the 8 warps every 8th piece of the run each, so
+// that a run of a thousand positions is a few loads deep; the warps' sums are
+// added in warp order.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinCols = 128;
+
+__global__ void __launch_bounds__(kJoinWarps * 32)
 embed_join_kernel(float scale, int accumulate, int64_t V, int64_t B, int64_t C, GradWs ws,
                   float *__restrict__ dtable)
 {
-    const int64_t C8 = C >> 3;
-    const int64_t c8 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    __shared__ float4 sums[kJoinWarps][32];
+    __shared__ int lasts[kJoinWarps * 32];
+    __shared__ unsigned cut[kJoinWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kJoinCols + lane * 4;
     ptx::pdl_wait();
     ptx::pdl_trigger();
     const int count = *ws.count;
-    for (int64_t k = blockIdx.y; (k + 1) * kChunk < count; k += gridDim.y) {
-        // the run that chunk k's end cuts, if it starts in chunk k
-        const int64_t last = ws.last[k];
-        if (last < 0) continue;
-        const int v = ws.row[(k + 1) * kChunk];
-        if (c8 >= C8 || !in_range(1431, v, 1, V) || !in_range(1432, last, 1, chunks_of(B))) continue;
-        float acc[8];
-        const float4 *src = reinterpret_cast<const float4 *>(ws.part + (2 * k + 1) * C + c8 * 8);
-        float4 a = __ldcs(src), b = __ldcs(src + 1);
-        acc[0] = a.x; acc[1] = a.y; acc[2] = a.z; acc[3] = a.w;
-        acc[4] = b.x; acc[5] = b.y; acc[6] = b.z; acc[7] = b.w;
-#pragma unroll 8
-        for (int64_t kk = k + 1; kk <= last; ++kk) {
-            src = reinterpret_cast<const float4 *>(ws.part + 2 * kk * C + c8 * 8);
-            a = __ldcs(src);
-            b = __ldcs(src + 1);
-            acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
-            acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
-        }
-        put8(dtable + static_cast<int64_t>(v) * C + c8 * 8, acc, scale, accumulate);
+    // a CTA takes every gridDim.y-th chunk; its threads look for the cut runs among them
+    const int64_t chunks = chunks_of(count);
+    for (int64_t k0 = blockIdx.y; k0 < chunks; k0 += static_cast<int64_t>(gridDim.y) * kJoinWarps * 32) {
+        const int64_t mine = k0 + static_cast<int64_t>(threadIdx.x) * gridDim.y;
+        const int l = (mine + 1) * kChunk < count ? ws.last[mine] : -1;
+        const unsigned m = __ballot_sync(0xffffffffu, l >= 0);
+        lasts[threadIdx.x] = l;
+        if (lane == 0) cut[warp] = m;
+        __syncthreads();
+        for (int x = 0; x < kJoinWarps; ++x)
+            for (unsigned left = cut[x]; left != 0; left &= left - 1) {
+                // the run that starts in chunk k and is cut by its end: its piece there, then one
+                // of each chunk up to `last`
+                const int at = x * 32 + __ffs(left) - 1;
+                const int64_t k = k0 + static_cast<int64_t>(at) * gridDim.y, last = lasts[at];
+                const int v = ws.row[(k + 1) * kChunk];
+                const bool ok = c < C && in_range(1431, v, 1, V) && in_range(1432, last, 1, chunks_of(B));
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (ok) {
+#pragma unroll 4
+                    for (int64_t kk = k + warp; kk <= last; kk += kJoinWarps) {
+                        const float4 a = __ldcs(reinterpret_cast<const float4 *>(
+                            ws.part + (2 * kk + (kk == k ? 1 : 0)) * C + c));
+                        s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+                    }
+                }
+                sums[warp][lane] = s;
+                __syncthreads();
+                if (warp == 0 && ok) {
+#pragma unroll
+                    for (int w = 1; w < kJoinWarps; ++w) {
+                        const float4 a = sums[w][lane];
+                        s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+                    }
+                    float4 *d = reinterpret_cast<float4 *>(dtable + v * C + c);
+                    s = make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
+                    if (accumulate) {
+                        const float4 x = *d;
+                        s = make_float4(x.x + s.x, x.y + s.y, x.z + s.z, x.w + s.w);
+                    }
+                    __stcs(d, s);
+                }
+                __syncthreads();
+            }
+        __syncthreads();
     }
 }
 
@@ -380,8 +414,13 @@ cudaError_t launch_embed_backward(const uint16_t *dX, const int64_t *ids, float 
     default: return cudaErrorInvalidValue;
     }
     if (e != cudaSuccess || B <= kChunk) return e;  // one chunk cuts no run
-    return launch_pdl(embed_join_kernel, grid, dim3(threads), 0, stream, scale, accumulate, V, B,
-                      C, ws, dtable);
+    // enough CTAs to fill the GPU once or twice
+    const int64_t strips = (C + kJoinCols - 1) / kJoinCols;
+    const int64_t rows = 16 * num_sms / strips > 1 ? 16 * num_sms / strips : 1;
+    const dim3 join(static_cast<unsigned>(strips),
+                    static_cast<unsigned>(rows < chunks_of(B) ? rows : chunks_of(B)));
+    return launch_pdl(embed_join_kernel, join, dim3(kJoinWarps * 32), 0, stream, scale, accumulate,
+                      V, B, C, ws, dtable);
 }
 
 }  // namespace mhc

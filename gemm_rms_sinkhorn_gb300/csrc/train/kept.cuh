@@ -109,12 +109,16 @@ __device__ __forceinline__ uint4 codes8_bf16(const uint2 &q)
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// The values that eight codes stand for, as bf16 (exact).
-__device__ __forceinline__ uint4 decode8_bf16(const uint2 &q, float scale)
+// The values that eight codes stand for under the scale E, as bf16 (exact: the
+// scale is a power of two, so it may multiply the packed bf16 pairs).
+__device__ __forceinline__ uint4 decode8_bf16(const uint2 &q, uint32_t E)
 {
-    float f[8];
-    decode8(q, scale, f);
-    return pack8(f);
+    const uint4 c = codes8_bf16(q);
+    const uint32_t s = (E << 7) | (E << 23);  // 2^(E - 127) as a bf16 pair
+    uint32_t r[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int p = 0; p < 4; ++p) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r[p]) : "r"(s));
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 __device__ __forceinline__ uint2 ld_stream_v2(const void *p)

@@ -9,13 +9,17 @@
 // of 64 tokens, the (strip, block) units dealt out in equal contiguous ranges,
 // one CTA per SM:
 //
-//   warps 0-7  load codes and scales two units ahead into registers, write the
-//              bf16 values to the stage's A tile and hand it over; after a
-//              strip's last unit they read the accumulators (tcgen05.ld), add
-//              the three terms and store the sums to the workspace;
-//   warp 8     TMA: the dY terms of the block (B tile);
-//   warp 9     tcgen05.mma, M = 128 channels (two accumulators), N = 3n² + 6n
-//              columns padded to 48, K = 16 tokens.
+//   warps 0-15  load codes and scales two units ahead into registers, write the
+//               bf16 values to the stage's A tile and hand it over;
+//   warp 16     TMA: the dY terms of the block (B tile);
+//   warp 17     tcgen05.mma, M = 128 channels (two accumulators), N = 3n² + 6n
+//               columns padded to 48, K = 16 tokens.
+//
+// Every kFlush units the sixteen warps read the accumulators (tcgen05.ld) and
+// add them to fp32 sums in registers; after a strip's last unit the sums go to
+// the workspace.  The accumulator drops what is below its last bit at each step
+// (a bias towards zero: over 16384 tokens in one chain dφ was 9e-6 off, in
+// chains of kFlush · 64 tokens 4e-7), the additions in registers round.
 //
 // Channels are contiguous in the codes, so A is written MN-major: a unit's tile
 // is [4 × 64 channels][8 × 8 tokens], each 64 × 8 part 1 KB with the 128-byte
@@ -23,7 +27,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 
 #include "check.cuh"
@@ -37,7 +40,9 @@ namespace {
 
 constexpr int kStrip = 256;
 constexpr int kTok = kPhiTokens;
-constexpr int kLoadWarps = 8;
+constexpr int kLoadWarps = 16;
+constexpr int kRowsEach = kTok / kLoadWarps;  // tokens of a unit that a load warp takes
+constexpr int kFlush = 16;                    // units in one accumulation chain
 constexpr int kThreads = (kLoadWarps + 2) * 32;
 constexpr int kABytes = kStrip * kTok * 2;  // 32 KB
 constexpr int kStatusTimeout = -5;          // MHC_ERR_TIMEOUT
@@ -47,7 +52,7 @@ __device__ int g_phi_status;
 template <int n>
 struct Cfg {
     static constexpr int N = n * n + 2 * n;
-    static constexpr int NT = (kPhiTerms * N + 47) / 48 * 48;  // columns: three terms × 16 k at a time
+    static constexpr int NT = phi_term_rows(N);  // columns
     static constexpr int kBBytes = NT * kTok * 2;
     static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kStages = n <= 4 ? 4 : 3;
@@ -81,9 +86,9 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead,
     return d;
 }
 
-struct Tile {  // a thread's codes of one unit: 8 channels of 8 tokens
-    uint2 q[8];
-    uint32_t E[8];
+struct Tile {  // a thread's codes of one unit: 8 channels of kRowsEach tokens
+    uint2 q[kRowsEach];
+    uint32_t E[kRowsEach];
 };
 
 template <int n>
@@ -119,7 +124,7 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
         ptx::fence_barrier_init();
         ptx::prefetch_tensormap(&tm_y);
     }
-    if (warp == 9) ptx::tmem_alloc<Cf::kTmemCols>(tmem_holder);
+    if (warp == kLoadWarps + 1) ptx::tmem_alloc<Cf::kTmemCols>(tmem_holder);
     ptx::tc_fence_before();
     __syncwarp();
     __syncthreads();
@@ -135,74 +140,111 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
     };
 
     if (warp < kLoadWarps) {
-        // lane: 8 channels of the strip; warp: tokens warp, warp + 8, ... of the block
-        const auto load = [&](int64_t u, Tile &x) {
-            const int64_t strip = u / un.blocks, b0 = (u - strip * un.blocks) * kTok + warp;
-            const int64_t q = strip * kStrip + lane * 8;
-            const int64_t i = q / C, c = q - i * C;
+        // lane: 8 channels of the strip; warp: tokens warp, warp + 16, ... of the block
+        int64_t l_strip = u0 / un.blocks, l_block = u0 - l_strip * un.blocks, l_u = u0;
+        const uint8_t *l_q = nullptr, *l_E = nullptr;  // of token `warp` of the strip's first block
+        bool l_in = false;
+        const auto enter = [&] {
+            const int64_t q = l_strip * kStrip + lane * 8, i = q / C, c = q - i * C;
+            l_in = q < K;
+            l_q = Xq + warp * K + q;
+            l_E = Xs + (static_cast<int64_t>(warp) * n + i) * nb + (c >> 5);
+        };
+        enter();
+        // the next unit of the CTA's range
+        const auto load = [&](Tile &x) {
+            const bool live = l_u < u1 && l_in;
+            const int64_t b0 = l_block * kTok;
+            const uint8_t *q = l_q + b0 * K, *E = l_E + b0 * n * nb;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t b = b0 + 8 * e;
-                if (u < u1 && q < K && b < B && in_range(1301, b * K + q, 8, B * K)) {
-                    x.q[e] = kept::ld_stream_v2(Xq + b * K + q);
-                    x.E[e] = __ldg(Xs + (b * n + i) * nb + (c >> 5));
-                } else {
-                    x.q[e] = make_uint2(0, 0);
-                    x.E[e] = kept::kScaleMin;
+            for (int e = 0; e < kRowsEach; ++e) {
+                x.q[e] = make_uint2(0, 0);
+                x.E[e] = kept::kScaleMin;
+                if (live && b0 + warp + kLoadWarps * e < B &&
+                    in_range(1301, b0 + warp + kLoadWarps * e, 1, B)) {
+                    x.q[e] = kept::ld_stream_v2(q + kLoadWarps * e * K);
+                    x.E[e] = __ldg(E + kLoadWarps * e * n * nb);
                 }
             }
+            ++l_u;
+            if (++l_block == un.blocks) {
+                l_block = 0;
+                ++l_strip;
+                enter();
+            }
         };
-        const uint32_t at = static_cast<uint32_t>((lane >> 3) * 8192 + warp * 128 +
-                                                  (((lane & 7) ^ warp) << 4));
-        int stage = 0, seg = 0;
+        const uint32_t at = static_cast<uint32_t>((lane >> 3) * 8192 + (warp >> 3) * 1024 +
+                                                  (warp & 7) * 128 + (((lane & 7) ^ (warp & 7)) << 4));
+        // the accumulators' side: channel half·128 + quarter·32 + lane, every other 16 columns
+        const int quarter = warp & 3, half = warp >> 2 & 1, m0 = warp >> 3;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                               static_cast<uint32_t>(half * Cf::NT);
+        constexpr int kM = (Cf::NT / 48 + 1) / 2;  // groups of 16 columns a warp takes, at most
+        float sums[kM][16];
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sums[m][e] = 0.f;
+        int stage = 0, chain = 0, in_chain = 0;
         uint32_t phase = 0;
+        int64_t s_strip = l_strip, s_block = l_block;  // of the unit being stored
         // the tile of one unit into its stage, then the unit after next into x
         const auto step = [&](int64_t u, Tile &x) {
             if (!wait(&empty[stage], phase ^ 1)) return false;
             uint8_t *dst = smem + stage * Cf::kStage + at;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4 *>(dst + e * 1024) =
-                    kept::decode8_bf16(x.q[e], kept::scale_value(x.E[e]));
-            load(u + 2, x);
+            for (int e = 0; e < kRowsEach; ++e)
+                *reinterpret_cast<uint4 *>(dst + e * (kLoadWarps / 8) * 1024) =
+                    kept::decode8_bf16(x.q[e], x.E[e]);
+            load(x);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&full[stage]);
             if (++stage == Cf::kStages) { stage = 0; phase ^= 1; }
-            const int64_t strip = u / un.blocks;
-            if (u + 1 < u1 && (u + 1) / un.blocks == strip) return true;
-            // the strip's (part of the) sum is complete: channel h·128 + 32·quarter + lane
-            if (!wait(acc_full, seg & 1)) return false;
-            ptx::tc_fence_after();
-            const int h = warp >> 2, quarter = warp & 3;
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                   static_cast<uint32_t>(h * Cf::NT);
-            float *dst_p = part + (cta + strip) * static_cast<int64_t>(Cf::N) * kStrip + h * 128 +
-                           quarter * 32 + lane;
-            const bool ok = in_range(1302, cta + strip, 1, un.grid + un.total / un.blocks);
+            const bool last = u + 1 == u1 || s_block + 1 == un.blocks;
+            if (++in_chain == kFlush || last) {
+                in_chain = 0;
+                if (!wait(acc_full, chain & 1)) return false;
+                ++chain;
+                ptx::tc_fence_after();
 #pragma unroll
-            for (int m = 0; m < Cf::NT / 48; ++m) {
-                float v[3][16];
+                for (int m = 0; m < kM; ++m) {
+                    if (2 * m + m0 >= Cf::NT / 48) break;
 #pragma unroll
-                for (int w = 0; w < 3; ++w) ptx::tmem_ld_16(taddr + m * 48 + w * 16, v[w]);
-                ptx::tmem_ld_wait();
+                    for (int w = kPhiTerms - 1; w >= 0; --w) {  // the small terms first
+                        float v[16];
+                        ptx::tmem_ld_16(taddr + (2 * m + m0) * 48 + w * 16, v);
+                        ptx::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (m * 16 + e < Cf::N && ok)
-                        dst_p[(m * 16 + e) * kStrip] =
-                            (v[(3 * e) / 16][(3 * e) % 16] + v[(3 * e + 1) / 16][(3 * e + 1) % 16]) +
-                            v[(3 * e + 2) / 16][(3 * e + 2) % 16];
+                        for (int e = 0; e < 16; ++e) sums[m][e] += v[e];
+                    }
+                }
+                ptx::tc_fence_before();
                 __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(acc_empty);
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(acc_empty);
-            ++seg;
+            if (last) {
+                float *dst_p = part + (cta + s_strip) * static_cast<int64_t>(Cf::N) * kStrip +
+                               half * 128 + quarter * 32 + lane;
+                const bool ok = in_range(1302, cta + s_strip, 1, un.grid + un.total / un.blocks);
+#pragma unroll
+                for (int m = 0; m < kM; ++m)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int k = (2 * m + m0) * 16 + e;
+                        if (k < Cf::N && ok) dst_p[k * kStrip] = sums[m][e];
+                        sums[m][e] = 0.f;
+                    }
+            }
+            if (++s_block == un.blocks) {
+                s_block = 0;
+                ++s_strip;
+            }
             return true;
         };
         Tile x0, x1;
-        load(u0, x0);
-        load(u0 + 1, x1);
+        load(x0);
+        load(x1);
         for (int64_t u = u0; u < u1; u += 2) {
             if (!step(u, x0)) break;
             if (u + 1 < u1 && !step(u + 1, x1)) break;
@@ -235,11 +277,12 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
     } else {
         if (lane == 0) {
             constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, Cf::NT) | (1u << 15);  // A MN-major
-            int stage = 0, seg = 0;
+            int stage = 0, chain = 0, in_chain = 0;
             uint32_t phase = 0;
-            bool ok = true, first = true;
+            bool ok = true;
+            int64_t block = u0 % un.blocks;
             for (int64_t u = u0; u < u1; ++u) {
-                if (first && !(ok = wait(acc_empty, (seg & 1) ^ 1))) break;
+                if (in_chain == 0 && !(ok = wait(acc_empty, (chain & 1) ^ 1))) break;
                 if (!(ok = wait(&full[stage], phase))) break;
                 ptx::tc_fence_after();
                 const uint32_t a = ptx::smem_u32(smem + stage * Cf::kStage);
@@ -250,13 +293,15 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
                     for (int ks = 0; ks < kTok / 16; ++ks)
                         ptx::mma_bf16(tmem + static_cast<uint32_t>(h * Cf::NT),
                                       desc_mn_sw128(a + h * 16384 + ks * 2048, 8192, 1024),
-                                      b_desc + 2 * ks, idesc, first && ks == 0 ? 0u : 1u);
+                                      b_desc + 2 * ks, idesc, in_chain == 0 && ks == 0 ? 0u : 1u);
                 ptx::mma_commit(&empty[stage]);
                 if (++stage == Cf::kStages) { stage = 0; phase ^= 1; }
-                first = u + 1 < u1 && (u + 1) / un.blocks != u / un.blocks;
-                if (first || u + 1 == u1) {
+                const bool last = u + 1 == u1 || block + 1 == un.blocks;
+                if (++block == un.blocks) block = 0;
+                if (++in_chain == kFlush || last) {
+                    in_chain = 0;
+                    ++chain;
                     ptx::mma_commit(acc_full);
-                    ++seg;
                 }
             }
             if (!ok || *abort) {  // every MMA issued has to end before TMEM is freed
@@ -270,7 +315,7 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
     ptx::tc_fence_before();
     __syncthreads();
     ptx::pdl_trigger();
-    if (warp == 9) {
+    if (warp == kLoadWarps + 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc<Cf::kTmemCols>(tmem);
     }
@@ -322,14 +367,13 @@ cudaError_t launch_n(const CUtensorMap &tm, const uint8_t *Xq, const uint8_t *Xs
                      int64_t C, const Units &un, int accumulate, float *dphi_t, float *part,
                      cudaStream_t stream)
 {
-    static std::atomic<bool> set{false};
-    if (!set.load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            phi_grad_kernel<n>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<n>::kSmem);
-        if (e != cudaSuccess) return e;
-        set.store(true, std::memory_order_release);
-    }
-    cudaError_t e = launch_pdl(phi_grad_kernel<n>, dim3(un.grid), dim3(kThreads), Cfg<n>::kSmem,
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t e = once_per_device(configured, [] {
+        return cudaFuncSetAttribute(phi_grad_kernel<n>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<n>::kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(phi_grad_kernel<n>, dim3(un.grid), dim3(kThreads), Cfg<n>::kSmem,
                                stream, tm, Xq, Xs, B, C, un, part, kWaitLimitNs);
     if (e != cudaSuccess) return e;
     const int64_t K = n * C;
@@ -353,9 +397,8 @@ cudaError_t launch_phi_grad(const uint8_t *Xq, const uint8_t *Xs, const uint16_t
     const Units un = make_units(B, n, C, num_sms);
     CUtensorMap tm;
     const int N = num_coeffs(n);
-    const uint32_t box = static_cast<uint32_t>((kPhiTerms * N + 47) / 48 * 48);
-    if (!make_tmap(&tm, dY_terms, static_cast<uint64_t>(phi_grad_padded_tokens(B)),
-                   static_cast<uint64_t>(kPhiTerms * N), box))
+    const uint32_t rows = static_cast<uint32_t>(phi_term_rows(N));
+    if (!make_tmap(&tm, dY_terms, static_cast<uint64_t>(phi_grad_padded_tokens(B)), rows, rows))
         return cudaErrorInvalidValue;
     float *part = static_cast<float *>(workspace);
     switch (n) {

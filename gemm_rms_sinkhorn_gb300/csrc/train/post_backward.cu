@@ -8,20 +8,20 @@
 // (dX = H_resᵀ·G + … is left to the backward of what precedes, which has more
 // to add to it, so G is not mixed and written twice.)
 //
-// One pass over G, the codes and F_out, bound by their bytes.  A CTA takes one
-// group of tokens over all channels.  The lanes of a warp are 8 slots × 4: a
-// slot is one stream of one token (n rounded up to a power of two, so 8, 4, 2
-// or 1 tokens a group), and its four lanes hold 8 neighbouring channels each.
-//   - G·Xᵀ over the slots is an 8 × 8 product per 32 channels: two
-//     mma.m16n8k16 on values that are exact in bf16, accumulated in fp32, with
-//     the slots of X as the rows (the other 8 rows zero) and those of G as the
-//     columns.  What it wastes (rows, pairs of different tokens) costs nothing
-//     here: tcgen05's smallest tile is 128 rows, and per-thread FMAs would take
-//     n² registers of accumulators and as many cross-lane sums at the end.
-//   - dF_out sums over the slots of a token: a butterfly that halves the
-//     channels a lane holds at each step, so 7 shuffles for 8 streams.
-//   - the warps of the CTA take the channel groups in turn, and their sums are
-//     added in warp order at the end: the result does not depend on timing.
+// One pass over G, the codes and F_out, bound by their bytes.  Two forms, both
+// with one or eight warps per token and their sums added in warp order, so that
+// results do not depend on timing:
+//
+//   n <= 4  a lane takes 8 channels of all streams: n² + 2n packed multiply-adds
+//           a channel pair, accumulators in registers.
+//   n >= 5  those would be n² register pairs.  Here a warp takes 32 channels of
+//           all streams, stream g at lanes 4g .. 4g+3, 8 channels a lane, as the
+//           operands of mma.m16n8k16: X's rows and, below them, F_out's against
+//           G's columns give dH_res and dH_post, on values that are exact in
+//           bf16; the block's scale multiplies the product of its 32 channels.
+//           dF_out is a product too, of H_post (three bf16 terms, 2^-26) with G
+//           transposed in registers.  tcgen05's smallest tile is 128 rows and
+//           has its operands in shared memory; this work is 8 rows a token.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -29,86 +29,51 @@
 #include "check.cuh"
 #include "kept.cuh"
 #include "mix.cuh"
+#include "mma.cuh"
 #include "ptx.cuh"
-#include "slots.cuh"
 #include "train.h"
 
 namespace mhc {
 namespace {
 
-// Keeps half of the 2·W values per step, those this lane's slot bit selects,
-// with the other lane's halves added: after log2(n2) steps the sum over the
-// n2 slots of 8/n2 channels is left in v[0 ..], the channels from `off` on.
-template <int n2>
-__device__ __forceinline__ int sum_over_slots(float (&v)[8], int slot)
-{
-    int off = 0;
-#pragma unroll
-    for (int s = 1, w = 4; s < n2; s *= 2, w /= 2) {
-        const bool up = (slot & s) != 0;
-#pragma unroll
-        for (int e = 0; e < w; ++e) {
-            const float give = up ? v[e] : v[w + e];
-            const float keep = up ? v[w + e] : v[e];
-            v[e] = keep + __shfl_xor_sync(0xffffffffu, give, s * 4);
-        }
-        off += up ? w : 0;
-    }
-    return off;
-}
+constexpr int kWarps = 8;
 
-template <int cnt>
-__device__ __forceinline__ void store_vals(uint16_t *p, const float (&v)[8])
-{
-    if constexpr (cnt == 8) {
-        ptx::st_stream_v4(p, pack8(v));
-    } else if constexpr (cnt == 4) {
-        kept::st_stream_v2(p, make_uint2(pack_bf16_rn(v[0], v[1]), pack_bf16_rn(v[2], v[3])));
-    } else if constexpr (cnt == 2) {
-        *reinterpret_cast<uint32_t *>(p) = pack_bf16_rn(v[0], v[1]);
-    } else {
-        *p = static_cast<uint16_t>(pack_bf16_rn(v[0], 0.f));
-    }
-}
-
-template <int cnt>
-__device__ __forceinline__ void store_vals(float *p, const float (&v)[8])
-{
-#pragma unroll
-    for (int e = 0; e < cnt; e += (cnt >= 4 ? 4 : cnt)) {
-        if constexpr (cnt >= 4)
-            *reinterpret_cast<float4 *>(p + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        else if constexpr (cnt == 2)
-            *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
-        else
-            *p = v[0];
-    }
-}
-
-template <typename FT>
-struct FRaw;  // 8 values of F_out as loaded
-template <>
-struct FRaw<uint16_t> {
-    uint4 a;
-    __device__ void load(const uint16_t *p) { a = ptx::ld_stream_v4(p); }
-    __device__ void zero() { a = make_uint4(0, 0, 0, 0); }
-    __device__ void get(float (&f)[8]) const { unpack8(a, f); }
+// Eight values of F_out or dF_out, in bf16 or fp32.
+struct Raw8 {
+    uint4 a, b;  // b: fp32's second half
 };
-template <>
-struct FRaw<float> {
-    uint4 a, b;
-    __device__ void load(const float *p) { a = ptx::ld_stream_v4(p); b = ptx::ld_stream_v4(p + 4); }
-    __device__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
-    __device__ void get(float (&f)[8]) const
-    {
-        f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
-        f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-        f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
-        f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+__device__ __forceinline__ void load_raw(Raw8 &r, const uint16_t *p) { r.a = ptx::ld_stream_v4(p); }
+__device__ __forceinline__ void load_raw(Raw8 &r, const float *p)
+{
+    r.a = ptx::ld_stream_v4(p);
+    r.b = ptx::ld_stream_v4(p + 4);
+}
+__device__ __forceinline__ void raw_pairs(const Raw8 &r, const uint16_t *, uint64_t (&f)[4])
+{
+    unpack8_pairs(r.a, f);
+}
+__device__ __forceinline__ void raw_pairs(const Raw8 &r, const float *, uint64_t (&f)[4])
+{
+    f[0] = (static_cast<uint64_t>(r.a.y) << 32) | r.a.x;
+    f[1] = (static_cast<uint64_t>(r.a.w) << 32) | r.a.z;
+    f[2] = (static_cast<uint64_t>(r.b.y) << 32) | r.b.x;
+    f[3] = (static_cast<uint64_t>(r.b.w) << 32) | r.b.z;
+}
+__device__ __forceinline__ void store8(uint16_t *p, const uint64_t (&v)[4])
+{
+    ptx::st_stream_v4(p, pack8_pairs(v));
+}
+__device__ __forceinline__ void store8(float *p, const uint64_t (&v)[4])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint64_t x = v[2 * h], y = v[2 * h + 1];
+        ptx::st_stream_v4(p + 4 * h, make_uint4(static_cast<uint32_t>(x), static_cast<uint32_t>(x >> 32),
+                                                static_cast<uint32_t>(y), static_cast<uint32_t>(y >> 32)));
     }
-};
+}
 
-template <int n, typename FT, int kWarps>
+template <int n, typename FT, int W>
 __global__ void __launch_bounds__(kWarps * 32)
 post_backward_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *__restrict__ Xq,
                      const uint8_t *__restrict__ Xs, const FT *__restrict__ F_out,
@@ -116,106 +81,213 @@ post_backward_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *__rest
                      FT *__restrict__ dF_out, float *__restrict__ dH_res,
                      float *__restrict__ dH_post)
 {
-    using S = Slots<n>;
-    __shared__ float part[kWarps][3][32];
+    constexpr int kSums = n * n + n;  // dH_res row-major, then dH_post
+    __shared__ float part[kWarps][kSums];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = lane & 3, slot = (lane >> 2) & (S::n2 - 1), tok = (lane >> 2) / S::n2;
-    const int64_t nb = kept_blocks(C), groups = nb;
+    const int64_t nb = kept_blocks(C);
+    const int C8 = static_cast<int>(C >> 3);
     ptx::pdl_wait();
     ptx::pdl_trigger();
-    for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * S::tokens; b0 < B;
-         b0 += static_cast<int64_t>(gridDim.x) * S::tokens) {
-        const int64_t b = b0 + tok;
-        const bool have_tok = b < B && in_range(1101, b, 1, B);
-        const bool have = have_tok && slot < n;
-        const int64_t row = b * n + slot;
-        const uint16_t *g_row = dX_next + row * C;
-        const uint8_t *q_row = Xq + row * C;
-        const uint8_t *s_row = Xs + row * nb;
-        const FT *f_row = F_out + b * C;
-        const float h = have ? __ldg(H_post + row) : 0.f;
+    const int64_t b = static_cast<int64_t>(blockIdx.x) * (kWarps / W) + warp / W;
+    const bool have = b < B && in_range(1101, b, 1, B);
+    const uint16_t *g_row = dX_next + b * n * C;
+    const uint8_t *q_row = Xq + b * n * C, *s_row = Xs + b * n * nb;
+    const FT *f_row = F_out + b * C;
+    float h[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) h[i] = have ? __ldg(H_post + b * n + i) : 0.f;
 
-        uint4 g;
-        uint2 q;
-        uint32_t E;
-        FRaw<FT> fr;
-        const auto load = [&](int64_t cg) {
-            const int64_t c = cg * 32 + t * 8;
-            const bool in = cg < groups && c < C;
-            if (in && have && in_range(1102, c, 8, C)) {
-                g = ptx::ld_stream_v4(g_row + c);
-                q = kept::ld_stream_v2(q_row + c);
-                E = __ldg(s_row + cg);
-                fr.load(f_row + c);
-            } else {
-                g = make_uint4(0, 0, 0, 0);
-                q = make_uint2(0, 0);
-                E = kept::kScaleMin;
-                fr.zero();
-            }
-        };
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        float dpost = 0.f;
-        load(warp);
-        for (int64_t cg = warp; cg < groups; cg += kWarps) {
-            const uint4 x = kept::decode8_bf16(q, kept::scale_value(E));
-            mma_16816(acc, x.x, x.y, g.x, g.y);
-            mma_16816(acc, x.z, x.w, g.z, g.w);
-            float v[8], f[8];
-            unpack8(g, v);
-            fr.get(f);
+    uint64_t acc[n][n], post[n];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dpost = fmaf(v[e], f[e], dpost);
-            load(cg + kWarps);
+    for (int i = 0; i < n; ++i) {
+        post[i] = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= h;
-            const int off = sum_over_slots<S::n2>(v, slot);
-            const int64_t c = cg * 32 + t * 8 + off;
-            if (have_tok && c < C && in_range(1103, c, 8 / S::n2, C))
-                store_vals<8 / S::n2>(dF_out + b * C + c, v);
+        for (int j = 0; j < n; ++j) acc[i][j] = 0;
+    }
+    const int c0 = (warp % W) * 32 + lane;
+    for (int c8 = c0; have && c8 < C8; c8 += W * 32) {
+        if (!in_range(1102, c8 * 8, 8, C)) break;
+        uint4 gv[n];
+        uint2 q[n];
+        uint32_t E[n];
+        Raw8 fr;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            gv[i] = ptx::ld_stream_v4(g_row + i * C + c8 * 8);
+            q[i] = kept::ld_stream_v2(q_row + i * C + c8 * 8);
+            E[i] = __ldg(s_row + i * nb + (c8 >> 2));
         }
-        // over the four lanes of a slot, then over the warps
-        dpost += __shfl_xor_sync(0xffffffffu, dpost, 1);
-        dpost += __shfl_xor_sync(0xffffffffu, dpost, 2);
-        part[warp][0][lane] = acc[0];
-        part[warp][1][lane] = acc[1];
-        part[warp][2][lane] = dpost;
-        __syncthreads();
-        if (warp < 3) {
-            float s = 0.f;
+        load_raw(fr, f_row + c8 * 8);
+        uint64_t g[n][4], f[4], df[4];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += part[w][warp][lane];
-            if (warp == 2) {
-                if (have && t == 0 && in_range(1104, row, 1, B * n)) dH_post[row] = s;
-            } else {
-                // accumulator: row = the X slot of this lane's group, column = a G slot
-                const int col = 2 * t + warp, i = col & (S::n2 - 1);
-                if (have && i < n && col / S::n2 == tok && in_range(1105, (b * n + i) * n + slot, 1, B * n * n))
-                    dH_res[(b * n + i) * n + slot] = s;
+        for (int i = 0; i < n; ++i) unpack8_pairs(gv[i], g[i]);
+        raw_pairs(fr, f_row, f);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) df[p] = 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const uint64_t hh = f2_pack(h[i], h[i]);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                df[p] = f2_fma(hh, g[i][p], df[p]);
+                post[i] = f2_fma(g[i][p], f[p], post[i]);
             }
         }
-        __syncthreads();
+        store8(dF_out + b * C + c8 * 8, df);
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            float x[8];
+            kept::decode8(q[j], kept::scale_value(E[j]), x);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint64_t xp = f2_pack(x[2 * p], x[2 * p + 1]);
+#pragma unroll
+                for (int i = 0; i < n; ++i) acc[i][j] = f2_fma(g[i][p], xp, acc[i][j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) {
+        float lo, hi;
+        f2_unpack(k < n * n ? acc[k / n][k % n] : post[k - n * n], lo, hi);
+        float s = lo + hi;
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
+        if (lane == 0) part[warp][k] = s;
+    }
+    if constexpr (W == 1) __syncwarp(); else __syncthreads();
+    if (!have || warp % W != 0) return;
+    for (int k = lane; k < kSums; k += 32) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) s += part[warp + w][k];
+        if (k < n * n) dH_res[b * n * n + k] = s; else dH_post[b * n + (k - n * n)] = s;
     }
 }
 
-template <typename FT, int kWarps>
-cudaError_t launch_w(const uint16_t *dX_next, const uint8_t *Xq, const uint8_t *Xs,
-                     const FT *F_out, const float *H_post, int64_t B, int n, int64_t C, FT *dF_out,
-                     float *dH_res, float *dH_post, cudaStream_t stream)
+// bf16 terms hi, mid, low of an fp32 value, as the low halves of words.
+__device__ __forceinline__ void split3(float v, uint32_t &hi, uint32_t &mid, uint32_t &low)
 {
-    switch (n) {
-#define MHC_CASE(k)                                                                              \
-    case k: {                                                                                    \
-        const int64_t gs = (B + Slots<k>::tokens - 1) / Slots<k>::tokens;                        \
-        const dim3 grid(static_cast<unsigned>(gs < 0x7fffffff ? gs : 0x7fffffff));               \
-        return launch_pdl(post_backward_kernel<k, FT, kWarps>, grid, dim3(kWarps * 32), 0,       \
-                          stream, dX_next, Xq, Xs, F_out, H_post, B, C, dF_out, dH_res, dH_post); \
+    hi = pack_bf16_rn(v, 0.f);
+    const float r = v - bf16_lo(hi);
+    mid = pack_bf16_rn(r, 0.f);
+    low = pack_bf16_rn(r - bf16_lo(mid), 0.f);
+}
+
+template <int n, typename FT, int W>
+__global__ void __launch_bounds__(kWarps * 32)
+post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *__restrict__ Xq,
+                          const uint8_t *__restrict__ Xs, const FT *__restrict__ F_out,
+                          const float *__restrict__ H_post, int64_t B, int64_t C,
+                          FT *__restrict__ dF_out, float *__restrict__ dH_res,
+                          float *__restrict__ dH_post)
+{
+    constexpr bool kF32 = sizeof(FT) == 4;
+    __shared__ float part[kWarps][4][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;  // stream; 8 channels of a group of 32
+    const int64_t nb = kept_blocks(C);
+    const int groups = static_cast<int>(nb);
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+    const int64_t b = static_cast<int64_t>(blockIdx.x) * (kWarps / W) + warp / W;
+    const bool have_tok = b < B && in_range(1111, b, 1, B);
+    const bool have = have_tok && g < n;
+    const uint16_t *g_row = dX_next + (b * n + g) * C + t * 8;
+    const uint8_t *q_row = Xq + (b * n + g) * C + t * 8, *s_row = Xs + (b * n + g) * nb;
+    const FT *f_row = F_out + b * C + t * 8;
+    FT *df_row = dF_out + b * C + t * 8;
+
+    // H_post as row 0 of a product's left operand: hi at k = 0 .. 7, mid at 8 .. 15; low apart
+    uint32_t h_hi = 0, h_mid = 0, h_low = 0;
+    if (g == 0 && have_tok) {
+        uint32_t a[3], c[3] = {0, 0, 0};
+        split3(2 * t < n ? __ldg(H_post + b * n + 2 * t) : 0.f, a[0], a[1], a[2]);
+        if (2 * t + 1 < n) split3(__ldg(H_post + b * n + 2 * t + 1), c[0], c[1], c[2]);
+        h_hi = __byte_perm(a[0], c[0], 0x5410);
+        h_mid = __byte_perm(a[1], c[1], 0x5410);
+        h_low = __byte_perm(a[2], c[2], 0x5410);
     }
-        MHC_CASE(1) MHC_CASE(2) MHC_CASE(3) MHC_CASE(4) MHC_CASE(5) MHC_CASE(6) MHC_CASE(7)
-        MHC_CASE(8)
-#undef MHC_CASE
-    default: return cudaErrorInvalidValue;
+
+    uint4 gv;
+    uint2 q;
+    uint32_t E;
+    Raw8 fr;
+    const auto load = [&](int cg) {
+        const bool in = cg < groups && cg * 32 + t * 8 < C && in_range(1112, cg * 32 + t * 8, 8, C);
+        gv = in && have ? ptx::ld_stream_v4(g_row + cg * 32) : make_uint4(0, 0, 0, 0);
+        q = in && have ? kept::ld_stream_v2(q_row + cg * 32) : make_uint2(0, 0);
+        // every lane scales its row's sums, also where its own channels are past C
+        E = cg < groups && have ? __ldg(s_row + cg) : kept::kScaleMin;
+        // bf16: F_out is row 8 of the left operand, at lanes 0 .. 3
+        fr.a = fr.b = make_uint4(0, 0, 0, 0);
+        if (in && (kF32 ? have : have_tok && g == 0)) load_raw(fr, f_row + cg * 32);
+    };
+    float acc[2] = {0.f, 0.f}, post[2] = {0.f, 0.f};
+    load((warp % W));
+    for (int cg = warp % W; cg < groups; cg += W) {
+        const uint4 x = kept::codes8_bf16(q);
+        const float scale = kept::scale_value(E);
+        const uint4 gw = gv;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (kF32) {
+            mma_16816(d, x.x, 0u, x.y, 0u, gw.x, gw.y);
+            mma_16816(d, x.z, 0u, x.w, 0u, gw.z, gw.w);
+            uint64_t v[4], f[4], s = 0;
+            unpack8_pairs(gw, v);
+            raw_pairs(fr, f_row, f);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) s = f2_fma(v[p], f[p], s);
+            float lo, hi;
+            f2_unpack(s, lo, hi);
+            post[0] += lo + hi;
+        } else {
+            mma_16816(d, x.x, fr.a.x, x.y, fr.a.y, gw.x, gw.y);
+            mma_16816(d, x.z, fr.a.z, x.w, fr.a.w, gw.z, gw.w);
+            post[0] += d[2];
+            post[1] += d[3];
+        }
+        acc[0] = fmaf(d[0], scale, acc[0]);
+        acc[1] = fmaf(d[1], scale, acc[1]);
+        load(cg + W);
+        // dF_out: word w of the group's lanes, channels 8t + 2w, + 1, transposed
+        const uint32_t word[4] = {gw.x, gw.y, gw.z, gw.w};
+        uint64_t df[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t m = transpose_8x8(word[w]);
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_1688(o, h_low, 0u, m);
+            mma_16816(o, h_hi, 0u, h_mid, 0u, m, m);
+            df[w] = f2_pack(o[0], o[1]);
+        }
+        if (g == 0 && have_tok && cg * 32 + t * 8 < C) store8(df_row + cg * 32, df);
     }
+    if constexpr (kF32) {
+        post[0] += __shfl_xor_sync(0xffffffffu, post[0], 1);
+        post[0] += __shfl_xor_sync(0xffffffffu, post[0], 2);
+    }
+    part[warp][0][lane] = acc[0];
+    part[warp][1][lane] = acc[1];
+    part[warp][2][lane] = post[0];
+    part[warp][3][lane] = post[1];
+    if constexpr (W == 1) __syncwarp(); else __syncthreads();
+    if (!have_tok || warp % W != 0) return;
+    float s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        s[k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) s[k] += part[warp + w][k][lane];
+    }
+    // product rows: X's stream g (dH_res) and F_out (dH_post); columns: G's stream 2t + e
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = 2 * t + e;
+        if (i < n && g < n) dH_res[(b * n + i) * n + g] = s[e];
+        if (!kF32 && i < n && g == 0) dH_post[b * n + i] = s[2 + e];
+    }
+    if (kF32 && t == 0 && g < n) dH_post[b * n + g] = s[2];
 }
 
 }  // namespace
@@ -223,11 +295,29 @@ cudaError_t launch_w(const uint16_t *dX_next, const uint8_t *Xq, const uint8_t *
 template <typename FT>
 cudaError_t launch_post_backward(const uint16_t *dX_next, const uint8_t *Xq, const uint8_t *Xs,
                                  const FT *F_out, const float *H_post, int64_t B, int n, int64_t C,
-                                 FT *dF_out, float *dH_res, float *dH_post, int,
+                                 FT *dF_out, float *dH_res, float *dH_post, int num_sms,
                                  cudaStream_t stream)
 {
-    return launch_w<FT, 8>(dX_next, Xq, Xs, F_out, H_post, B, n, C, dF_out, dH_res, dH_post,
-                           stream);
+    // a warp a token once there are tokens for some warps on every SM, else a CTA a token
+    const bool many = B >= 16 * static_cast<int64_t>(num_sms);
+    const dim3 grid(static_cast<unsigned>(many ? (B + kWarps - 1) / kWarps : B));
+    switch (n) {
+#define MHC_CASE(k, name)                                                                        \
+    case k:                                                                                      \
+        return launch_pdl(many ? name<k, FT, 1> : name<k, FT, kWarps>, grid, dim3(kWarps * 32),  \
+                          0, stream, dX_next, Xq, Xs, F_out, H_post, B, C, dF_out, dH_res,       \
+                          dH_post);
+        MHC_CASE(1, post_backward_kernel)
+        MHC_CASE(2, post_backward_kernel)
+        MHC_CASE(3, post_backward_kernel)
+        MHC_CASE(4, post_backward_kernel)
+        MHC_CASE(5, post_backward_wide_kernel)
+        MHC_CASE(6, post_backward_wide_kernel)
+        MHC_CASE(7, post_backward_wide_kernel)
+        MHC_CASE(8, post_backward_wide_kernel)
+#undef MHC_CASE
+    default: return cudaErrorInvalidValue;
+    }
 }
 template cudaError_t launch_post_backward<uint16_t>(const uint16_t *, const uint8_t *,
                                                     const uint8_t *, const uint16_t *,

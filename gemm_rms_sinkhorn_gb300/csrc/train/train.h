@@ -5,6 +5,7 @@
 // post_backward.cu, 1200s pre_backward.cu, 1300s phi_grad.cu, 1400s embed.cu.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -13,6 +14,20 @@
 #include "mhc_internal.h"
 
 namespace mhc {
+
+// Runs `set` the first time on each device (attributes of kernels are kept per
+// device); the bits of `done` are devices.
+template <typename F>
+cudaError_t once_per_device(std::atomic<uint64_t> &done, F set)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+    if ((e = set()) == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 constexpr int kKeptBlock = 32;  // channels that share a scale
 __host__ __device__ inline int64_t kept_blocks(int64_t C)
@@ -58,11 +73,17 @@ cudaError_t launch_pre_backward(const PreBackwardArgs &a, void *workspace, int n
                                 cudaStream_t stream);
 
 // ---- dφ (phi_grad.cu)
-// dY in three bf16 terms that add up to it (to about 2^-26 of its size), the
-// three terms of column k in rows 3k .. 3k + 2, tokens contiguous and padded
+// dY in three bf16 terms that add up to it (to about 2^-26 of its size): the hi
+// terms of 16 columns in 16 rows, then their mid and low terms, for each 16
+// columns (rows of columns past N hold anything); tokens contiguous and padded
 // with zeros to a multiple of kPhiTokens.
 constexpr int kPhiTerms = 3;
 constexpr int kPhiTokens = 64;
+__host__ __device__ constexpr int phi_term_row(int k, int term)
+{
+    return k / 16 * (16 * kPhiTerms) + term * 16 + k % 16;
+}
+__host__ __device__ constexpr int phi_term_rows(int N) { return (N + 15) / 16 * 16 * kPhiTerms; }
 inline int64_t phi_grad_padded_tokens(int64_t B)
 {
     return (B + kPhiTokens - 1) / kPhiTokens * kPhiTokens;
