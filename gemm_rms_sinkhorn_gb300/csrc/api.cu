@@ -841,11 +841,12 @@ int mhc_testing_check_selftest(void)
 int mhc_device_status(int *status)
 {
     if (status == nullptr) return MHC_ERR_INVALID;
-    int st[6] = {0, 0, 0, 0, 0, 0};
+    int st[7] = {0, 0, 0, 0, 0, 0, 0};
     if (read_and_clear_device_status(&st[0]) != cudaSuccess) return MHC_ERR_CUDA;
     if (read_and_clear_fused_status(&st[1]) != cudaSuccess) return MHC_ERR_CUDA;
     if (read_and_clear_decode_status(&st[2]) != cudaSuccess) return MHC_ERR_CUDA;
     if (read_and_clear_rmsnorm_gemm_status(&st[3]) != cudaSuccess) return MHC_ERR_CUDA;
+    if (read_and_clear_streams_status(&st[6]) != cudaSuccess) return MHC_ERR_CUDA;
     if (read_and_clear_phi_grad_status(&st[5]) != cudaSuccess) return MHC_ERR_CUDA;
     if (kCheckBuild) {
         // the records stay readable through mhc_testing_check_record

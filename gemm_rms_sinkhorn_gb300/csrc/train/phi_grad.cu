@@ -16,10 +16,10 @@
 //               columns padded to 48, K = 16 tokens.
 //
 // Every kFlush units the sixteen warps read the accumulators (tcgen05.ld) and
-// add them to fp32 sums in registers; after a strip's last unit the sums go to
-// the workspace.  The accumulator drops what is below its last bit at each step
-// (a bias towards zero: over 16384 tokens in one chain dφ was 9e-6 off, in
-// chains of kFlush · 64 tokens 4e-7), the additions in registers round.
+// add them to the workspace's fp32 sums, each value always by the same thread,
+// so in a fixed order.  The accumulator drops what is below its last bit at each
+// step (a bias towards zero: over 16384 tokens in one chain dφ was 9.1e-6 off,
+// in chains of kFlush · 64 tokens 7e-7); these additions round.
 //
 // Channels are contiguous in the codes, so A is written MN-major: a unit's tile
 // is [4 × 64 channels][8 × 8 tokens], each 64 × 8 part 1 KB with the 128-byte
@@ -141,33 +141,43 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
 
     if (warp < kLoadWarps) {
         // lane: 8 channels of the strip; warp: tokens warp, warp + 16, ... of the block
-        int64_t l_strip = u0 / un.blocks, l_block = u0 - l_strip * un.blocks, l_u = u0;
-        const uint8_t *l_q = nullptr, *l_E = nullptr;  // of token `warp` of the strip's first block
+        const int blocks = static_cast<int>(un.blocks);
+        const int64_t row_q = kLoadWarps * K, row_E = kLoadWarps * n * nb;  // to its next token
+        int l_block = static_cast<int>(u0 % un.blocks);
+        int64_t l_strip = u0 / un.blocks, l_left = u1 - u0;
+        const uint8_t *l_q = nullptr, *l_E = nullptr;  // of its first token of the next unit
         bool l_in = false;
         const auto enter = [&] {
             const int64_t q = l_strip * kStrip + lane * 8, i = q / C, c = q - i * C;
+            const int64_t b = static_cast<int64_t>(l_block) * kTok + warp;
             l_in = q < K;
-            l_q = Xq + warp * K + q;
-            l_E = Xs + (static_cast<int64_t>(warp) * n + i) * nb + (c >> 5);
+            l_q = Xq + b * K + q;
+            l_E = Xs + (b * n + i) * nb + (c >> 5);
         };
         enter();
         // the next unit of the CTA's range
         const auto load = [&](Tile &x) {
-            const bool live = l_u < u1 && l_in;
-            const int64_t b0 = l_block * kTok;
-            const uint8_t *q = l_q + b0 * K, *E = l_E + b0 * n * nb;
+            const uint8_t *q = l_q, *E = l_E;
+            const int64_t rows = B - static_cast<int64_t>(l_block) * kTok;
+            if (l_left > 0 && l_in && rows >= kTok && in_range(1301, l_q - Xq, 8, B * K)) {
 #pragma unroll
-            for (int e = 0; e < kRowsEach; ++e) {
-                x.q[e] = make_uint2(0, 0);
-                x.E[e] = kept::kScaleMin;
-                if (live && b0 + warp + kLoadWarps * e < B &&
-                    in_range(1301, b0 + warp + kLoadWarps * e, 1, B)) {
-                    x.q[e] = kept::ld_stream_v2(q + kLoadWarps * e * K);
-                    x.E[e] = __ldg(E + kLoadWarps * e * n * nb);
+                for (int e = 0; e < kRowsEach; ++e, q += row_q, E += row_E) {
+                    x.q[e] = kept::ld_stream_v2(q);
+                    x.E[e] = __ldg(E);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < kRowsEach; ++e, q += row_q, E += row_E) {
+                    const bool ok = l_left > 0 && l_in && warp + kLoadWarps * e < rows &&
+                                    in_range(1303, q - Xq, 8, B * K);
+                    x.q[e] = ok ? kept::ld_stream_v2(q) : make_uint2(0, 0);
+                    x.E[e] = ok ? __ldg(E) : kept::kScaleMin;
                 }
             }
-            ++l_u;
-            if (++l_block == un.blocks) {
+            --l_left;
+            l_q = q;
+            l_E = E;
+            if (++l_block == blocks) {
                 l_block = 0;
                 ++l_strip;
                 enter();
@@ -179,18 +189,15 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
         const int quarter = warp & 3, half = warp >> 2 & 1, m0 = warp >> 3;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                static_cast<uint32_t>(half * Cf::NT);
-        constexpr int kM = (Cf::NT / 48 + 1) / 2;  // groups of 16 columns a warp takes, at most
-        float sums[kM][16];
-#pragma unroll
-        for (int m = 0; m < kM; ++m)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) sums[m][e] = 0.f;
         int stage = 0, chain = 0, in_chain = 0;
         uint32_t phase = 0;
-        int64_t s_strip = l_strip, s_block = l_block;  // of the unit being stored
+        int64_t s_strip = l_strip;  // of the unit being stored
+        int s_block = l_block;
+        bool fresh = true;  // no chain of this strip has been stored
         // the tile of one unit into its stage, then the unit after next into x
-        const auto step = [&](int64_t u, Tile &x) {
-            if (!wait(&empty[stage], phase ^ 1)) return false;
+        const auto step = [&](bool end, Tile &x) {
+            // (warp-uniform: the loads of the accumulators are warp-collective)
+            if (!__all_sync(0xffffffffu, wait(&empty[stage], phase ^ 1))) return false;
             uint8_t *dst = smem + stage * Cf::kStage + at;
 #pragma unroll
             for (int e = 0; e < kRowsEach; ++e)
@@ -201,42 +208,41 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&full[stage]);
             if (++stage == Cf::kStages) { stage = 0; phase ^= 1; }
-            const bool last = u + 1 == u1 || s_block + 1 == un.blocks;
+            const bool last = end || s_block + 1 == blocks;
             if (++in_chain == kFlush || last) {
                 in_chain = 0;
-                if (!wait(acc_full, chain & 1)) return false;
+                if (!__all_sync(0xffffffffu, wait(acc_full, chain & 1))) return false;
                 ++chain;
                 ptx::tc_fence_after();
+                float *dst_p = part + (cta + s_strip) * static_cast<int64_t>(Cf::N) * kStrip +
+                               half * 128 + quarter * 32 + lane;
+                const bool ok = in_range(1302, cta + s_strip, 1, un.grid + un.total / un.blocks);
+#pragma unroll 1
+                for (int m = m0; m < Cf::NT / 48; m += 2) {
+                    float s[16], v[16];
+                    ptx::tmem_ld_16(taddr + m * 48 + 32, s);  // the low terms first
+                    ptx::tmem_ld_16(taddr + m * 48 + 16, v);
+                    ptx::tmem_ld_wait();
 #pragma unroll
-                for (int m = 0; m < kM; ++m) {
-                    if (2 * m + m0 >= Cf::NT / 48) break;
+                    for (int e = 0; e < 16; ++e) s[e] += v[e];
+                    ptx::tmem_ld_16(taddr + m * 48, v);
+                    ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int w = kPhiTerms - 1; w >= 0; --w) {  // the small terms first
-                        float v[16];
-                        ptx::tmem_ld_16(taddr + (2 * m + m0) * 48 + w * 16, v);
-                        ptx::tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) sums[m][e] += v[e];
+                    for (int e = 0; e < 16; ++e) {
+                        const int k = m * 16 + e;
+                        if (k >= Cf::N || !ok) break;
+                        // this thread alone writes the value, in the order of the chains
+                        if (fresh) dst_p[k * kStrip] = s[e] + v[e];
+                        else atomicAdd(dst_p + k * kStrip, s[e] + v[e]);
                     }
+                    __syncwarp();
                 }
+                fresh = last;
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(acc_empty);
             }
-            if (last) {
-                float *dst_p = part + (cta + s_strip) * static_cast<int64_t>(Cf::N) * kStrip +
-                               half * 128 + quarter * 32 + lane;
-                const bool ok = in_range(1302, cta + s_strip, 1, un.grid + un.total / un.blocks);
-#pragma unroll
-                for (int m = 0; m < kM; ++m)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int k = (2 * m + m0) * 16 + e;
-                        if (k < Cf::N && ok) dst_p[k * kStrip] = sums[m][e];
-                        sums[m][e] = 0.f;
-                    }
-            }
-            if (++s_block == un.blocks) {
+            if (++s_block == blocks) {
                 s_block = 0;
                 ++s_strip;
             }
@@ -245,9 +251,9 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
         Tile x0, x1;
         load(x0);
         load(x1);
-        for (int64_t u = u0; u < u1; u += 2) {
-            if (!step(u, x0)) break;
-            if (u + 1 < u1 && !step(u + 1, x1)) break;
+        for (int64_t left = u1 - u0; left > 0; left -= 2) {
+            if (!step(left == 1, x0)) break;
+            if (left > 1 && !step(left == 2, x1)) break;
         }
     } else if (warp == kLoadWarps) {
         if (lane == 0) {

@@ -37,6 +37,7 @@ namespace mhc {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kDepth = 4;  // channel groups that a warp of the n >= 5 form has in flight
 
 // Eight values of F_out or dF_out, in bf16 or fp32.
 struct Raw8 {
@@ -209,37 +210,41 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
         h_low = __byte_perm(a[2], c[2], 0x5410);
     }
 
-    uint4 gv;
-    uint2 q;
-    uint32_t E;
-    Raw8 fr;
-    const auto load = [&](int cg) {
+    // kDepth groups are in flight: a slot is loaded again as soon as it is used
+    struct Slot {
+        uint4 g;
+        uint2 q;
+        uint32_t E;
+        Raw8 f;
+    } slots[kDepth];
+    const auto load = [&](Slot &x, int cg) {
         const bool in = cg < groups && cg * 32 + t * 8 < C && in_range(1112, cg * 32 + t * 8, 8, C);
-        gv = in && have ? ptx::ld_stream_v4(g_row + cg * 32) : make_uint4(0, 0, 0, 0);
-        q = in && have ? kept::ld_stream_v2(q_row + cg * 32) : make_uint2(0, 0);
+        x.g = in && have ? ptx::ld_stream_v4(g_row + cg * 32) : make_uint4(0, 0, 0, 0);
+        x.q = in && have ? kept::ld_stream_v2(q_row + cg * 32) : make_uint2(0, 0);
         // every lane scales its row's sums, also where its own channels are past C
-        E = cg < groups && have ? __ldg(s_row + cg) : kept::kScaleMin;
+        x.E = cg < groups && have ? __ldg(s_row + cg) : kept::kScaleMin;
         // bf16: F_out is row 8 of the left operand, at lanes 0 .. 3
-        fr.a = fr.b = make_uint4(0, 0, 0, 0);
-        if (in && (kF32 ? have : have_tok && g == 0)) load_raw(fr, f_row + cg * 32);
+        x.f.a = x.f.b = make_uint4(0, 0, 0, 0);
+        if (in && (kF32 ? have : have_tok && g == 0)) load_raw(x.f, f_row + cg * 32);
     };
     float acc[2] = {0.f, 0.f}, post[2] = {0.f, 0.f};
-    load((warp % W));
-    for (int cg = warp % W; cg < groups; cg += W) {
-        const uint4 x = kept::codes8_bf16(q);
-        const float scale = kept::scale_value(E);
-        const uint4 gw = gv;
+    const auto use = [&](Slot &s, int cg) {
+        const uint4 x = kept::codes8_bf16(s.q);
+        const float scale = kept::scale_value(s.E);
+        const uint4 gw = s.g;
+        const Raw8 fr = s.f;
+        load(s, cg + kDepth * W);
         float d[4] = {0.f, 0.f, 0.f, 0.f};
         if constexpr (kF32) {
             mma_16816(d, x.x, 0u, x.y, 0u, gw.x, gw.y);
             mma_16816(d, x.z, 0u, x.w, 0u, gw.z, gw.w);
-            uint64_t v[4], f[4], s = 0;
+            uint64_t v[4], f[4], a = 0;
             unpack8_pairs(gw, v);
             raw_pairs(fr, f_row, f);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) s = f2_fma(v[p], f[p], s);
+            for (int p = 0; p < 4; ++p) a = f2_fma(v[p], f[p], a);
             float lo, hi;
-            f2_unpack(s, lo, hi);
+            f2_unpack(a, lo, hi);
             post[0] += lo + hi;
         } else {
             mma_16816(d, x.x, fr.a.x, x.y, fr.a.y, gw.x, gw.y);
@@ -249,7 +254,6 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
         }
         acc[0] = fmaf(d[0], scale, acc[0]);
         acc[1] = fmaf(d[1], scale, acc[1]);
-        load(cg + W);
         // dF_out: word w of the group's lanes, channels 8t + 2w, + 1, transposed
         const uint32_t word[4] = {gw.x, gw.y, gw.z, gw.w};
         uint64_t df[4];
@@ -261,8 +265,13 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
             mma_16816(o, h_hi, 0u, h_mid, 0u, m, m);
             df[w] = f2_pack(o[0], o[1]);
         }
-        if (g == 0 && have_tok && cg * 32 + t * 8 < C) store8(df_row + cg * 32, df);
-    }
+        if (g == 0 && have_tok && cg < groups && cg * 32 + t * 8 < C) store8(df_row + cg * 32, df);
+    };
+#pragma unroll
+    for (int x = 0; x < kDepth; ++x) load(slots[x], warp % W + x * W);
+    for (int cg = warp % W; cg < groups; cg += kDepth * W)
+#pragma unroll
+        for (int x = 0; x < kDepth; ++x) use(slots[x], cg + x * W);
     if constexpr (kF32) {
         post[0] += __shfl_xor_sync(0xffffffffu, post[0], 1);
         post[0] += __shfl_xor_sync(0xffffffffu, post[0], 2);

@@ -11,6 +11,7 @@
 //           dbias = Σ_b dH̃,  dα_seg = Σ_b Σ_{k in seg} dH̃·Y/r
 //           dY = α·dH̃/r,     s = −Σ_k dY·Y/(K·r²)       (r = sqrt(Σx²/K))
 //   streams dX[j] = Σ_i H_res[i][j]·G[i] + H_pre[j]·dF + Σ_k dY[k]·φ[k] + s·X[j]
+//           (streams.cu)
 //   phi     dφ_t[k] = Σ_b dY[b][k]·X[b]                  (phi_grad.cu)
 //
 // The sum over all channels in `dots` stands between F's gradient and dX, so
@@ -34,7 +35,6 @@
 #include "check.cuh"
 #include "kept.cuh"
 #include "mix.cuh"
-#include "mma.cuh"
 #include "ptx.cuh"
 #include "train.h"
 
@@ -48,11 +48,39 @@ namespace {
 // values.  W warps share a token.
 constexpr int kDotWarps = 8;
 
+//
+// The CTAs past the tokens' lay φ_t [N][K] out for the product dY·φ (train.h).
 template <int n, int W>
 __global__ void __launch_bounds__(kDotWarps * 32)
 dots_kernel(const uint16_t *__restrict__ dF, const uint8_t *__restrict__ Xq,
-            const uint8_t *__restrict__ Xs, int64_t B, int64_t C, float *__restrict__ dH_pre)
+            const uint8_t *__restrict__ Xs, const uint16_t *__restrict__ phi_t, int64_t B,
+            int64_t C, unsigned dot_ctas, float *__restrict__ dH_pre,
+            uint8_t *__restrict__ phi_img)
 {
+    if (blockIdx.x >= dot_ctas) {
+        constexpr int N = n * n + 2 * n, kCols = dy_cols(n);
+        const int64_t K = n * C;
+        const int64_t q = static_cast<int64_t>(blockIdx.x - dot_ctas) * (kDotWarps * 32) + threadIdx.x;
+        ptx::pdl_wait();
+        ptx::pdl_trigger();
+        if (q >= K || !in_range(1203, q, 1, K)) return;
+        constexpr int W = streams_width(n), RB = phi_image_row(n);
+        const int64_t j = q / C, c = q - j * C;
+        const int row = static_cast<int>(j) * W + static_cast<int>(c % W);
+        uint8_t *img = phi_img + c / W * phi_image_bytes(n);
+#pragma unroll
+        for (int k8 = 0; k8 < kCols / 8; ++k8) {
+            uint32_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = k8 * 8 + e < N ? __ldg(phi_t + (k8 * 8 + e) * K + q) : 0u;
+            uint8_t *dst = k8 * 16 < RB ? img + row * RB + (k8 ^ swizzle_xor(RB, row)) * 16
+                                        : img + n * W * RB + row * 32 +
+                                              ((k8 - RB / 16) ^ swizzle_xor(32, row)) * 16;
+            *reinterpret_cast<uint4 *>(dst) =
+                make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        }
+        return;
+    }
     __shared__ float part[kDotWarps][n];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t nb = kept_blocks(C);
@@ -127,16 +155,9 @@ constexpr int kCoefThreads = 64;
 constexpr int kCoefWarps = kCoefThreads / 32;
 constexpr int kHistSmem = 96 * 1024;  // u_t and v_t of a CTA's tokens, where they fit
 
-// k of the product dY·φ, padded to the tensor instruction's 16
-__host__ __device__ constexpr int dy_cols(int n) { return (n * n + 2 * n + 15) / 16 * 16; }
-// what mixes a token's streams: H_resᵀ [j][i], H_pre[j], s
-__host__ __device__ constexpr int mix_vals(int n) { return n * n + n + 1; }
-
-// What coefs hands to streams is laid out by tiles of 16 tokens, as the lanes of
-// streams read it: lane (g, t) works on tokens g and g + 8.
 struct CoefOut {
-    float *mix;          // [tiles][mix_vals][8 g][2]
-    uint32_t *dY_frag;   // [tiles][dy_cols / 16][32 lanes][4]: the left operand, bf16 pairs
+    float *mix;          // [mix_vals][padded tokens] (train.h)
+    uint16_t *dY_rows;   // [padded tokens][dy_cols] bf16, zeros past N
     uint16_t *dY_terms;  // bf16 terms of dY (train.h)
     float *part;         // [CTAs][N + 3]: Σ dH̃ by column, then by α
     float *hist;         // [CTAs][iters][2n][threads], or NULL: in shared memory
@@ -265,17 +286,15 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
                 for (int j = 0; j < n; ++j) A[i][j] = dA[i][j] = 0.f;
         }
 
-        const int64_t tile = b >> 4;
-        const int g = static_cast<int>(b & 7), upper = static_cast<int>(b >> 3 & 1);
-        float *mix = o.mix + (tile * mix_vals(n) * 8 + g) * 2 + upper;
-        uint32_t *frag = o.dY_frag + tile * (kCols / 16) * 128 + g * 16 + upper;
+        float *mix = o.mix + b;
+        uint32_t *row = reinterpret_cast<uint32_t *>(o.dY_rows + b * kCols);
         const bool in = b < Bp && in_range(1212, b, 1, Bp);
         if (in) {
 #pragma unroll
             for (int i = 0; i < n; ++i)
 #pragma unroll
                 for (int j = 0; j < n; ++j)
-                    mix[(j * n + i) * 16] = live ? __ldg(a.H_res + (b * n + i) * n + j) : 0.f;
+                    mix[(j * n + i) * Bp] = live ? __ldg(a.H_res + (b * n + i) * n + j) : 0.f;
         }
         float sx = 0.f, da[3] = {0.f, 0.f, 0.f};
         uint32_t packed = 0;
@@ -285,7 +304,7 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
             if (k < n) {
                 if (live) {
                     const float h = __ldg(a.H_pre + b * n + k);
-                    mix[(n * n + k) * 16] = h;
+                    mix[(n * n + k) * Bp] = h;
                     d = __ldg(dH_pre + b * n + k) * h * (1.0f - h);
                 }
             } else if (k < 2 * n) {
@@ -318,15 +337,12 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
                 dst[32 * Bp] = static_cast<uint16_t>(low);
             }
             if (k % 2 == 0) packed = hi;
-            if ((k % 2 == 1 || k + 1 == N) && in)
-                frag[(k / 16) * 128 + (k % 8 / 2) * 4 + (k % 16 / 8) * 2] =
-                    k % 2 == 1 ? packed | (hi << 16) : packed;
+            if ((k % 2 == 1 || k + 1 == N) && in) row[k / 2] = k % 2 == 1 ? packed | (hi << 16) : packed;
         }
         if (in) {
 #pragma unroll
-            for (int k = (N + 1) / 2 * 2; k < kCols; k += 2)
-                frag[(k / 16) * 128 + (k % 8 / 2) * 4 + (k % 16 / 8) * 2] = 0;
-            mix[(n * n + n) * 16] = sx * inv_r * inv_r * inv_K;
+            for (int k = (N + 1) / 2; k < kCols / 2; ++k) row[k] = 0;
+            mix[(n * n + n) * Bp] = sx * inv_r * inv_r * inv_K;
         }
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
@@ -362,197 +378,12 @@ bias_join_kernel(const float *__restrict__ part, int ctas, int N, int accumulate
     *dst = accumulate ? *dst + s : s;
 }
 
-// --------------------------------------------------------------- streams
-//
-// Bound by memory (G, the codes and dF in, dX out).  A CTA holds φ for a strip
-// of channels in shared memory, in the order of the tensor product's operand,
-// and walks the tokens; a warp mixes 16 tokens × 32 channels of all streams.
-// dY·φ runs as mma.m16n8k16 (16 tokens, N padded to 16 as k) into the very
-// registers in which the other terms are added: with the four column tiles of a
-// warp taken as channels 8t + 2q, 8t + 2q + 1 (t: lane, q: tile), a lane ends up
-// with 8 neighbouring channels of two tokens, its 128-bit accesses.  The product
-// is a rank-N update of a streamed matrix; tcgen05 would bring it through TMEM
-// and shared memory to where these lanes have it already.
-//
-// The warps of a CTA run free of each other (a barrier only where the strip
-// changes), so that some wait for their loads while others compute; a barrier a
-// step had them all wait, then all compute (B=16384, n=4, C=7168: 640 us).
-
-template <int n>
-struct DX {
-    static constexpr int N = n * n + 2 * n;
-    static constexpr int kCols = dy_cols(n);
-    static constexpr int KS = kCols / 16;
-    static constexpr int kWarps = n <= 2 ? 16 : n <= 4 ? 12 : 8;  // 128, 168, 255 registers
-    static constexpr int CG = n <= 2 ? 8 : n <= 6 ? 4 : 2;  // groups of 32 channels in a strip
-    static constexpr int S = CG * 32;
-    static constexpr int TS = kWarps / CG * 16;             // tokens of a step
-    static constexpr int P = mix_vals(n);
-    static constexpr int J = n <= 1 ? 1 : 2;                // streams of dX formed together
-    static constexpr int kPhiBytes = n * CG * KS * 2 * 32 * 16;
-};
-
-// φ of a strip to shared memory: two rows k, k + 1 of 8 channels at a time.
-// Lane (gg, tk) of k step ks reads, for column tile q, k = 16·ks + 2·tk (+1, +8,
-// +9) at channel 8·(gg / 2) + 2q + gg % 2.
-template <int n>
-__device__ __forceinline__ void load_phi(const uint16_t *phi_t, int64_t strip, int64_t C,
-                                         uint32_t *phi_s)
-{
-    using D = DX<n>;
-    constexpr int kPairs = D::kCols / 2, kOct = D::S / 8;
-    const int64_t K = n * C;
-    for (int x = threadIdx.x; x < n * kPairs * kOct; x += D::kWarps * 32) {
-        const int oct = x % kOct, pair = x / kOct % kPairs, j = x / (kOct * kPairs);
-        const int64_t c = strip * D::S + oct * 8;
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-        if (c < C && in_range(1222, c, 8, C)) {
-            const uint16_t *src = phi_t + 2 * pair * K + j * C + c;
-            if (2 * pair < D::N) lo = __ldg(reinterpret_cast<const uint4 *>(src));
-            if (2 * pair + 1 < D::N) hi = __ldg(reinterpret_cast<const uint4 *>(src + K));
-        }
-        const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
-        const int ks = pair / 8, half = pair % 8 / 4, tk = pair % 4, toct = oct % 4;
-        uint32_t *dst = phi_s + (((j * D::CG + oct / 4) * D::KS + ks) * 2) * 128;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t *d = dst + (q / 2) * 128 + (q % 2) * 2 + half;
-            d[((2 * toct) * 4 + tk) * 4] = __byte_perm(l[q], h[q], 0x5410);
-            d[((2 * toct + 1) * 4 + tk) * 4] = __byte_perm(l[q], h[q], 0x7632);
-        }
-    }
-}
-
-template <int n>
-__global__ void __launch_bounds__(DX<n>::kWarps * 32, 1)
-streams_kernel(const uint16_t *dX_next, const uint16_t *__restrict__ dF,
-               const uint8_t *__restrict__ Xq, const uint8_t *__restrict__ Xs,
-               const uint16_t *__restrict__ phi_t, const float *__restrict__ mix,
-               const uint32_t *__restrict__ dY_frag, int64_t B, int64_t C, int64_t steps,
-               int64_t units, uint16_t *dX)
-{
-    using D = DX<n>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    const uint4 *phi_s = reinterpret_cast<const uint4 *>(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, t = lane & 3;
-    const int cg = warp % D::CG, tt = warp / D::CG;
-    const int64_t nb = kept_blocks(C);
-    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-    // φ was there before the call: the kernels before this one do not write it, and
-    // they let this one start only when what preceded the call had finished
-    int64_t strip = u0 / steps, step = u0 - strip * steps;
-    load_phi<n>(phi_t, strip, C, reinterpret_cast<uint32_t *>(smem));
-    ptx::pdl_wait();
-    ptx::pdl_trigger();
-    __syncthreads();
-
-    for (int64_t u = u0; u < u1; ++u, ++step) {
-        if (step == steps) {
-            step = 0;
-            ++strip;
-            __syncthreads();
-            load_phi<n>(phi_t, strip, C, reinterpret_cast<uint32_t *>(smem));
-            __syncthreads();
-        }
-        const int64_t b0 = step * D::TS + tt * 16;
-        if (b0 >= B) continue;
-        const int64_t c = strip * D::S + cg * 32 + t * 8;
-        const bool okc = c < C && in_range(1223, c, 8, C);
-        const int64_t bb[2] = {b0 + g, b0 + g + 8};
-        const bool ok[2] = {okc && bb[0] < B, okc && bb[1] < B && in_range(1224, bb[1], 1, B)};
-        uint4 gv[2][n], fv[2];
-        uint2 q[2][n];
-        uint32_t E[2][n];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint16_t *gp = dX_next + bb[h] * n * C + c;
-            const uint8_t *qp = Xq + bb[h] * n * C + c, *ep = Xs + bb[h] * n * nb + (c >> 5);
-#pragma unroll
-            for (int i = 0; i < n; ++i) gv[h][i] = ok[h] ? ptx::ld_stream_v4(gp + i * C) : make_uint4(0, 0, 0, 0);
-            fv[h] = ok[h] ? ptx::ld_stream_v4(dF + bb[h] * C + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < n; ++i) {
-                q[h][i] = ok[h] ? kept::ld_stream_v2(qp + i * C) : make_uint2(0, 0);
-                E[h][i] = ok[h] ? __ldg(ep + i * nb) : kept::kScaleMin;
-            }
-        }
-        const int64_t tile = b0 >> 4;
-        const uint4 *frag = reinterpret_cast<const uint4 *>(dY_frag) + tile * D::KS * 32 + lane;
-        const float2 *mx = reinterpret_cast<const float2 *>(mix) + tile * D::P * 8 + g;
-        const float2 s2 = __ldg(mx + (n * n + n) * 8);
-#pragma unroll
-        for (int j0 = 0; j0 < n; j0 += D::J) {
-            float d[D::J][4][4];
-#pragma unroll
-            for (int jj = 0; jj < D::J; ++jj)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) d[jj][x][0] = d[jj][x][1] = d[jj][x][2] = d[jj][x][3] = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < D::KS; ++ks) {
-                const uint4 y = __ldg(frag + ks * 32);
-#pragma unroll
-                for (int jj = 0; jj < D::J; ++jj) {
-                    if (j0 + jj >= n) break;
-                    const uint4 *ph = phi_s + (((j0 + jj) * D::CG + cg) * D::KS + ks) * 64 + lane;
-                    const uint4 p0 = ph[0], p1 = ph[32];
-                    mma_16816(d[jj][0], y.x, y.y, y.z, y.w, p0.x, p0.y);
-                    mma_16816(d[jj][1], y.x, y.y, y.z, y.w, p0.z, p0.w);
-                    mma_16816(d[jj][2], y.x, y.y, y.z, y.w, p1.x, p1.y);
-                    mma_16816(d[jj][3], y.x, y.y, y.z, y.w, p1.z, p1.w);
-                }
-            }
-            uint64_t acc[D::J][2][4], w[4];
-#pragma unroll
-            for (int jj = 0; jj < D::J; ++jj)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) acc[jj][h][x] = f2_pack(d[jj][x][2 * h], d[jj][x][2 * h + 1]);
-#pragma unroll
-            for (int i = 0; i <= n; ++i) {  // the streams of G, then dF
-                float2 co[D::J];
-#pragma unroll
-                for (int jj = 0; jj < D::J; ++jj)
-                    if (j0 + jj < n) co[jj] = __ldg(mx + (i < n ? (j0 + jj) * n + i : n * n + j0 + jj) * 8);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    unpack8_pairs(i < n ? gv[h][i < n ? i : 0] : fv[h], w);
-#pragma unroll
-                    for (int jj = 0; jj < D::J; ++jj) {
-                        if (j0 + jj >= n) break;
-                        const float v = h == 0 ? co[jj].x : co[jj].y;
-                        const uint64_t vv = f2_pack(v, v);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) acc[jj][h][x] = f2_fma(vv, w[x], acc[jj][h][x]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int jj = 0; jj < D::J; ++jj) {
-                const int j = j0 + jj;
-                if (j >= n) break;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // s·X: s and the block's scale first, then the codes
-                    const float v = (h == 0 ? s2.x : s2.y) * kept::scale_value(E[h][j]);
-                    const uint64_t vv = f2_pack(v, v);
-                    kept::codes8_pairs(q[h][j], w);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) acc[jj][h][x] = f2_fma(vv, w[x], acc[jj][h][x]);
-                    if (ok[h]) ptx::st_stream_v4(dX + (bb[h] * n + j) * C + c, pack8_pairs(acc[jj][h]));
-                }
-            }
-        }
-    }
-}
-
 // -------------------------------------------------------------- launches
 
 struct Ws {
     float *dH_pre, *mix, *part, *hist;
-    uint32_t *dY_frag;
-    uint16_t *dY_terms;
+    uint16_t *dY_rows, *dY_terms;
+    uint8_t *phi_img;
     void *phi;
     int64_t ctas;      // of coefs_kernel
     size_t hist_smem;  // its dynamic shared memory
@@ -576,7 +407,9 @@ Ws carve(void *base, int64_t B, int n, int64_t C, int iters, int num_sms)
     w.dH_pre = reinterpret_cast<float *>(take(static_cast<size_t>(B) * n * 4));
     w.mix = reinterpret_cast<float *>(take(static_cast<size_t>(Bp) * mix_vals(n) * 4));
     w.part = reinterpret_cast<float *>(take(static_cast<size_t>(w.ctas) * (N + 3) * 4));
-    w.dY_frag = reinterpret_cast<uint32_t *>(take(static_cast<size_t>(Bp) * dy_cols(n) * 2));
+    w.dY_rows = reinterpret_cast<uint16_t *>(take(static_cast<size_t>(Bp) * dy_cols(n) * 2));
+    w.phi_img = take(static_cast<size_t>((C + streams_width(n) - 1) / streams_width(n) *
+                                         phi_image_bytes(n)));
     w.dY_terms = reinterpret_cast<uint16_t *>(take(static_cast<size_t>(Bp) * phi_term_rows(N) * 2));
     w.hist = nullptr;
     if (w.hist_smem == 0 && iters > 0)
@@ -589,35 +422,29 @@ Ws carve(void *base, int64_t B, int n, int64_t C, int iters, int num_sms)
 template <int n>
 cudaError_t launch_n(const PreBackwardArgs &a, const Ws &w, int num_sms, cudaStream_t stream)
 {
-    using D = DX<n>;
-    constexpr int N = D::N;
+    constexpr int N = n * n + 2 * n;
     const int64_t Bp = phi_grad_padded_tokens(a.B);
     // a warp a token once there are tokens for some warps on every SM, else a CTA a token
     const bool many = a.B >= 16 * static_cast<int64_t>(num_sms);
     const int64_t dot_ctas = many ? (a.B + kDotWarps - 1) / kDotWarps : a.B;
+    const int64_t phi_ctas = (n * a.C + kDotWarps * 32 - 1) / (kDotWarps * 32);
     cudaError_t e = launch_pdl(many ? dots_kernel<n, 1> : dots_kernel<n, kDotWarps>,
-                               dim3(static_cast<unsigned>(dot_ctas)), dim3(kDotWarps * 32), 0,
-                               stream, a.dF_pre, a.Xq, a.Xs, a.B, a.C, w.dH_pre);
+                               dim3(static_cast<unsigned>(dot_ctas + phi_ctas)),
+                               dim3(kDotWarps * 32), 0, stream, a.dF_pre, a.Xq, a.Xs, a.phi_t, a.B,
+                               a.C, static_cast<unsigned>(dot_ctas), w.dH_pre, w.phi_img);
     if (e != cudaSuccess) return e;
-    const CoefOut o{w.mix, w.dY_frag, w.dY_terms, w.part, w.hist};
+    const CoefOut o{w.mix, w.dY_rows, w.dY_terms, w.part, w.hist};
     static std::atomic<uint64_t> configured{0};
     e = once_per_device(configured, [] {
-        const cudaError_t c = cudaFuncSetAttribute(
-            coefs_kernel<n>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHistSmem);
-        return c != cudaSuccess ? c
-                                : cudaFuncSetAttribute(streams_kernel<n>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       D::kPhiBytes);
+        return cudaFuncSetAttribute(coefs_kernel<n>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kHistSmem);
     });
     if (e != cudaSuccess) return e;
     e = launch_pdl(coefs_kernel<n>, dim3(static_cast<unsigned>(w.ctas)), dim3(kCoefThreads),
                    w.hist_smem, stream, a, w.dH_pre, Bp, o);
     if (e != cudaSuccess) return e;
-    const int64_t steps = (a.B + D::TS - 1) / D::TS;
-    const int64_t units = (a.C + D::S - 1) / D::S * steps;
-    e = launch_pdl(streams_kernel<n>, dim3(static_cast<unsigned>(units < num_sms ? units : num_sms)),
-                   dim3(D::kWarps * 32), D::kPhiBytes, stream, a.dX_next, a.dF_pre, a.Xq, a.Xs,
-                   a.phi_t, w.mix, w.dY_frag, a.B, a.C, steps, units, a.dX);
+    e = launch_streams(StreamsArgs{a.dX_next, a.dF_pre, w.phi_img, w.dY_rows, a.Xq, a.Xs, w.mix, a.B,
+                                   Bp, a.C, a.dX}, n, num_sms, stream);
     if (e != cudaSuccess) return e;
     e = launch_phi_grad(a.Xq, a.Xs, w.dY_terms, a.B, n, a.C, a.accumulate, a.dphi_t, w.phi,
                         num_sms, stream);

@@ -2,7 +2,8 @@
 // Arguments have already been validated by train_api.cu when these run.
 //
 // Sites of the device index checks (check.cuh) here: 1000s ckpt.cu, 1100s
-// post_backward.cu, 1200s pre_backward.cu, 1300s phi_grad.cu, 1400s embed.cu.
+// post_backward.cu, 1200s pre_backward.cu and (1240s) streams.cu, 1300s
+// phi_grad.cu, 1400s embed.cu.
 #pragma once
 
 #include <atomic>
@@ -71,6 +72,42 @@ struct PreBackwardArgs {
 size_t pre_backward_workspace_bytes(int64_t B, int n, int64_t C, int iters, int num_sms);
 cudaError_t launch_pre_backward(const PreBackwardArgs &a, void *workspace, int num_sms,
                                 cudaStream_t stream);
+
+// ---- dX (streams.cu)
+// k of the product dY·φ, padded to the tensor instruction's 16
+__host__ __device__ constexpr int dy_cols(int n) { return (n * n + 2 * n + 15) / 16 * 16; }
+// what mixes a token's streams: H_resᵀ [j][i], H_pre[j], s
+__host__ __device__ constexpr int mix_vals(int n) { return n * n + n + 1; }
+// Channels of a unit of streams.cu, and how φ is laid out for it: for each chunk of
+// that many channels, rows (j, channel) of k in bf16, phi_image_row bytes each with
+// the 16-byte pieces swizzled as the tensor cores read them; for n = 8 the k past
+// 64 in rows of their own behind them.
+__host__ __device__ constexpr int streams_width(int n) { return n <= 4 ? 64 : 32; }
+__host__ __device__ constexpr int phi_image_row(int n)
+{
+    return dy_cols(n) <= 16 ? 32 : dy_cols(n) <= 32 ? 64 : 128;
+}
+__host__ __device__ constexpr int phi_image_row2(int n) { return dy_cols(n) > 64 ? 32 : 0; }
+__host__ __device__ constexpr int64_t phi_image_bytes(int n)  // of a chunk
+{
+    return static_cast<int64_t>(n) * streams_width(n) * (phi_image_row(n) + phi_image_row2(n));
+}
+// What a row's 16-byte piece numbers are XORed with, in rows of `bytes`.
+__host__ __device__ constexpr int swizzle_xor(int bytes, int row)
+{
+    return bytes == 128 ? row & 7 : bytes == 64 ? row >> 1 & 3 : bytes == 32 ? row >> 2 & 1 : 0;
+}
+struct StreamsArgs {
+    const uint16_t *dX_next, *dF;
+    const uint8_t *phi_img;    // [chunks][phi_image_bytes]
+    const uint16_t *dY_rows;   // [Bp][dy_cols], zeros past N
+    const uint8_t *Xq, *Xs;
+    const float *mix;          // [mix_vals][Bp]
+    int64_t B, Bp, C;          // Bp: tokens, padded
+    uint16_t *dX;
+};
+cudaError_t launch_streams(const StreamsArgs &s, int n, int num_sms, cudaStream_t stream);
+cudaError_t read_and_clear_streams_status(int *status);
 
 // ---- dφ (phi_grad.cu)
 // dY in three bf16 terms that add up to it (to about 2^-26 of its size): the hi
