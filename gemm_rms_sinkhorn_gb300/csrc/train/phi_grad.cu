@@ -9,8 +9,12 @@
 // of 64 tokens, the (strip, block) units dealt out in equal contiguous ranges,
 // one CTA per SM:
 //
-//   warps 0-15  load codes and scales two units ahead into registers, write the
-//               bf16 values to the stage's A tile and hand it over;
+//   warp 18     TMA: the codes (64 rows of 256 bytes) into a ring of their own, up
+//               to four units ahead;
+//   warps 0-15  read them there, write the bf16 values to a stage's A tile and hand
+//               it over.  (Loaded to registers ahead of use, the codes in flight
+//               held up the proxy fence that the hand-over needs: 180 us at
+//               B=16384, n=4, C=7168.)  The scales are loaded between hand-overs;
 //   warp 16     TMA: the dY terms of the block (B tile);
 //   warp 17     tcgen05.mma, M = 128 channels (two accumulators), N = 3n² + 6n
 //               columns padded to 48, K = 16 tokens.
@@ -43,7 +47,8 @@ constexpr int kTok = kPhiTokens;
 constexpr int kLoadWarps = 16;
 constexpr int kRowsEach = kTok / kLoadWarps;  // tokens of a unit that a load warp takes
 constexpr int kFlush = 16;                    // units in one accumulation chain
-constexpr int kThreads = (kLoadWarps + 2) * 32;
+constexpr int kThreads = (kLoadWarps + 3) * 32;
+constexpr int kRawBytes = kStrip * kTok;  // a unit's codes
 constexpr int kABytes = kStrip * kTok * 2;  // 32 KB
 constexpr int kStatusTimeout = -5;          // MHC_ERR_TIMEOUT
 
@@ -55,8 +60,9 @@ struct Cfg {
     static constexpr int NT = phi_term_rows(N);  // columns
     static constexpr int kBBytes = NT * kTok * 2;
     static constexpr int kStage = kABytes + kBBytes;
-    static constexpr int kStages = n <= 4 ? 4 : 3;
-    static constexpr int kSmem = 1024 + kStages * kStage + 256;
+    static constexpr int kStages = n <= 7 ? 3 : 2;
+    static constexpr int kRaw = n == 7 ? 3 : 4;  // units of codes in flight
+    static constexpr int kSmem = 1024 + kStages * kStage + kRaw * kRawBytes + 256;
     static constexpr int kTmemCols = 2 * NT <= 128 ? 128 : 2 * NT <= 256 ? 256 : 512;
     static_assert(NT <= 256 && NT % 16 == 0, "MMA N for M = 128");
     static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -86,14 +92,11 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead,
     return d;
 }
 
-struct Tile {  // a thread's codes of one unit: 8 channels of kRowsEach tokens
-    uint2 q[kRowsEach];
-    uint32_t E[kRowsEach];
-};
-
-template <int n>
+// kTma: the codes can be copied by TMA, whose row strides are multiples of 16 bytes.
+template <int n, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
-phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restrict__ Xq,
+phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y,
+                const __grid_constant__ CUtensorMap tm_x, const uint8_t *__restrict__ Xq,
                 const uint8_t *__restrict__ Xs, int64_t B, int64_t C, Units un,
                 float *__restrict__ part, uint64_t limit_ns)
 {
@@ -101,8 +104,10 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cf::kStages * Cf::kStage);
-    uint64_t *empty = full + Cf::kStages;
+    uint8_t *raw = smem + Cf::kStages * Cf::kStage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(raw + Cf::kRaw * kRawBytes);
+    uint64_t *raw_full = full + Cf::kStages, *raw_empty = raw_full + Cf::kRaw;
+    uint64_t *empty = raw_empty + Cf::kRaw;
     uint64_t *acc_full = empty + Cf::kStages, *acc_empty = acc_full + 1, *drain = acc_empty + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -116,6 +121,10 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
         for (int s = 0; s < Cf::kStages; ++s) {
             ptx::mbar_init(&full[s], kLoadWarps + 1);
             ptx::mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < Cf::kRaw; ++s) {
+            ptx::mbar_init(&raw_full[s], 1);
+            ptx::mbar_init(&raw_empty[s], kLoadWarps);
         }
         ptx::mbar_init(acc_full, 1);
         ptx::mbar_init(acc_empty, kLoadWarps);
@@ -155,28 +164,19 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
             l_E = Xs + (b * n + i) * nb + (c >> 5);
         };
         enter();
-        // the next unit of the CTA's range
-        const auto load = [&](Tile &x) {
-            const uint8_t *q = l_q, *E = l_E;
+        uint32_t E[kRowsEach];
+        uint2 q[kRowsEach];
+        // the scales (and without TMA the codes) of the next unit of the CTA's range
+        const auto load = [&] {
             const int64_t rows = B - static_cast<int64_t>(l_block) * kTok;
-            if (l_left > 0 && l_in && rows >= kTok && in_range(1301, l_q - Xq, 8, B * K)) {
 #pragma unroll
-                for (int e = 0; e < kRowsEach; ++e, q += row_q, E += row_E) {
-                    x.q[e] = kept::ld_stream_v2(q);
-                    x.E[e] = __ldg(E);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < kRowsEach; ++e, q += row_q, E += row_E) {
-                    const bool ok = l_left > 0 && l_in && warp + kLoadWarps * e < rows &&
-                                    in_range(1303, q - Xq, 8, B * K);
-                    x.q[e] = ok ? kept::ld_stream_v2(q) : make_uint2(0, 0);
-                    x.E[e] = ok ? __ldg(E) : kept::kScaleMin;
-                }
+            for (int e = 0; e < kRowsEach; ++e, l_q += row_q, l_E += row_E) {
+                const bool ok = l_left > 0 && l_in && warp + kLoadWarps * e < rows &&
+                                in_range(1301, l_q - Xq, 8, B * K);
+                E[e] = ok ? __ldg(l_E) : kept::kScaleMin;
+                if constexpr (!kTma) q[e] = ok ? kept::ld_stream_v2(l_q) : make_uint2(0, 0);
             }
             --l_left;
-            l_q = q;
-            l_E = E;
             if (++l_block == blocks) {
                 l_block = 0;
                 ++l_strip;
@@ -189,25 +189,37 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
         const int quarter = warp & 3, half = warp >> 2 & 1, m0 = warp >> 3;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                static_cast<uint32_t>(half * Cf::NT);
-        int stage = 0, chain = 0, in_chain = 0;
-        uint32_t phase = 0;
+        int stage = 0, slot = 0, chain = 0, in_chain = 0;
+        uint32_t phase = 0, raw_phase = 0;
         int64_t s_strip = l_strip;  // of the unit being stored
         int s_block = l_block;
         bool fresh = true;  // no chain of this strip has been stored
-        // the tile of one unit into its stage, then the unit after next into x
-        const auto step = [&](bool end, Tile &x) {
+        // the tile of one unit into its stage
+        const auto step = [&](bool end) {
             // (warp-uniform: the loads of the accumulators are warp-collective)
-            if (!__all_sync(0xffffffffu, wait(&empty[stage], phase ^ 1))) return false;
+            bool ok = wait(&empty[stage], phase ^ 1);
+            if constexpr (kTma) ok = ok && wait(&raw_full[slot], raw_phase);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            if constexpr (kTma) {
+                const uint8_t *src = raw + slot * kRawBytes + warp * kStrip + lane * 8;
+#pragma unroll
+                for (int e = 0; e < kRowsEach; ++e)
+                    q[e] = *reinterpret_cast<const uint2 *>(src + e * (kLoadWarps * kStrip));
+            }
             uint8_t *dst = smem + stage * Cf::kStage + at;
 #pragma unroll
             for (int e = 0; e < kRowsEach; ++e)
                 *reinterpret_cast<uint4 *>(dst + e * (kLoadWarps / 8) * 1024) =
-                    kept::decode8_bf16(x.q[e], x.E[e]);
-            load(x);
+                    kept::decode8_bf16(q[e], E[e]);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&full[stage]);
+            if (lane == 0) {
+                ptx::mbar_arrive(&full[stage]);
+                if (kTma) ptx::mbar_arrive(&raw_empty[slot]);
+            }
             if (++stage == Cf::kStages) { stage = 0; phase ^= 1; }
+            if (++slot == Cf::kRaw) { slot = 0; raw_phase ^= 1; }
+            load();
             const bool last = end || s_block + 1 == blocks;
             if (++in_chain == kFlush || last) {
                 in_chain = 0;
@@ -248,13 +260,9 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
             }
             return true;
         };
-        Tile x0, x1;
-        load(x0);
-        load(x1);
-        for (int64_t left = u1 - u0; left > 0; left -= 2) {
-            if (!step(left == 1, x0)) break;
-            if (left > 1 && !step(left == 2, x1)) break;
-        }
+        load();
+        for (int64_t left = u1 - u0; left > 0; --left)
+            if (!step(left == 1)) break;
     } else if (warp == kLoadWarps) {
         if (lane == 0) {
             const uint64_t pol = ptx::policy_evict_last();  // every strip reads them
@@ -275,6 +283,30 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y, const uint8_t *__restr
             // barrier cannot tell that the copy has landed: wait by the clock, far
             // longer than any copy takes
             if (*abort) {
+                const uint64_t t0 = ptx::globaltimer_ns();
+                for (int polls = 0; polls < (1 << 20) && ptx::globaltimer_ns() - t0 < 1000000; ++polls)
+                    __nanosleep(200);
+            }
+        }
+    } else if (warp == kLoadWarps + 2) {
+        if (kTma && lane == 0) {
+            const uint64_t pol = ptx::policy_evict_first();
+            int slot = 0;
+            uint32_t phase = 0;
+            int64_t strip = u0 / un.blocks;
+            int block = static_cast<int>(u0 % un.blocks);
+            for (int64_t left = u1 - u0; left > 0; --left) {
+                if (!wait(&raw_empty[slot], phase ^ 1)) break;
+                ptx::mbar_arrive_expect_tx(&raw_full[slot], kRawBytes);
+                ptx::tma_load_2d(raw + slot * kRawBytes, &tm_x, static_cast<int32_t>(strip * kStrip),
+                                 static_cast<int32_t>(block) * kTok, &raw_full[slot], pol);
+                if (++slot == Cf::kRaw) { slot = 0; phase ^= 1; }
+                if (++block == un.blocks) {
+                    block = 0;
+                    ++strip;
+                }
+            }
+            if (*abort) {  // as above
                 const uint64_t t0 = ptx::globaltimer_ns();
                 for (int polls = 0; polls < (1 << 20) && ptx::globaltimer_ns() - t0 < 1000000; ++polls)
                     __nanosleep(200);
@@ -373,14 +405,24 @@ cudaError_t launch_n(const CUtensorMap &tm, const uint8_t *Xq, const uint8_t *Xs
                      int64_t C, const Units &un, int accumulate, float *dphi_t, float *part,
                      cudaStream_t stream)
 {
+    using Cf = Cfg<n>;
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = once_per_device(configured, [] {
-        return cudaFuncSetAttribute(phi_grad_kernel<n>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<n>::kSmem);
+        const cudaError_t c = cudaFuncSetAttribute(
+            phi_grad_kernel<n, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::kSmem);
+        return c != cudaSuccess ? c
+                                : cudaFuncSetAttribute(phi_grad_kernel<n, false>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       Cf::kSmem);
     });
     if (e != cudaSuccess) return e;
-    e = launch_pdl(phi_grad_kernel<n>, dim3(un.grid), dim3(kThreads), Cfg<n>::kSmem,
-                               stream, tm, Xq, Xs, B, C, un, part, kWaitLimitNs);
+    CUtensorMap tx = tm;
+    const bool tma = n * C % 16 == 0;
+    const int64_t dims[2] = {n * C, B};
+    const int box[2] = {kStrip, kTok};
+    if (tma && !encode_tensor(&tx, 1, 2, Xq, dims, box)) return cudaErrorInvalidValue;
+    e = launch_pdl(tma ? phi_grad_kernel<n, true> : phi_grad_kernel<n, false>, dim3(un.grid),
+                   dim3(kThreads), Cf::kSmem, stream, tm, tx, Xq, Xs, B, C, un, part, kWaitLimitNs);
     if (e != cudaSuccess) return e;
     const int64_t K = n * C;
     return launch_pdl(phi_join_kernel,

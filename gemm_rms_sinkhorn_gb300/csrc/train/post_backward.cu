@@ -217,15 +217,32 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
         uint32_t E;
         Raw8 f;
     } slots[kDepth];
+#pragma unroll
+    for (int x = 0; x < kDepth; ++x) {
+        slots[x].g = slots[x].f.a = slots[x].f.b = make_uint4(0, 0, 0, 0);
+        slots[x].q = make_uint2(0, 0);
+        slots[x].E = kept::kScaleMin;
+    }
+    const int whole = static_cast<int>(C >> 5);  // groups with all their channels
+    const bool have_f = kF32 ? have : have_tok && g == 0;  // bf16: F_out is row 8 of the left operand
     const auto load = [&](Slot &x, int cg) {
-        const bool in = cg < groups && cg * 32 + t * 8 < C && in_range(1112, cg * 32 + t * 8, 8, C);
-        x.g = in && have ? ptx::ld_stream_v4(g_row + cg * 32) : make_uint4(0, 0, 0, 0);
-        x.q = in && have ? kept::ld_stream_v2(q_row + cg * 32) : make_uint2(0, 0);
-        // every lane scales its row's sums, also where its own channels are past C
-        x.E = cg < groups && have ? __ldg(s_row + cg) : kept::kScaleMin;
-        // bf16: F_out is row 8 of the left operand, at lanes 0 .. 3
-        x.f.a = x.f.b = make_uint4(0, 0, 0, 0);
-        if (in && (kF32 ? have : have_tok && g == 0)) load_raw(x.f, f_row + cg * 32);
+        if (cg < whole && in_range(1112, cg * 32 + t * 8, 8, C)) {
+            // (a lane without a stream keeps its zeros)
+            if (have) {
+                x.g = ptx::ld_stream_v4(g_row + cg * 32);
+                x.q = kept::ld_stream_v2(q_row + cg * 32);
+                x.E = __ldg(s_row + cg);
+            }
+            if (have_f) load_raw(x.f, f_row + cg * 32);
+        } else if (cg < groups) {
+            const bool in = cg * 32 + t * 8 < C;
+            x.g = in && have ? ptx::ld_stream_v4(g_row + cg * 32) : make_uint4(0, 0, 0, 0);
+            x.q = in && have ? kept::ld_stream_v2(q_row + cg * 32) : make_uint2(0, 0);
+            // every lane scales its row's sums, also where its own channels are past C
+            x.E = have ? __ldg(s_row + cg) : kept::kScaleMin;
+            x.f.a = x.f.b = make_uint4(0, 0, 0, 0);
+            if (in && have_f) load_raw(x.f, f_row + cg * 32);
+        }
     };
     float acc[2] = {0.f, 0.f}, post[2] = {0.f, 0.f};
     const auto use = [&](Slot &s, int cg) {
@@ -234,9 +251,9 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
         const uint4 gw = s.g;
         const Raw8 fr = s.f;
         load(s, cg + kDepth * W);
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        float d[4];
         if constexpr (kF32) {
-            mma_16816(d, x.x, 0u, x.y, 0u, gw.x, gw.y);
+            mma_16816_new(d, x.x, 0u, x.y, 0u, gw.x, gw.y);
             mma_16816(d, x.z, 0u, x.w, 0u, gw.z, gw.w);
             uint64_t v[4], f[4], a = 0;
             unpack8_pairs(gw, v);
@@ -247,7 +264,7 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
             f2_unpack(a, lo, hi);
             post[0] += lo + hi;
         } else {
-            mma_16816(d, x.x, fr.a.x, x.y, fr.a.y, gw.x, gw.y);
+            mma_16816_new(d, x.x, fr.a.x, x.y, fr.a.y, gw.x, gw.y);
             mma_16816(d, x.z, fr.a.z, x.w, fr.a.w, gw.z, gw.w);
             post[0] += d[2];
             post[1] += d[3];
@@ -256,22 +273,29 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
         acc[1] = fmaf(d[1], scale, acc[1]);
         // dF_out: word w of the group's lanes, channels 8t + 2w, + 1, transposed
         const uint32_t word[4] = {gw.x, gw.y, gw.z, gw.w};
-        uint64_t df[4];
+        float o[4][4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const uint32_t m = transpose_8x8(word[w]);
-            float o[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_1688(o, h_low, 0u, m);
-            mma_16816(o, h_hi, 0u, h_mid, 0u, m, m);
-            df[w] = f2_pack(o[0], o[1]);
+            mma_1688_new(o[w], h_low, 0u, m);
+            mma_16816(o[w], h_hi, 0u, h_mid, 0u, m, m);
         }
-        if (g == 0 && have_tok && cg < groups && cg * 32 + t * 8 < C) store8(df_row + cg * 32, df);
+        if (g == 0 && cg * 32 + t * 8 < C) {
+            uint64_t df[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) df[w] = f2_pack(o[w][0], o[w][1]);
+            store8(df_row + cg * 32, df);
+        }
     };
+    // (a token's warps all have it or all do not)
+    if (have_tok) {
 #pragma unroll
-    for (int x = 0; x < kDepth; ++x) load(slots[x], warp % W + x * W);
-    for (int cg = warp % W; cg < groups; cg += kDepth * W)
+        for (int x = 0; x < kDepth; ++x) load(slots[x], warp % W + x * W);
+        for (int cg = warp % W; cg < groups; cg += kDepth * W)
 #pragma unroll
-        for (int x = 0; x < kDepth; ++x) use(slots[x], cg + x * W);
+            for (int x = 0; x < kDepth; ++x)
+                if (cg + x * W < groups) use(slots[x], cg + x * W);
+    }
     if constexpr (kF32) {
         post[0] += __shfl_xor_sync(0xffffffffu, post[0], 1);
         post[0] += __shfl_xor_sync(0xffffffffu, post[0], 2);

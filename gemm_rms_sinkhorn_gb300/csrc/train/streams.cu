@@ -24,7 +24,14 @@
 // products, a 128-bit request touches 8 lines and L1 is at its limit: 623 us.
 // With 128 tokens × 32 channels by TMA, rows are 64 bytes (32 of codes): L2 lines
 // were evicted between a row's chunks under evict_first (2.5 GB read in place of
-// 1.7), and TMA takes about 2.8 cycles a row whatever its length: 490 us.
+// 1.7): 640 us, and 490 without that hint.  Now 445; the copies alone, with the
+// mixing taken out, take 416.  Copying with cp.async in four warps in place of TMA:
+// 494.  A warp of its own for the scales, in place of a byte per thread and stream:
+// no faster (n = 8: 478 against 418 us).
+//
+// For n >= 6 a mixing thread needs more than its share of registers (H_res is 64 of
+// them at n = 8), and the other warps give theirs up (n = 8: 654 -> 418 us); up to
+// n = 5 it does not, and the exchange costs 10 %.
 //
 // Codes can only be copied by TMA where C % 16 == 0 (16-byte row strides);
 // otherwise the threads read them from global memory.
@@ -33,7 +40,6 @@
 
 #include <atomic>
 #include <cstdint>
-#include <mutex>
 
 #include "check.cuh"
 #include "kept.cuh"
@@ -49,6 +55,9 @@ constexpr int kTok = 64;           // tokens of a tile
 constexpr int kLanes = 128;        // TMEM lanes, threads of a group: each token twice
 constexpr int kGroups = 2;         // groups of 128 threads that share a unit's channels
 constexpr int kThreads = kGroups * kLanes + 4 * 32;
+// registers of a mixing thread and of the others where they are shared out anew; as
+// launched every thread has 168: 256·232 + 128·40 = 384·168
+constexpr int kRegsMix = 232, kRegsRest = 40;
 constexpr int kStatusTimeout = -5; // MHC_ERR_TIMEOUT
 constexpr int kRingBudget = 223 * 1024;
 
@@ -66,6 +75,7 @@ struct Cfg {
     static constexpr int kBBytes = NC * (RB + RB2), kGBytes = n * kTok * GB;
     static constexpr int kXBytes = n * kTok * W, kFBytes = kTok * GB;
     static constexpr int kStage = kBBytes + kGBytes + kXBytes + kFBytes;
+    static constexpr bool kShareRegs = n >= 6;
     static constexpr int kABytes = kLanes * (RB + RB2);
     static constexpr int kFit = (kRingBudget - kABytes) / kStage;
     static constexpr int kStages = kFit < 6 ? kFit : 6;
@@ -215,6 +225,12 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
         return false;
     };
 
+    if constexpr (Cf::kShareRegs) {
+        if (warp < 8)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMix));
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    }
     if (warp < 8) {
         // ------------------------------------------------------------- mix
         const int group = warp >> 2, row = threadIdx.x & (kTok - 1);
@@ -451,53 +467,6 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
     }
 }
 
-typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                             const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                             const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn()
-{
-    static EncodeFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeFn>(p);
-    });
-    return fn;
-}
-
-// A tensor of `rank` dimensions, innermost first, densely packed, read in boxes of
-// box[] elements whose rows are swizzled by their width.
-bool encode(CUtensorMap *m, int esize, int rank, const void *base, const int64_t *dims,
-            const int *box)
-{
-    const EncodeFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t d[3], strides[2];
-    cuuint32_t b[3], one[3] = {1, 1, 1};
-    uint64_t stride = static_cast<uint64_t>(esize);
-    for (int k = 0; k < rank; ++k) {
-        d[k] = static_cast<cuuint64_t>(dims[k]);
-        b[k] = static_cast<cuuint32_t>(box[k]);
-        stride *= d[k];
-        if (k + 1 < rank) strides[k] = stride;
-    }
-    const int row = box[0] * esize;
-    const CUtensorMapSwizzle sw = row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                  : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                  : row == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
-                                              : CU_TENSOR_MAP_SWIZZLE_NONE;
-    return fn(m, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-              static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, strides, b, one,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int n>
 cudaError_t launch_n(const StreamsArgs &s, int num_sms, cudaStream_t stream)
 {
@@ -507,10 +476,10 @@ cudaError_t launch_n(const StreamsArgs &s, int num_sms, cudaStream_t stream)
     const int64_t g_dims[3] = {s.C, n, s.B}, f_dims[2] = {s.C, s.B}, y_dims[2] = {Cf::kCols, s.Bp};
     const int g_box[3] = {Cf::W, 1, kTok}, f_box[2] = {Cf::W, kTok};
     const int y_box[2] = {Cf::RB / 2, kTok}, y2_box[2] = {16, kTok};
-    bool ok = encode(&m.g, 2, 3, s.dX_next, g_dims, g_box) && encode(&m.dx, 2, 3, s.dX, g_dims, g_box) &&
-              encode(&m.f, 2, 2, s.dF, f_dims, f_box) && encode(&m.y, 2, 2, s.dY_rows, y_dims, y_box);
-    if (ok && tma_x) ok = encode(&m.x, 1, 3, s.Xq, g_dims, g_box);
-    if (ok && Cf::RB2 != 0) ok = encode(&m.y2, 2, 2, s.dY_rows, y_dims, y2_box);
+    bool ok = encode_tensor(&m.g, 2, 3, s.dX_next, g_dims, g_box) && encode_tensor(&m.dx, 2, 3, s.dX, g_dims, g_box) &&
+              encode_tensor(&m.f, 2, 2, s.dF, f_dims, f_box) && encode_tensor(&m.y, 2, 2, s.dY_rows, y_dims, y_box);
+    if (ok && tma_x) ok = encode_tensor(&m.x, 1, 3, s.Xq, g_dims, g_box);
+    if (ok && Cf::RB2 != 0) ok = encode_tensor(&m.y2, 2, 2, s.dY_rows, y_dims, y2_box);
     if (!ok) return cudaErrorInvalidValue;
     if (!tma_x) m.x = m.g;  // not used
     if (Cf::RB2 == 0) m.y2 = m.y;

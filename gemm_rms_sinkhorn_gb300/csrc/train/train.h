@@ -10,6 +10,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "mhc_internal.h"
@@ -29,6 +30,12 @@ cudaError_t once_per_device(std::atomic<uint64_t> &done, F set)
     if ((e = set()) == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
+
+// A tensor of `rank` dimensions, innermost first, densely packed, read in boxes of
+// box[] elements of 1 or 2 bytes, whose rows are swizzled by their width where that
+// is 32, 64 or 128 bytes (tensor_map.cu).  False when there is no such map.
+bool encode_tensor(CUtensorMap *m, int esize, int rank, const void *base, const int64_t *dims,
+                   const int *box);
 
 constexpr int kKeptBlock = 32;  // channels that share a scale
 __host__ __device__ inline int64_t kept_blocks(int64_t C)

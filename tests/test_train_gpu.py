@@ -278,6 +278,23 @@ def test_pre_backward(B, n, C, iters):
         within(out[k], ref[k], tol[k], k)
 
 
+@pytest.mark.parametrize("term", ["G", "dF", "phi", "X"])
+@pytest.mark.parametrize("B,n,C", [(70, 1, 200), (130, 2, 72), (65, 3, 264), (200, 4, 136), (70, 4, 2056),
+                                   (67, 5, 96), (66, 6, 264), (131, 7, 72), (129, 8, 136), (70, 8, 288)])
+def test_each_term_of_dX_alone(B, n, C, term):
+    """The other terms' inputs are zero, so that an error in a small term is not hidden by a large one's
+    rounding (H̃ does not depend on X where Y is zero)."""
+    d = pre_case(B + n, B, n, C, 5)
+    zero = {"G": ("dF", "dhr", "dhq"), "dF": ("G", "phi", "dhr", "dhq", "Y"), "phi": ("G", "dF", "Y"),
+            "X": ("G", "dF", "phi")}[term]
+    for k in zero:
+        d[k] = torch.zeros_like(d[k])
+    out, _ = pre_run(d, B, n, C, 5, Guarded())
+    ref, tol = pre_ref(d, B, n, C, 5)
+    assert float(ref["dX"].abs().max()) > 0
+    within(out["dX"], ref["dX"], tol["dX"], "dX")
+
+
 def test_pre_backward_many_iterations_keep_their_history_in_the_workspace():
     """More steps than shared memory holds (2·8·64·4 bytes each), and more tokens than one walk."""
     B, n, C, iters = 300, 8, 40, 60
