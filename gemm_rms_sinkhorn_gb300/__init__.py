@@ -136,6 +136,8 @@ def _ptr(t, dtype, name):
     """Device pointer of a contiguous CUDA tensor of `dtype` (None -> NULL)."""
     if t is None:
         return None
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype != dtype:
@@ -170,7 +172,8 @@ def _ws(ws):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -317,6 +320,8 @@ def _ptr8(t, name):
     """Device pointer of a contiguous CUDA tensor of e4m3 codes (uint8 or float8_e4m3fn)."""
     if t is None:
         return None
+    if type(t) is torch.Tensor and t.dtype is torch.uint8 and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype not in (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8)):

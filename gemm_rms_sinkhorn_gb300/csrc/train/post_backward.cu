@@ -8,9 +8,9 @@
 // (dX = H_resᵀ·G + … is left to the backward of what precedes, which has more
 // to add to it, so G is not mixed and written twice.)
 //
-// One pass over G, the codes and F_out, bound by their bytes.  Two forms, both
-// with one or eight warps per token and their sums added in warp order, so that
-// results do not depend on timing:
+// One pass over G, the codes and F_out, bound by their bytes.  Two forms; where
+// several warps share a token their sums are added in warp order, so that results
+// do not depend on timing:
 //
 //   n <= 4  a lane takes 8 channels of all streams: n² + 2n packed multiply-adds
 //           a channel pair, accumulators in registers.
@@ -37,7 +37,7 @@ namespace mhc {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kDepth = 4;  // channel groups that a warp of the n >= 5 form has in flight
+constexpr int kDepth = 2;  // channel groups that a warp of the n >= 5 form has in flight
 
 // Eight values of F_out or dF_out, in bf16 or fp32.
 struct Raw8 {
@@ -175,8 +175,10 @@ __device__ __forceinline__ void split3(float v, uint32_t &hi, uint32_t &mid, uin
     low = pack_bf16_rn(r - bf16_lo(mid), 0.f);
 }
 
-template <int n, typename FT, int W>
-__global__ void __launch_bounds__(kWarps * 32)
+// Three CTAs an SM (80 registers): at B=8192, n=8, C=4096 206 us; two, with two or
+// four groups in flight, 255 and 237; four, with one, 211.
+template <int n, typename FT>
+__global__ void __launch_bounds__(kWarps * 32, 3)
 post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *__restrict__ Xq,
                           const uint8_t *__restrict__ Xs, const FT *__restrict__ F_out,
                           const float *__restrict__ H_post, int64_t B, int64_t C,
@@ -191,7 +193,7 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
     const int groups = static_cast<int>(nb);
     ptx::pdl_wait();
     ptx::pdl_trigger();
-    const int64_t b = static_cast<int64_t>(blockIdx.x) * (kWarps / W) + warp / W;
+    const int64_t b = blockIdx.x;
     const bool have_tok = b < B && in_range(1111, b, 1, B);
     const bool have = have_tok && g < n;
     const uint16_t *g_row = dX_next + (b * n + g) * C + t * 8;
@@ -250,7 +252,7 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
         const float scale = kept::scale_value(s.E);
         const uint4 gw = s.g;
         const Raw8 fr = s.f;
-        load(s, cg + kDepth * W);
+        load(s, cg + kDepth * kWarps);
         float d[4];
         if constexpr (kF32) {
             mma_16816_new(d, x.x, 0u, x.y, 0u, gw.x, gw.y);
@@ -287,14 +289,13 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
             store8(df_row + cg * 32, df);
         }
     };
-    // (a token's warps all have it or all do not)
     if (have_tok) {
 #pragma unroll
-        for (int x = 0; x < kDepth; ++x) load(slots[x], warp % W + x * W);
-        for (int cg = warp % W; cg < groups; cg += kDepth * W)
+        for (int x = 0; x < kDepth; ++x) load(slots[x], warp + x * kWarps);
+        for (int cg = warp; cg < groups; cg += kDepth * kWarps)
 #pragma unroll
             for (int x = 0; x < kDepth; ++x)
-                if (cg + x * W < groups) use(slots[x], cg + x * W);
+                if (cg + x * kWarps < groups) use(slots[x], cg + x * kWarps);
     }
     if constexpr (kF32) {
         post[0] += __shfl_xor_sync(0xffffffffu, post[0], 1);
@@ -304,14 +305,14 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
     part[warp][1][lane] = acc[1];
     part[warp][2][lane] = post[0];
     part[warp][3][lane] = post[1];
-    if constexpr (W == 1) __syncwarp(); else __syncthreads();
-    if (!have_tok || warp % W != 0) return;
+    __syncthreads();
+    if (!have_tok || warp != 0) return;
     float s[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         s[k] = 0.f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) s[k] += part[warp + w][k][lane];
+        for (int w = 0; w < kWarps; ++w) s[k] += part[w][k][lane];
     }
     // product rows: X's stream g (dH_res) and F_out (dH_post); columns: G's stream 2t + e
 #pragma unroll
@@ -331,23 +332,24 @@ cudaError_t launch_post_backward(const uint16_t *dX_next, const uint8_t *Xq, con
                                  FT *dF_out, float *dH_res, float *dH_post, int num_sms,
                                  cudaStream_t stream)
 {
-    // a warp a token once there are tokens for some warps on every SM, else a CTA a token
-    const bool many = B >= 16 * static_cast<int64_t>(num_sms);
+    // n <= 4: a warp a token once there are tokens for some warps on every SM, else a
+    // CTA a token.  n >= 5: always a CTA a token, whose warps read neighbouring 64-byte
+    // pieces of a row together (a warp a token: 267 us at B=8192, n=8, C=4096).
+    const bool many = n <= 4 && B >= 16 * static_cast<int64_t>(num_sms);
     const dim3 grid(static_cast<unsigned>(many ? (B + kWarps - 1) / kWarps : B));
     switch (n) {
-#define MHC_CASE(k, name)                                                                        \
+#define MHC_CASE(k, few, all)                                                                    \
     case k:                                                                                      \
-        return launch_pdl(many ? name<k, FT, 1> : name<k, FT, kWarps>, grid, dim3(kWarps * 32),  \
-                          0, stream, dX_next, Xq, Xs, F_out, H_post, B, C, dF_out, dH_res,       \
-                          dH_post);
-        MHC_CASE(1, post_backward_kernel)
-        MHC_CASE(2, post_backward_kernel)
-        MHC_CASE(3, post_backward_kernel)
-        MHC_CASE(4, post_backward_kernel)
-        MHC_CASE(5, post_backward_wide_kernel)
-        MHC_CASE(6, post_backward_wide_kernel)
-        MHC_CASE(7, post_backward_wide_kernel)
-        MHC_CASE(8, post_backward_wide_kernel)
+        return launch_pdl(many ? all : few, grid, dim3(kWarps * 32), 0, stream, dX_next, Xq, Xs, \
+                          F_out, H_post, B, C, dF_out, dH_res, dH_post);
+        MHC_CASE(1, (post_backward_kernel<1, FT, kWarps>), (post_backward_kernel<1, FT, 1>))
+        MHC_CASE(2, (post_backward_kernel<2, FT, kWarps>), (post_backward_kernel<2, FT, 1>))
+        MHC_CASE(3, (post_backward_kernel<3, FT, kWarps>), (post_backward_kernel<3, FT, 1>))
+        MHC_CASE(4, (post_backward_kernel<4, FT, kWarps>), (post_backward_kernel<4, FT, 1>))
+        MHC_CASE(5, (post_backward_wide_kernel<5, FT>), (post_backward_wide_kernel<5, FT>))
+        MHC_CASE(6, (post_backward_wide_kernel<6, FT>), (post_backward_wide_kernel<6, FT>))
+        MHC_CASE(7, (post_backward_wide_kernel<7, FT>), (post_backward_wide_kernel<7, FT>))
+        MHC_CASE(8, (post_backward_wide_kernel<8, FT>), (post_backward_wide_kernel<8, FT>))
 #undef MHC_CASE
     default: return cudaErrorInvalidValue;
     }
