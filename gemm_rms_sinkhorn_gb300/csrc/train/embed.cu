@@ -251,24 +251,31 @@ embed_sum_kernel(const uint16_t *__restrict__ dX, float scale, int accumulate, i
         float acc[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-        uint4 x[n];
-        const auto load = [&](int p) {
-            if (!in_range(1421, pos[p], 1, B)) return;
+        // kBatch positions in flight
+        constexpr int kBatch = n <= 2 ? 8 : n <= 4 ? 4 : 2;
+        uint4 x[kBatch][n];
+        const auto load = [&](int p, uint4 (&to)[n]) {
+            if (p >= len || !in_range(1421, pos[p], 1, B)) return;
             const uint16_t *src = dX + static_cast<int64_t>(pos[p]) * n * C + c8 * 8;
 #pragma unroll
-            for (int i = 0; i < n; ++i) x[i] = ptx::ld_stream_v4(src + i * C);
+            for (int i = 0; i < n; ++i) to[i] = ptx::ld_stream_v4(src + i * C);
         };
-        load(0);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) load(q, x[q]);
         bool begins = row[0] != row[1];  // the current run starts in this chunk
-        for (int p = 0; p < len; ++p) {
+        for (int p0 = 0; p0 < len; p0 += kBatch)
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int p = p0 + q;
+            if (p >= len) break;
 #pragma unroll
             for (int i = 0; i < n; ++i) {
                 float f[8];
-                unpack8(x[i], f);
+                unpack8(x[q][i], f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] += f[e];
             }
-            if (p + 1 < len) load(p + 1);
+            load(p + kBatch, x[q]);
             const int v = row[p + 1];
             const bool ends = row[p + 2] != v;
             if (!ends && p + 1 < len) continue;

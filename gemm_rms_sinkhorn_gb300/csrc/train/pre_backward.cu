@@ -151,43 +151,79 @@ dots_kernel(const uint16_t *__restrict__ dF, const uint8_t *__restrict__ Xq,
 
 // ----------------------------------------------------------------- coefs
 
+// A thread per token.  What a token needs of Y, r, H and dH comes through shared
+// memory, a row of odd length per token (read by a thread each from global memory,
+// every request touches 32 lines), and the sums over tokens go back through it: by
+// shuffles, five dependent ones per column, they took as long as the iteration.  Up
+// to dH_pre nothing here depends on dots, so all that runs beside it.
+// (B=8191, n=8: 42 -> XX us.)
 constexpr int kCoefThreads = 64;
-constexpr int kCoefWarps = kCoefThreads / 32;
-constexpr int kHistSmem = 96 * 1024;  // u_t and v_t of a CTA's tokens, where they fit
+constexpr int kSmemMost = 200 * 1024;
+
+// A token's staged row: Y, dH_res, H_res, H_pre, H_post, dH_post.
+__host__ __device__ constexpr int coef_row(int n) { return (n * n + 2 * n + 2 * n * n + 3 * n) | 1; }
+// dH̃ by column and the α's sums, by token; and u_t, v_t of the iteration.
+__host__ __device__ constexpr int coef_sums(int n) { return (n * n + 2 * n + 3) * (kCoefThreads + 1); }
+inline size_t coef_smem(int n, int iters, bool with_hist)
+{
+    return sizeof(float) * (static_cast<size_t>(kCoefThreads) * coef_row(n) + coef_sums(n) +
+                            (with_hist ? static_cast<size_t>(iters) * 2 * n * kCoefThreads : 0));
+}
 
 struct CoefOut {
     float *mix;          // [mix_vals][padded tokens] (train.h)
     uint16_t *dY_rows;   // [padded tokens][dy_cols] bf16, zeros past N
     uint16_t *dY_terms;  // bf16 terms of dY (train.h)
     float *part;         // [CTAs][N + 3]: Σ dH̃ by column, then by α
-    float *hist;         // [CTAs][iters][2n][threads], or NULL: in shared memory
+    float *hist;         // u_t, v_t: [CTAs][iters][2n][threads], or NULL: in shared memory
 };
 
 template <int n>
 __global__ void __launch_bounds__(kCoefThreads)
 coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, CoefOut o)
 {
-    constexpr int N = n * n + 2 * n, kCols = dy_cols(n);
-    extern __shared__ float smem_hist[];
-    __shared__ float bsum[kCoefWarps][N + 3];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int N = n * n + 2 * n, kCols = dy_cols(n), kRow = coef_row(n);
+    constexpr int kS = kCoefThreads + 1;
+    extern __shared__ float smem_f[];
+    float *rows = smem_f, *sums = rows + kCoefThreads * kRow;  // sums: [N + 3][kS]
     float *hist = o.hist ? o.hist + static_cast<int64_t>(blockIdx.x) * a.iters * 2 * n * kCoefThreads
-                         : smem_hist;
+                         : sums + coef_sums(n);
     hist += threadIdx.x;
     const auto u_at = [&](int t, int i) -> float & { return hist[(t * 2 * n + i) * kCoefThreads]; };
     const auto v_at = [&](int t, int j) -> float & { return hist[(t * 2 * n + n + j) * kCoefThreads]; };
-    for (int k = lane; k < N + 3; k += 32) bsum[warp][k] = 0.f;
-    __syncwarp();
-    ptx::pdl_wait();
-    ptx::pdl_trigger();
+    float total[(N + 3 + kCoefThreads - 1) / kCoefThreads] = {};  // of columns threadIdx.x, + 64
+
+    // the rows of a token block, element by element in the order of global memory
+    const auto stage = [&](int64_t b0) {
+        const int live = static_cast<int>(a.B - b0 < kCoefThreads ? a.B - b0 : kCoefThreads);
+        const auto take = [&](const float *src, int len, int at) {
+            if (live <= 0 || !in_range(1213, b0, live, a.B)) return;
+            for (int x = threadIdx.x; x < live * len; x += kCoefThreads)
+                ptx::cp_async4(rows + x / len * kRow + at + x % len, src + b0 * len + x);
+        };
+        take(a.Y, N, 0);
+        take(a.dH_res, n * n, N);
+        take(a.H_res, n * n, N + n * n);
+        take(a.H_pre, n, N + 2 * n * n);
+        take(a.H_post, n, N + 2 * n * n + n);
+        take(a.dH_post, n, N + 2 * n * n + 2 * n);
+        ptx::cp_async_commit();
+        ptx::cp_async_wait_all();
+        __syncthreads();
+    };
+    // (inputs: the kernel before this one does not write them, and lets this one start only
+    // when what preceded the call had finished)
+    bool waited = false;
 
     const float inv_K = 1.0f / (static_cast<float>(n) * static_cast<float>(a.C));
     for (int64_t b0 = static_cast<int64_t>(blockIdx.x) * kCoefThreads; b0 < Bp;
          b0 += static_cast<int64_t>(gridDim.x) * kCoefThreads) {
         const int64_t b = b0 + threadIdx.x;
         const bool live = b < a.B && in_range(1211, b, 1, a.B);
-        const float *y = a.Y + b * N;
         const float inv_r = live ? 1.0f / __ldg(a.r + b) : 0.f;
+        stage(b0);
+        const float *y = rows + threadIdx.x * kRow, *row_D = y + N, *row_H = row_D + n * n;
+        const float *row_hp = row_H + n * n, *row_hq = row_hp + n, *row_dq = row_hq + n;
         float A[n][n], dA[n][n];
         if (live) {
 #pragma unroll
@@ -195,8 +231,8 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
 #pragma unroll
                 for (int j = 0; j < n; ++j) {
                     const int k = 2 * n + i * n + j;
-                    A[i][j] = a.a_res * __ldg(y + k) * inv_r + __ldg(a.bias + k);
-                    dA[i][j] = __ldg(a.dH_res + b * n * n + i * n + j);
+                    A[i][j] = a.a_res * y[k] * inv_r + __ldg(a.bias + k);
+                    dA[i][j] = row_D[i * n + j];
                 }
             if (a.iters > 0) {
 #pragma unroll
@@ -286,78 +322,83 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
                 for (int j = 0; j < n; ++j) A[i][j] = dA[i][j] = 0.f;
         }
 
+        if (!waited) {
+            ptx::pdl_wait();  // dH_pre
+            ptx::pdl_trigger();
+            waited = true;
+        }
         float *mix = o.mix + b;
-        uint32_t *row = reinterpret_cast<uint32_t *>(o.dY_rows + b * kCols);
+        uint4 *row = reinterpret_cast<uint4 *>(o.dY_rows + b * kCols);
         const bool in = b < Bp && in_range(1212, b, 1, Bp);
         if (in) {
 #pragma unroll
             for (int i = 0; i < n; ++i)
 #pragma unroll
-                for (int j = 0; j < n; ++j)
-                    mix[(j * n + i) * Bp] = live ? __ldg(a.H_res + (b * n + i) * n + j) : 0.f;
+                for (int j = 0; j < n; ++j) mix[(j * n + i) * Bp] = live ? row_H[i * n + j] : 0.f;
         }
         float sx = 0.f, da[3] = {0.f, 0.f, 0.f};
-        uint32_t packed = 0;
+        uint32_t packed[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            float d = 0.f;  // dH̃ of column k
-            if (k < n) {
-                if (live) {
-                    const float h = __ldg(a.H_pre + b * n + k);
-                    mix[(n * n + k) * Bp] = h;
-                    d = __ldg(dH_pre + b * n + k) * h * (1.0f - h);
+        for (int k = 0; k < kCols; ++k) {
+            uint32_t hi = 0;
+            if (k < N) {
+                float d = 0.f;  // dH̃ of column k
+                if (k < n) {
+                    if (live) {
+                        const float h = row_hp[k];
+                        mix[(n * n + k) * Bp] = h;
+                        d = __ldg(dH_pre + b * n + k) * h * (1.0f - h);
+                    }
+                } else if (k < 2 * n) {
+                    if (live) d = row_dq[k - n] * row_hq[k - n] * (1.0f - 0.5f * row_hq[k - n]);
+                } else {
+                    d = dA[(k - 2 * n) / n][(k - 2 * n) % n] * A[(k - 2 * n) / n][(k - 2 * n) % n];
                 }
-            } else if (k < 2 * n) {
-                if (live) {
-                    const float h = __ldg(a.H_post + b * n + (k - n));
-                    d = __ldg(a.dH_post + b * n + (k - n)) * h * (1.0f - 0.5f * h);
+                const float yk = live ? y[k] : 0.f;
+                const float alpha = k < n ? a.a_pre : k < 2 * n ? a.a_post : a.a_res;
+                da[k < n ? 0 : k < 2 * n ? 1 : 2] += d * (yk * inv_r);
+                const float dy = alpha * d * inv_r;
+                sx = fmaf(-dy, yk, sx);
+                sums[k * kS + threadIdx.x] = d;
+                // dY as one bf16 for dX, whose own rounding is as large, and as three
+                // for dφ, which is kept in fp32
+                hi = pack_bf16_rn(dy, 0.f) & 0xFFFFu;
+                const float rest = dy - bf16_lo(hi);
+                const uint32_t mid = pack_bf16_rn(rest, 0.f) & 0xFFFFu;
+                const uint32_t low = pack_bf16_rn(rest - bf16_lo(mid), 0.f) & 0xFFFFu;
+                if (in) {
+                    uint16_t *dst = o.dY_terms + static_cast<int64_t>(phi_term_row(k, 0)) * Bp + b;
+                    dst[0] = static_cast<uint16_t>(hi);
+                    dst[16 * Bp] = static_cast<uint16_t>(mid);
+                    dst[32 * Bp] = static_cast<uint16_t>(low);
                 }
-            } else {
-                d = dA[(k - 2 * n) / n][(k - 2 * n) % n] * A[(k - 2 * n) / n][(k - 2 * n) % n];
             }
-            const float yk = live ? __ldg(y + k) : 0.f;
-            const float alpha = k < n ? a.a_pre : k < 2 * n ? a.a_post : a.a_res;
-            da[k < n ? 0 : k < 2 * n ? 1 : 2] += d * (yk * inv_r);
-            const float dy = alpha * d * inv_r;
-            sx = fmaf(-dy, yk, sx);
-            float s = d;
+            packed[k % 8 / 2] = k % 2 == 0 ? hi : packed[k % 8 / 2] | (hi << 16);
+            if (k % 8 == 7 && in) row[k / 8] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        }
+        if (in) mix[(n * n + n) * Bp] = sx * inv_r * inv_r * inv_K;
 #pragma unroll
-            for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
-            if (lane == 0) bsum[warp][k] += s;
-            // dY as one bf16 for dX, whose own rounding is as large, and as three
-            // for dφ, which is kept in fp32
-            const uint32_t hi = pack_bf16_rn(dy, 0.f) & 0xFFFFu;
-            const float rest = dy - bf16_lo(hi);
-            const uint32_t mid = pack_bf16_rn(rest, 0.f) & 0xFFFFu;
-            const uint32_t low = pack_bf16_rn(rest - bf16_lo(mid), 0.f) & 0xFFFFu;
-            if (in) {
-                uint16_t *dst = o.dY_terms + static_cast<int64_t>(phi_term_row(k, 0)) * Bp + b;
-                dst[0] = static_cast<uint16_t>(hi);
-                dst[16 * Bp] = static_cast<uint16_t>(mid);
-                dst[32 * Bp] = static_cast<uint16_t>(low);
+        for (int e = 0; e < 3; ++e) sums[(N + e) * kS + threadIdx.x] = da[e];
+        __syncthreads();
+        // a thread per column, in the order of the tokens
+#pragma unroll
+        for (int x = 0; x < (N + 3 + kCoefThreads - 1) / kCoefThreads; ++x) {
+            const int k = x * kCoefThreads + threadIdx.x;
+            if (k < N + 3) {
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (int t = 0; t < kCoefThreads; t += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[e] += sums[k * kS + t + e];
+                total[x] += (s[0] + s[1]) + (s[2] + s[3]);
             }
-            if (k % 2 == 0) packed = hi;
-            if ((k % 2 == 1 || k + 1 == N) && in) row[k / 2] = k % 2 == 1 ? packed | (hi << 16) : packed;
         }
-        if (in) {
-#pragma unroll
-            for (int k = (N + 1) / 2; k < kCols / 2; ++k) row[k] = 0;
-            mix[(n * n + n) * Bp] = sx * inv_r * inv_r * inv_K;
-        }
-#pragma unroll
-        for (int e = 0; e < 3; ++e) {
-            float s = da[e];
-#pragma unroll
-            for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
-            if (lane == 0) bsum[warp][N + e] += s;
-        }
+        __syncthreads();
     }
-    __syncthreads();
-    for (int k = threadIdx.x; k < N + 3; k += kCoefThreads) {
-        float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kCoefWarps; ++w) s += bsum[w][k];
-        o.part[static_cast<int64_t>(blockIdx.x) * (N + 3) + k] = s;
+    for (int x = 0; x < (N + 3 + kCoefThreads - 1) / kCoefThreads; ++x) {
+        const int k = x * kCoefThreads + threadIdx.x;
+        if (k < N + 3) o.part[static_cast<int64_t>(blockIdx.x) * (N + 3) + k] = total[x];
     }
 }
 
@@ -386,7 +427,7 @@ struct Ws {
     uint8_t *phi_img;
     void *phi;
     int64_t ctas;      // of coefs_kernel
-    size_t hist_smem;  // its dynamic shared memory
+    size_t coef_smem;  // its dynamic shared memory
     size_t total;
 };
 
@@ -400,8 +441,9 @@ Ws carve(void *base, int64_t B, int n, int64_t C, int iters, int num_sms)
     size_t at = 0;
     const auto take = [&](size_t bytes) { uint8_t *r = p + at; at += up(bytes); return r; };
     const size_t hist = static_cast<size_t>(iters) * 2 * n * kCoefThreads * sizeof(float);
-    w.hist_smem = hist <= static_cast<size_t>(kHistSmem) ? hist : 0;
-    const int64_t most = (w.hist_smem != 0 || iters == 0 ? 16 : 2) * static_cast<int64_t>(num_sms);
+    const bool in_smem = coef_smem(n, iters, true) <= static_cast<size_t>(kSmemMost);
+    w.coef_smem = coef_smem(n, iters, in_smem);
+    const int64_t most = (in_smem ? 16 : 2) * static_cast<int64_t>(num_sms);
     const int64_t need = (Bp + kCoefThreads - 1) / kCoefThreads;
     w.ctas = need < most ? need : most;
     w.dH_pre = reinterpret_cast<float *>(take(static_cast<size_t>(B) * n * 4));
@@ -412,7 +454,7 @@ Ws carve(void *base, int64_t B, int n, int64_t C, int iters, int num_sms)
                                          phi_image_bytes(n)));
     w.dY_terms = reinterpret_cast<uint16_t *>(take(static_cast<size_t>(Bp) * phi_term_rows(N) * 2));
     w.hist = nullptr;
-    if (w.hist_smem == 0 && iters > 0)
+    if (!in_smem)
         w.hist = reinterpret_cast<float *>(take(static_cast<size_t>(w.ctas) * hist));
     w.phi = take(phi_grad_workspace_bytes(B, n, C, num_sms));
     w.total = at;
@@ -437,11 +479,11 @@ cudaError_t launch_n(const PreBackwardArgs &a, const Ws &w, int num_sms, cudaStr
     static std::atomic<uint64_t> configured{0};
     e = once_per_device(configured, [] {
         return cudaFuncSetAttribute(coefs_kernel<n>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kHistSmem);
+                                    kSmemMost);
     });
     if (e != cudaSuccess) return e;
     e = launch_pdl(coefs_kernel<n>, dim3(static_cast<unsigned>(w.ctas)), dim3(kCoefThreads),
-                   w.hist_smem, stream, a, w.dH_pre, Bp, o);
+                   w.coef_smem, stream, a, w.dH_pre, Bp, o);
     if (e != cudaSuccess) return e;
     e = launch_streams(StreamsArgs{a.dX_next, a.dF_pre, w.phi_img, w.dY_rows, a.Xq, a.Xs, w.mix, a.B,
                                    Bp, a.C, a.dX}, n, num_sms, stream);
