@@ -16,7 +16,7 @@
 //          exchange between CTAs.  (Reading B ids per CTA is L2 traffic, a few
 //          percent of the time of the rows of dX that follow.)  Rows of its range that do not
 //          occur it sets to zero, so the table is written once.
-//   sum    the sorted list is cut into chunks of kChunk positions, whatever the
+//   sum    the sorted list is cut into chunks of 16 or 32 positions, whatever the
 //          ids, so every CTA has the same work.  A run of one id that lies in a
 //          chunk is written; a run that a chunk's edge cuts leaves its sums in
 //          the workspace (one before the edge, one after).
@@ -41,7 +41,7 @@ constexpr int kMaxGridY = 65535;
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxRange = 512;  // table rows of a sorting CTA, at most
-constexpr int kChunk = 16;      // sorted positions of a summing CTA
+constexpr int kMostChunk = 32;  // sorted positions of a summing CTA, at most
 
 __device__ __forceinline__ uint4 scaled8(const uint16_t *p, float scale)
 {
@@ -87,11 +87,16 @@ struct GradWs {
     int *last;    // [chunks]: where the run that starts in a chunk and is cut by its end, ends
                   // (a chunk), or -1 where there is none
     float *part;  // [chunks][2][C]: the run cut by the chunk's start, then by its end
+    int chunk;    // positions of a chunk
 };
 
-__host__ __device__ inline int64_t chunks_of(int64_t positions)
+// Positions of a chunk: 32 halve the cut runs' pieces (B=16384, C=4096: 187 us
+// against 191 with 16), 16 halve the chain of loads where there are few CTAs (64
+// tokens: 10 us against 12).
+int chunk_of(int64_t B, int64_t C) { return B * C >= (int64_t{1} << 24) ? kMostChunk : 16; }
+__host__ __device__ inline int64_t chunks_of(int64_t positions, int chunk)
 {
-    return (positions + kChunk - 1) / kChunk;
+    return (positions + chunk - 1) / chunk;
 }
 
 size_t carve(GradWs &w, void *base, int64_t B, int64_t C)
@@ -101,14 +106,15 @@ size_t carve(GradWs &w, void *base, int64_t B, int64_t C)
     size_t at = 0;
     w.count = reinterpret_cast<int *>(p + at);
     at += 256;
+    w.chunk = chunk_of(B, C);
     w.pos = reinterpret_cast<int *>(p + at);
     at += up(static_cast<size_t>(B) * 4);
     w.row = reinterpret_cast<int *>(p + at);
     at += up(static_cast<size_t>(B) * 4);
     w.last = reinterpret_cast<int *>(p + at);
-    at += up(static_cast<size_t>(chunks_of(B)) * 4);
+    at += up(static_cast<size_t>(chunks_of(B, w.chunk)) * 4);
     w.part = reinterpret_cast<float *>(p + at);
-    at += up(static_cast<size_t>(chunks_of(B)) * 2 * static_cast<size_t>(C) * 4);
+    at += up(static_cast<size_t>(chunks_of(B, w.chunk)) * 2 * static_cast<size_t>(C) * 4);
     return at;
 }
 
@@ -169,10 +175,10 @@ embed_sort_kernel(const int64_t *__restrict__ ids, int64_t V, int64_t B, int64_t
     if (r < rows) {
         int at = base + incl - cnt;
         // this row's positions are [at, at + cnt): each chunk whose end lies among them
-        const int k1 = (at + cnt - 1) / kChunk;
-        for (int k = at / kChunk; cnt > 0 && k <= k1; ++k)
-            if ((k + 1) * static_cast<int64_t>(kChunk) <= at + cnt && in_range(1413, k, 1, chunks_of(B)))
-                ws.last[k] = k == at / kChunk && k < k1 ? k1 : -1;
+        const int k1 = (at + cnt - 1) / ws.chunk;
+        for (int k = at / ws.chunk; cnt > 0 && k <= k1; ++k)
+            if ((k + 1) * static_cast<int64_t>(ws.chunk) <= at + cnt && in_range(1413, k, 1, chunks_of(B, ws.chunk)))
+                ws.last[k] = k == at / ws.chunk && k < k1 ? k1 : -1;
         for (int w = 0; w < kSortWarps; ++w) {
             const int c = hist[w][r];
             hist[w][r] = at;
@@ -231,20 +237,20 @@ __global__ void __launch_bounds__(256)
 embed_sum_kernel(const uint16_t *__restrict__ dX, float scale, int accumulate, int64_t V,
                  int64_t B, int64_t C, GradWs ws, float *__restrict__ dtable)
 {
-    __shared__ int pos[kChunk], row[kChunk + 2];  // row: one before and one after too
+    __shared__ int pos[kMostChunk], row[kMostChunk + 2];  // row: one before and one after too
     const int64_t C8 = C >> 3;
     const int64_t c8 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     ptx::pdl_wait();
     ptx::pdl_trigger();
-    const int count = *ws.count;
-    for (int64_t k = blockIdx.y; k * kChunk < count; k += gridDim.y) {
-        const int first = static_cast<int>(k * kChunk);
-        const int len = count - first < kChunk ? count - first : kChunk;
+    const int count = *ws.count, chunk = ws.chunk;
+    for (int64_t k = blockIdx.y; k * chunk < count; k += gridDim.y) {
+        const int first = static_cast<int>(k * chunk);
+        const int len = count - first < chunk ? count - first : chunk;
         __syncthreads();
-        if (threadIdx.x < kChunk + 2) {
-            const int p = first + static_cast<int>(threadIdx.x) - 1;
-            row[threadIdx.x] = p >= 0 && p < count ? ws.row[p] : -1;
-            if (threadIdx.x < len) pos[threadIdx.x] = ws.pos[first + threadIdx.x];
+        for (int x = threadIdx.x; x < chunk + 2; x += blockDim.x) {
+            const int p = first + x - 1;
+            row[x] = p >= 0 && p < count ? ws.row[p] : -1;
+            if (x < len) pos[x] = ws.pos[first + x];
         }
         __syncthreads();
         if (c8 >= C8) continue;
@@ -282,7 +288,7 @@ embed_sum_kernel(const uint16_t *__restrict__ dX, float scale, int accumulate, i
             if (begins && ends) {
                 if (in_range(1422, v, 1, V))
                     put8(dtable + static_cast<int64_t>(v) * C + c8 * 8, acc, scale, accumulate);
-            } else if (in_range(1423, 2 * k + 1, 1, 2 * chunks_of(B))) {
+            } else if (in_range(1423, 2 * k + 1, 1, 2 * chunks_of(B, ws.chunk))) {
                 put8(ws.part + (2 * k + (begins ? 1 : 0)) * C + c8 * 8, acc, 1.f, 0);
             }
             begins = true;
@@ -292,9 +298,9 @@ embed_sum_kernel(const uint16_t *__restrict__ dX, float scale, int accumulate, i
     }
 }
 
-// 32 lanes take 128 columns, and the 8 warps every 8th piece of the run each, so
-// that a run of a thousand positions is a few loads deep; the warps' sums are
-// added in warp order.
+// A warp per cut run and 128 columns.  Most cut runs are two or three pieces, so a
+// run is a short chain of loads and what counts is how many run at once; the pieces
+// of a long one (a thousand positions are 64) are loaded eight at a time.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinCols = 128;
 
@@ -302,57 +308,47 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 embed_join_kernel(float scale, int accumulate, int64_t V, int64_t B, int64_t C, GradWs ws,
                   float *__restrict__ dtable)
 {
-    __shared__ float4 sums[kJoinWarps][32];
     __shared__ int lasts[kJoinWarps * 32];
     __shared__ unsigned cut[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * kJoinCols + lane * 4;
     ptx::pdl_wait();
     ptx::pdl_trigger();
-    const int count = *ws.count;
+    const int count = *ws.count, chunk = ws.chunk;
     // a CTA takes every gridDim.y-th chunk; its threads look for the cut runs among them
-    const int64_t chunks = chunks_of(count);
+    const int64_t chunks = chunks_of(count, chunk);
     for (int64_t k0 = blockIdx.y; k0 < chunks; k0 += static_cast<int64_t>(gridDim.y) * kJoinWarps * 32) {
         const int64_t mine = k0 + static_cast<int64_t>(threadIdx.x) * gridDim.y;
-        const int l = (mine + 1) * kChunk < count ? ws.last[mine] : -1;
+        const int l = (mine + 1) * chunk < count ? ws.last[mine] : -1;
         const unsigned m = __ballot_sync(0xffffffffu, l >= 0);
         lasts[threadIdx.x] = l;
         if (lane == 0) cut[warp] = m;
         __syncthreads();
+        int turn = 0;
         for (int x = 0; x < kJoinWarps; ++x)
             for (unsigned left = cut[x]; left != 0; left &= left - 1) {
-                // the run that starts in chunk k and is cut by its end: its piece there, then one
-                // of each chunk up to `last`
+                if (turn++ % kJoinWarps != warp) continue;
+                // the run that starts in chunk k and is cut by its end: its piece there, then
+                // one of each chunk up to `last`
                 const int at = x * 32 + __ffs(left) - 1;
                 const int64_t k = k0 + static_cast<int64_t>(at) * gridDim.y, last = lasts[at];
-                const int v = ws.row[(k + 1) * kChunk];
-                const bool ok = c < C && in_range(1431, v, 1, V) && in_range(1432, last, 1, chunks_of(B));
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (ok) {
-#pragma unroll 4
-                    for (int64_t kk = k + warp; kk <= last; kk += kJoinWarps) {
-                        const float4 a = __ldcs(reinterpret_cast<const float4 *>(
-                            ws.part + (2 * kk + (kk == k ? 1 : 0)) * C + c));
-                        s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
-                    }
+                const int v = ws.row[(k + 1) * chunk];
+                if (c >= C || !in_range(1431, v, 1, V) || !in_range(1432, last, 1, chunks_of(B, ws.chunk))) continue;
+                const float4 *piece = reinterpret_cast<const float4 *>(ws.part + (2 * k + 2) * C + c);
+                const int64_t step = C / 2;  // float4s between the pieces of chunks
+                float4 s = __ldcs(reinterpret_cast<const float4 *>(ws.part + (2 * k + 1) * C + c));
+#pragma unroll 8
+                for (int64_t kk = k + 1; kk <= last; ++kk, piece += step) {
+                    const float4 a = __ldcs(piece);
+                    s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
                 }
-                sums[warp][lane] = s;
-                __syncthreads();
-                if (warp == 0 && ok) {
-#pragma unroll
-                    for (int w = 1; w < kJoinWarps; ++w) {
-                        const float4 a = sums[w][lane];
-                        s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
-                    }
-                    float4 *d = reinterpret_cast<float4 *>(dtable + v * C + c);
-                    s = make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
-                    if (accumulate) {
-                        const float4 x = *d;
-                        s = make_float4(x.x + s.x, x.y + s.y, x.z + s.z, x.w + s.w);
-                    }
-                    __stcs(d, s);
+                float4 *d = reinterpret_cast<float4 *>(dtable + v * C + c);
+                s = make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
+                if (accumulate) {
+                    const float4 x4 = *d;
+                    s = make_float4(x4.x + s.x, x4.y + s.y, x4.z + s.z, x4.w + s.w);
                 }
-                __syncthreads();
+                __stcs(d, s);
             }
         __syncthreads();
     }
@@ -408,7 +404,7 @@ cudaError_t launch_embed_backward(const uint16_t *dX, const int64_t *ids, float 
                                static_cast<int>(range), accumulate, ws, dtable);
     if (e != cudaSuccess) return e;
     const int threads = block_threads(C / 8);
-    const dim3 grid = col_grid(chunks_of(B), C / 8, threads);
+    const dim3 grid = col_grid(chunks_of(B, ws.chunk), C / 8, threads);
     switch (n) {
 #define MHC_CASE(k)                                                                           \
     case k:                                                                                   \
@@ -420,12 +416,11 @@ cudaError_t launch_embed_backward(const uint16_t *dX, const int64_t *ids, float 
 #undef MHC_CASE
     default: return cudaErrorInvalidValue;
     }
-    if (e != cudaSuccess || B <= kChunk) return e;  // one chunk cuts no run
-    // enough CTAs to fill the GPU once or twice
+    if (e != cudaSuccess || B <= ws.chunk) return e;  // one chunk cuts no run
     const int64_t strips = (C + kJoinCols - 1) / kJoinCols;
     const int64_t rows = 16 * num_sms / strips > 1 ? 16 * num_sms / strips : 1;
     const dim3 join(static_cast<unsigned>(strips),
-                    static_cast<unsigned>(rows < chunks_of(B) ? rows : chunks_of(B)));
+                    static_cast<unsigned>(rows < chunks_of(B, ws.chunk) ? rows : chunks_of(B, ws.chunk)));
     return launch_pdl(embed_join_kernel, join, dim3(kJoinWarps * 32), 0, stream, scale, accumulate,
                       V, B, C, ws, dtable);
 }

@@ -360,7 +360,8 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y,
 }
 
 // Adds each strip's parts in the order of the CTAs, which is that of the tokens.
-__global__ void __launch_bounds__(64)
+constexpr int kJoinCols = 4;  // columns of dφ_t that a CTA of 64 × 4 threads adds
+__global__ void __launch_bounds__(64 * kJoinCols)
 phi_join_kernel(const float *__restrict__ part, int N, int64_t K, Units un, int accumulate,
                 float *__restrict__ dphi_t)
 {
@@ -370,10 +371,11 @@ phi_join_kernel(const float *__restrict__ part, int N, int64_t K, Units un, int 
     const int first = un.owner(strip * un.blocks), last = un.owner((strip + 1) * un.blocks - 1);
     const int64_t q = strip * kStrip + threadIdx.x * 4;
     if (q >= K) return;
-    for (int k = blockIdx.y; k < N; k += gridDim.y) {
+    const int k = blockIdx.y * kJoinCols + threadIdx.y;
+    if (k < N) {
         if (!in_range(1311, k * K + q, 4, N * K) ||
             !in_range(1312, first + strip, last - first + 1, un.grid + un.total / un.blocks))
-            continue;
+            return;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int c = first; c <= last; ++c) {
@@ -426,7 +428,8 @@ cudaError_t launch_n(const CUtensorMap &tm, const uint8_t *Xq, const uint8_t *Xs
     if (e != cudaSuccess) return e;
     const int64_t K = n * C;
     return launch_pdl(phi_join_kernel,
-                      dim3(static_cast<unsigned>((K + kStrip - 1) / kStrip), Cfg<n>::N), dim3(64),
+                      dim3(static_cast<unsigned>((K + kStrip - 1) / kStrip),
+                           (Cfg<n>::N + kJoinCols - 1) / kJoinCols), dim3(64, kJoinCols),
                       0, stream, part, Cfg<n>::N, K, un, accumulate, dphi_t);
 }
 

@@ -291,11 +291,11 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
     };
     if (have_tok) {
 #pragma unroll
-        for (int x = 0; x < kDepth; ++x) load(slots[x], warp + x * kWarps);
-        for (int cg = warp; cg < groups; cg += kDepth * kWarps)
+        for (int x = 0; x < kDepth; ++x) load(slots[x], warp * kDepth + x);
+        for (int cg = warp * kDepth; cg < groups; cg += kDepth * kWarps)
 #pragma unroll
             for (int x = 0; x < kDepth; ++x)
-                if (cg + x * kWarps < groups) use(slots[x], cg + x * kWarps);
+                if (cg + x < groups) use(slots[x], cg + x);
     }
     if constexpr (kF32) {
         post[0] += __shfl_xor_sync(0xffffffffu, post[0], 1);

@@ -410,7 +410,8 @@ def make_ids(kind, V, B, seed):
 EMBED = [("zipf", 1, 1, 1, 8), ("ragged", 100, 15, 4, 72), ("zipf", 100, 16, 4, 72), ("same", 100, 17, 3, 40),
          ("same", 7, 100, 8, 136), ("padding", 50, 40, 2, 40), ("ragged", 1000, 300, 4, 256),
          ("zipf", 20, 700, 5, 72), ("zipf", 200003, 500, 1, 8), ("ragged", 5000, 2000, 2, 264),
-         ("ragged", 400, 33, 6, 1000), ("zipf", 64, 130, 7, 2056)]
+         ("ragged", 400, 33, 6, 1000), ("zipf", 64, 130, 7, 2056), ("ragged", 97, 70001, 1, 256),
+         ("zipf", 3000, 8200, 1, 2056), ("same", 3, 8200, 1, 2048)]
 
 
 @pytest.mark.parametrize("ft", [BF, F32])
