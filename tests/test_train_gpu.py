@@ -513,3 +513,68 @@ def test_empty_batches():
             assert bool((t == acc).all())
     mhc.mhc_embed(e(V, C, dtype=BF), e(0, dtype=torch.int64), 1.0, V, 0, n, C, e(0, n, C, dtype=BF))
     mhc.mhc_ckpt_pack(e(0, n, C, dtype=BF), 0, n, C, q, s)
+
+
+# ---------------------------------------------------------- large and whole
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values in X: the last tokens get what they get in a batch of 2500 (which sums
+    over channels in the same order)."""
+    B, n, C, tail, iters = 76001, 4, 7168, 65, 3
+    N, K = n * n + 2 * n, n * C
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s, dtype=F32, std=1.0: torch.randn(*s, device="cuda", generator=gen, dtype=dtype).mul_(std)  # noqa: E731
+    X, G, F = rnd(B, n, C, dtype=BF), rnd(B, n, C, dtype=BF, std=1e-2), rnd(B, C, dtype=BF)
+    phi, bias = rnd(N, K, dtype=BF, std=0.02), rnd(N, std=0.3)
+    Y, r = rnd(B, N), rnd(B).abs() + 0.5
+    hp, hq, hr = torch.rand(B, n, device="cuda", generator=gen), rnd(B, n).abs(), rnd(B, n, n).abs()
+    dhr, dhq = rnd(B, n, n), rnd(B, n)
+
+    def everything(lo):
+        b = B - lo
+        cut = lambda t: t[lo:].clone() if lo else t  # noqa: E731
+        q, s = mhc.alloc_kept(b, n, C)
+        nxt = torch.empty(b, n, C, dtype=BF, device="cuda")
+        mhc.mhc_post_res_apply_ckpt(cut(X), cut(F), cut(hr), cut(hq), b, n, C, nxt, q, s)
+        dF = torch.empty(b, C, dtype=BF, device="cuda")
+        g = [torch.empty(b, n, n, device="cuda"), torch.empty(b, n, device="cuda")]
+        mhc.mhc_post_res_apply_backward(cut(G), q, s, cut(F), cut(hq), b, n, C, dF, *g)
+        dX = torch.empty(b, n, C, dtype=BF, device="cuda")
+        mhc.mhc_pre_backward(cut(G), cut(F), q, s, phi, *ALPHA, bias, iters, cut(Y), cut(r), cut(hp), cut(hq),
+                             cut(hr), cut(dhr), cut(dhq), 0, b, n, C, dX, torch.empty(N, K, device="cuda"),
+                             torch.empty(N, device="cuda"), torch.empty(3, device="cuda"),
+                             mhc.pre_backward_workspace(b, n, C, iters))
+        return [t[b - tail:].clone() for t in (nxt, q, s, dF, *g, dX)]
+
+    for a, b in zip(everything(0), everything(B - 2500)):
+        assert torch.equal(a, b)
+
+
+def test_table_offsets_past_32_bits():
+    V, C, B, n = 300007, 7168, 40, 1  # 2.15e9 values
+    ids = torch.tensor([V - 1, V - 2, V - 1] + list(range(37)), device="cuda")
+    T = torch.empty(V, C, dtype=BF, device="cuda")
+    T[-2:] = normal(1, 2, C).cuda()
+    T[:37] = normal(2, 37, C).cuda()
+    X = torch.empty(B, n, C, dtype=BF, device="cuda")
+    mhc.mhc_embed(T, ids, 2.0, V, B, n, C, X)
+    assert torch.equal(X[:, 0], T[ids] * 2)
+    del T
+    dT = torch.empty(V, C, device="cuda")
+    mhc.mhc_embed_backward(X, ids, 0.5, 0, V, B, n, C, dT, mhc.embed_backward_workspace(V, B, n, C))
+    x = X[:, 0].float() * 0.5
+    assert torch.equal(dT[V - 1], x[0] + x[2]) and torch.equal(dT[V - 2], x[1])
+    assert torch.equal(dT[:37], x[3:]) and not bool(dT[37:V - 2].any())
+
+
+def test_the_training_example_learns():
+    import os
+    import sys
+
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import train_mhc
+
+    losses = train_mhc.train(steps=40)
+    assert abs(losses[0] - math.log(512)) < 1.0  # a uniform guess, nearly
+    assert losses[-1] < 0.5 * losses[0]
