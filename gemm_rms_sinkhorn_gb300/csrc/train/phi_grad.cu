@@ -360,13 +360,29 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y,
 }
 
 // Adds each strip's parts in the order of the CTAs, which is that of the tokens.
+// The CTAs past the strips add dbias and dα, a warp per value (in a launch of their
+// own they cost 2 us and a launch).
 constexpr int kJoinCols = 4;  // columns of dφ_t that a CTA of 64 × 4 threads adds
 __global__ void __launch_bounds__(64 * kJoinCols)
 phi_join_kernel(const float *__restrict__ part, int N, int64_t K, Units un, int accumulate,
-                float *__restrict__ dphi_t)
+                float *__restrict__ dphi_t, BiasSums bs)
 {
     ptx::pdl_wait();
     ptx::pdl_trigger();
+    const int64_t strips = un.total / un.blocks;
+    if (blockIdx.x >= strips) {
+        const int lane = threadIdx.x & 31;
+        const int k = blockIdx.y * 2 * kJoinCols + threadIdx.y * 2 + (threadIdx.x >> 5);
+        if (k >= N + 3 || !in_range(1313, k, 1, N + 3)) return;
+        float s = 0.f;
+        for (int c = lane; c < bs.ctas; c += 32) s += __ldcg(bs.part + static_cast<int64_t>(c) * (N + 3) + k);
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
+        if (lane != 0) return;
+        float *dst = k < N ? bs.dbias + k : bs.dalpha + (k - N);
+        *dst = accumulate ? *dst + s : s;
+        return;
+    }
     const int64_t strip = blockIdx.x;
     const int first = un.owner(strip * un.blocks), last = un.owner((strip + 1) * un.blocks - 1);
     const int64_t q = strip * kStrip + threadIdx.x * 4;
@@ -374,7 +390,7 @@ phi_join_kernel(const float *__restrict__ part, int N, int64_t K, Units un, int 
     const int k = blockIdx.y * kJoinCols + threadIdx.y;
     if (k < N) {
         if (!in_range(1311, k * K + q, 4, N * K) ||
-            !in_range(1312, first + strip, last - first + 1, un.grid + un.total / un.blocks))
+            !in_range(1312, first + strip, last - first + 1, un.grid + strips))
             return;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -405,7 +421,7 @@ Units make_units(int64_t B, int n, int64_t C, int num_sms)
 template <int n>
 cudaError_t launch_n(const CUtensorMap &tm, const uint8_t *Xq, const uint8_t *Xs, int64_t B,
                      int64_t C, const Units &un, int accumulate, float *dphi_t, float *part,
-                     cudaStream_t stream)
+                     const BiasSums &bs, cudaStream_t stream)
 {
     using Cf = Cfg<n>;
     static std::atomic<uint64_t> configured{0};
@@ -428,9 +444,9 @@ cudaError_t launch_n(const CUtensorMap &tm, const uint8_t *Xq, const uint8_t *Xs
     if (e != cudaSuccess) return e;
     const int64_t K = n * C;
     return launch_pdl(phi_join_kernel,
-                      dim3(static_cast<unsigned>((K + kStrip - 1) / kStrip),
-                           (Cfg<n>::N + kJoinCols - 1) / kJoinCols), dim3(64, kJoinCols),
-                      0, stream, part, Cfg<n>::N, K, un, accumulate, dphi_t);
+                      dim3(static_cast<unsigned>((K + kStrip - 1) / kStrip) + 1,
+                           (Cf::N + kJoinCols - 1) / kJoinCols), dim3(64, kJoinCols),
+                      0, stream, part, Cf::N, K, un, accumulate, dphi_t, bs);
 }
 
 }  // namespace
@@ -443,7 +459,7 @@ size_t phi_grad_workspace_bytes(int64_t B, int n, int64_t C, int num_sms)
 
 cudaError_t launch_phi_grad(const uint8_t *Xq, const uint8_t *Xs, const uint16_t *dY_terms,
                             int64_t B, int n, int64_t C, int accumulate, float *dphi_t,
-                            void *workspace, int num_sms, cudaStream_t stream)
+                            void *workspace, const BiasSums &bs, int num_sms, cudaStream_t stream)
 {
     const Units un = make_units(B, n, C, num_sms);
     CUtensorMap tm;
@@ -454,7 +470,7 @@ cudaError_t launch_phi_grad(const uint8_t *Xq, const uint8_t *Xs, const uint16_t
     float *part = static_cast<float *>(workspace);
     switch (n) {
 #define MHC_CASE(k) \
-    case k: return launch_n<k>(tm, Xq, Xs, B, C, un, accumulate, dphi_t, part, stream);
+    case k: return launch_n<k>(tm, Xq, Xs, B, C, un, accumulate, dphi_t, part, bs, stream);
         MHC_CASE(1) MHC_CASE(2) MHC_CASE(3) MHC_CASE(4) MHC_CASE(5) MHC_CASE(6) MHC_CASE(7)
         MHC_CASE(8)
 #undef MHC_CASE

@@ -402,23 +402,6 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
     }
 }
 
-// dbias and dα from the CTAs' sums: a warp per value.
-__global__ void __launch_bounds__(32)
-bias_join_kernel(const float *__restrict__ part, int ctas, int N, int accumulate,
-                 float *__restrict__ dbias, float *__restrict__ dalpha)
-{
-    ptx::pdl_wait();
-    ptx::pdl_trigger();
-    const int k = blockIdx.x, lane = threadIdx.x;
-    float s = 0.f;
-    for (int c = lane; c < ctas; c += 32) s += __ldcg(part + static_cast<int64_t>(c) * (N + 3) + k);
-#pragma unroll
-    for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
-    if (lane != 0) return;
-    float *dst = k < N ? dbias + k : dalpha + (k - N);
-    *dst = accumulate ? *dst + s : s;
-}
-
 // -------------------------------------------------------------- launches
 
 struct Ws {
@@ -464,7 +447,6 @@ Ws carve(void *base, int64_t B, int n, int64_t C, int iters, int num_sms)
 template <int n>
 cudaError_t launch_n(const PreBackwardArgs &a, const Ws &w, int num_sms, cudaStream_t stream)
 {
-    constexpr int N = n * n + 2 * n;
     const int64_t Bp = phi_grad_padded_tokens(a.B);
     // a warp a token once there are tokens for some warps on every SM, else a CTA a token
     const bool many = a.B >= 16 * static_cast<int64_t>(num_sms);
@@ -488,11 +470,9 @@ cudaError_t launch_n(const PreBackwardArgs &a, const Ws &w, int num_sms, cudaStr
     e = launch_streams(StreamsArgs{a.dX_next, a.dF_pre, w.phi_img, w.dY_rows, a.Xq, a.Xs, w.mix, a.B,
                                    Bp, a.C, a.dX}, n, num_sms, stream);
     if (e != cudaSuccess) return e;
-    e = launch_phi_grad(a.Xq, a.Xs, w.dY_terms, a.B, n, a.C, a.accumulate, a.dphi_t, w.phi,
-                        num_sms, stream);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(bias_join_kernel, dim3(N + 3), dim3(32), 0, stream, w.part,
-                      static_cast<int>(w.ctas), N, a.accumulate, a.dbias, a.dalpha);
+    const BiasSums bs{w.part, static_cast<int>(w.ctas), a.dbias, a.dalpha};
+    return launch_phi_grad(a.Xq, a.Xs, w.dY_terms, a.B, n, a.C, a.accumulate, a.dphi_t, w.phi, bs,
+                           num_sms, stream);
 }
 
 }  // namespace

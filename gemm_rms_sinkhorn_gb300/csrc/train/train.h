@@ -132,10 +132,17 @@ inline int64_t phi_grad_padded_tokens(int64_t B)
 {
     return (B + kPhiTokens - 1) / kPhiTokens * kPhiTokens;
 }
+// Sums of dH̃ by CTA of what formed it, [ctas][N + 3] (columns, then the α), which
+// the last launch adds up beside dφ's parts.
+struct BiasSums {
+    const float *part;
+    int ctas;
+    float *dbias, *dalpha;
+};
 size_t phi_grad_workspace_bytes(int64_t B, int n, int64_t C, int num_sms);
 cudaError_t launch_phi_grad(const uint8_t *Xq, const uint8_t *Xs, const uint16_t *dY_terms,
                             int64_t B, int n, int64_t C, int accumulate, float *dphi_t,
-                            void *workspace, int num_sms, cudaStream_t stream);
+                            void *workspace, const BiasSums &bs, int num_sms, cudaStream_t stream);
 cudaError_t read_and_clear_phi_grad_status(int *status);
 
 // ---- token ids to streams and back (embed.cu)
