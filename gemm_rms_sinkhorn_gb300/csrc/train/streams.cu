@@ -149,6 +149,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t a)
                  : "memory");
     return v;
 }
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
@@ -277,42 +283,33 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
             const uint32_t gs = ptx::smem_u32(ring + s * Cf::kStage + Cf::kBBytes);
             const uint32_t xs = gs + Cf::kGBytes, fs = xs + Cf::kXBytes;
             const uint32_t taddr = tmem + lane_base + static_cast<uint32_t>(a * Cf::NC);
-            uint4 xq[n];  // codes: 16 channels
+            constexpr int J = n <= 4 ? n : n == 5 ? 3 : 2;  // streams of dX formed together
 #pragma unroll
             for (int c8 = 0; c8 < kEach / 8; ++c8) {  // 8 channels at a time
                 const int cc = ch0 / 8 + c8;
                 const uint32_t at = swizzled<Cf::GB>(row, cc);
-                uint4 gv[n];
+                uint64_t gp[n][4], f[4];
 #pragma unroll
-                for (int i = 0; i < n; ++i) gv[i] = lds128(gs + i * (kTok * Cf::GB) + at);
-                const uint4 fv = lds128(fs + at);
-                if (c8 % 2 == 0) {
-                    if constexpr (kTmaX) {
-#pragma unroll
-                        for (int j = 0; j < n; ++j)
-                            xq[j] = lds128(xs + j * (kTok * W) + swizzled<W>(row, cc / 2));
-                    } else {
-                        // rows of codes are 8-byte aligned only
-                        const int64_t c = static_cast<int64_t>(chunk) * W + cc / 2 * 16;
-#pragma unroll
-                        for (int j = 0; j < n; ++j) {
-                            const uint8_t *p = Xq + (b * n + j) * C + c;
-                            const uint2 z = make_uint2(0, 0);
-                            const uint2 lo = b < B && c < C ? kept::ld_stream_v2(p) : z;
-                            const uint2 hi = b < B && c + 8 < C ? kept::ld_stream_v2(p + 8) : z;
-                            xq[j] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                        }
-                    }
-                }
-                uint64_t f[4];
-                unpack8_pairs(fv, f);
-                constexpr int J = n <= 4 ? n : n == 5 ? 3 : 2;  // streams of dX formed together
+                for (int i = 0; i < n; ++i) unpack8_pairs(lds128(gs + i * (kTok * Cf::GB) + at), gp[i]);
+                unpack8_pairs(lds128(fs + at), f);
 #pragma unroll
                 for (int j0 = 0; j0 < n; j0 += J) {
                     uint32_t p[J][8];
+                    uint2 q[J];
 #pragma unroll
                     for (int jj = 0; jj < J; ++jj)
-                        if (j0 + jj < n) tmem_ld_8(taddr + (j0 + jj) * W + cc * 8, p[jj]);
+                        if (j0 + jj < n) {
+                            tmem_ld_8(taddr + (j0 + jj) * W + cc * 8, p[jj]);
+                            if constexpr (kTmaX) {
+                                q[jj] = lds64(xs + (j0 + jj) * (kTok * W) + swizzled<W>(row, cc / 2) +
+                                              (cc & 1) * 8);
+                            } else {
+                                const int64_t c = static_cast<int64_t>(chunk) * W + cc * 8;
+                                q[jj] = b < B && c < C
+                                            ? kept::ld_stream_v2(Xq + (b * n + j0 + jj) * C + c)
+                                            : make_uint2(0, 0);
+                            }
+                        }
                     ptx::tmem_ld_wait();
                     uint64_t acc[J][4], w[4];
 #pragma unroll
@@ -327,13 +324,12 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
                         }
 #pragma unroll
                     for (int i = 0; i < n; ++i) {
-                        unpack8_pairs(gv[i], w);
 #pragma unroll
                         for (int jj = 0; jj < J; ++jj)
                             if (j0 + jj < n) {
                                 const uint64_t hh = f2_pack(h[(j0 + jj) * n + i], h[(j0 + jj) * n + i]);
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) acc[jj][x] = f2_fma(hh, w[x], acc[jj][x]);
+                                for (int x = 0; x < 4; ++x) acc[jj][x] = f2_fma(hh, gp[i][x], acc[jj][x]);
                             }
                     }
 #pragma unroll
@@ -341,8 +337,7 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
                         if (j0 + jj < n) {
                             const int j = j0 + jj;
                             const uint64_t ss = f2_pack(sc[j], sc[j]);
-                            kept::codes8_pairs((cc & 1) == 0 ? make_uint2(xq[j].x, xq[j].y)
-                                                           : make_uint2(xq[j].z, xq[j].w), w);
+                            kept::codes8_pairs(q[jj], w);
 #pragma unroll
                             for (int x = 0; x < 4; ++x) acc[jj][x] = f2_fma(ss, w[x], acc[jj][x]);
                             sts128(gs + j * (kTok * Cf::GB) + at, pack8_pairs(acc[jj]));
