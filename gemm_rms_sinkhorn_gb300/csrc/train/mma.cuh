@@ -1,5 +1,5 @@
-// The tensor product of bf16 values in registers (16 × 8 × 16) that the token
-// sums and the gradient's mixing use, and the transposition that goes with it.
+// The tensor product of bf16 values in registers (16 × 8 × 16) that the
+// residual update's backward uses, and the transposition that goes with it.
 #pragma once
 
 #include <cstdint>

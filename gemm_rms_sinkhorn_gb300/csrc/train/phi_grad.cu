@@ -4,17 +4,16 @@
 // one bf16 rounding of dY (2^-9) would not have.
 //
 // A tall, skinny product: K = nC rows (the channels), 3N columns, summed over
-// the tokens.  Bound by the bytes of the codes while N is small; at n = 8 (240
-// columns) by the tensor cores.  A CTA takes strips of 256 channels and blocks
+// the tokens.  A CTA takes strips of 256 channels and blocks
 // of 64 tokens, the (strip, block) units dealt out in equal contiguous ranges,
 // one CTA per SM:
 //
 //   warp 18     TMA: the codes (64 rows of 256 bytes) into a ring of their own, up
 //               to four units ahead;
 //   warps 0-15  read them there, write the bf16 values to a stage's A tile and hand
-//               it over.  (Loaded to registers ahead of use, the codes in flight
-//               held up the proxy fence that the hand-over needs: 180 us at
-//               B=16384, n=4, C=7168.)  The scales are loaded between hand-overs;
+//               it over.  (Codes loaded to registers ahead of use, in place of the
+//               ring: 180 us at B=16384, n=4, C=7168 against 158.)  The scales are
+//               loaded between hand-overs;
 //   warp 16     TMA: the dY terms of the block (B tile);
 //   warp 17     tcgen05.mma, M = 128 channels (two accumulators), N = 3n² + 6n
 //               columns padded to 48, K = 16 tokens.
@@ -28,6 +27,13 @@
 // Channels are contiguous in the codes, so A is written MN-major: a unit's tile
 // is [4 × 64 channels][8 × 8 tokens], each 64 × 8 part 1 KB with the 128-byte
 // swizzle.  A second launch adds the strips' parts in the order of the tokens.
+//
+// Time: B=16384, n=4, C=7168 158 us for 470 MB of codes (70 us at the copy rate);
+// B=8191, n=8, C=4096 112 us.  Bound by shared-memory traffic, some 132 KB a unit
+// (codes in and out, the A tile in, the tensor cores' reads of A and B), whose parts
+// add up: without decoding 121 us, with a quarter of the products 144, with neither
+// 86-91.  Decoding once for two accumulators' columns (157), a deeper B ring (167)
+// and A written K-major (188) gained nothing.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -379,6 +379,9 @@ int mhc_gemm_rms_noalloc(const mhc_bf16 *X, const mhc_bf16 *phi_t, int64_t B, in
  *   table [V][C] bf16 (mhc_embed_f32: fp32), ids [B] int64, X [B][n][C] bf16
  * An id outside [0, V) is padding: its streams are zero.  scale finite and
  * V >= 1 (MHC_ERR_INVALID), V < 2^31 (MHC_ERR_UNSUPPORTED).
+ * An all-zero token has r = 0, for which steps 1-4a and their backward are not
+ * finite, and the gradients of the weights are sums over the batch: leave
+ * padding out of the batch that the layers see.
  */
 int mhc_embed(const mhc_bf16 *table, const int64_t *ids, float scale, int64_t V, int64_t B, int n,
               int64_t C, mhc_bf16 *X, mhc_stream_t stream);
