@@ -74,14 +74,16 @@ struct Cfg {
     static constexpr int GB = W * 2;                   // bytes of a row of G
     static constexpr int kBBytes = NC * (RB + RB2), kGBytes = n * kTok * GB;
     static constexpr int kXBytes = n * kTok * W, kFBytes = kTok * GB;
-    static constexpr int kStage = kBBytes + kGBytes + kXBytes + kFBytes;
+    static constexpr int kStage = kGBytes + kXBytes + kFBytes;
     static constexpr bool kShareRegs = n >= 6;
     static constexpr int kABytes = kLanes * (RB + RB2);
-    static constexpr int kFit = (kRingBudget - kABytes) / kStage;
-    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    // buffers of φ: two where that costs no stage
+    static constexpr int fit(int phi) { return (kRingBudget - kABytes - phi * kBBytes) / kStage; }
+    static constexpr int kPhi = fit(2) == fit(1) || fit(2) >= 6 ? 2 : 1;
+    static constexpr int kStages = fit(kPhi) < 6 ? fit(kPhi) : 6;
     static constexpr int kAcc = 512 / NC < 4 ? 512 / NC : 4;  // accumulators in TMEM
     static constexpr int kEach = W / 2 / kGroups;      // channels of a thread
-    static constexpr int kSmem = 1024 + kABytes + kStages * kStage + 512;
+    static constexpr int kSmem = 1024 + kABytes + kPhi * kBBytes + kStages * kStage + 512;
     static_assert(kStages >= 2 && kAcc >= 2 && kSmem <= 227 * 1024, "shared memory, TMEM");
     static_assert(kStage % 1024 == 0 && kBBytes % 1024 == 0 && kABytes % 1024 == 0 &&
                   kXBytes % 1024 == 0, "swizzle atoms");
@@ -187,11 +189,12 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t *a_tile = smem, *ring = smem + Cf::kABytes;
+    uint8_t *a_tile = smem, *phi = smem + Cf::kABytes, *ring = phi + Cf::kPhi * Cf::kBBytes;
     uint64_t *full = reinterpret_cast<uint64_t *>(ring + Cf::kStages * Cf::kStage);
     uint64_t *empty = full + Cf::kStages, *done = empty + Cf::kStages;
     uint64_t *acc_full = done + Cf::kStages, *acc_empty = acc_full + Cf::kAcc;
-    uint64_t *a_full = acc_empty + Cf::kAcc, *a_empty = a_full + 1, *drain = a_empty + 1;
+    uint64_t *phi_full = acc_empty + Cf::kAcc, *phi_empty = phi_full + Cf::kPhi;
+    uint64_t *a_full = phi_empty + Cf::kPhi, *a_empty = a_full + 1, *drain = a_empty + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
@@ -209,6 +212,10 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
         for (int a = 0; a < Cf::kAcc; ++a) {
             ptx::mbar_init(&acc_full[a], 1);
             ptx::mbar_init(&acc_empty[a], 4 * kGroups);
+        }
+        for (int p = 0; p < Cf::kPhi; ++p) {
+            ptx::mbar_init(&phi_full[p], 1);
+            ptx::mbar_init(&phi_empty[p], 1);
         }
         ptx::mbar_init(a_full, 1);
         ptx::mbar_init(a_empty, 1);
@@ -280,7 +287,7 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
             const bool ok = wait(&full[s], it / Cf::kStages & 1) && wait(&acc_full[a], it / Cf::kAcc & 1);
             if (!__all_sync(0xffffffffu, ok)) break;  // what follows is warp-collective
             ptx::tc_fence_after();
-            const uint32_t gs = ptx::smem_u32(ring + s * Cf::kStage + Cf::kBBytes);
+            const uint32_t gs = ptx::smem_u32(ring + s * Cf::kStage);
             const uint32_t xs = gs + Cf::kGBytes, fs = xs + Cf::kXBytes;
             const uint32_t taddr = tmem + lane_base + static_cast<uint32_t>(a * Cf::NC);
             constexpr int J = n <= 4 ? n : n == 5 ? 3 : 2;  // streams of dX formed together
@@ -361,6 +368,17 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
             Unit un(u0, chunks);
             for (uint32_t it = 0; it < count; ++it, un.step(1)) {
                 const int32_t c0 = un.chunk * W, b0 = static_cast<int32_t>(un.tile * kTok);
+                const uint32_t s = it % Cf::kStages, p = it % Cf::kPhi;
+                if (!wait(&empty[s], (it / Cf::kStages & 1) ^ 1)) break;
+                uint8_t *st = ring + s * Cf::kStage;
+                ptx::mbar_arrive_expect_tx(&full[s], kTmaX ? Cf::kStage : Cf::kStage - Cf::kXBytes);
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
+                    tma_load_3d(st + i * (kTok * Cf::GB), &maps.g, c0, i, b0, &full[s], once);
+                    if constexpr (kTmaX)
+                        tma_load_3d(st + Cf::kGBytes + i * (kTok * W), &maps.x, c0, i, b0, &full[s], once);
+                }
+                ptx::tma_load_2d(st + Cf::kGBytes + Cf::kXBytes, &maps.f, c0, b0, &full[s], once);
                 if (un.tile != have_tile) {
                     have_tile = un.tile;
                     if (!wait(a_empty, (tiles & 1) ^ 1)) break;
@@ -373,20 +391,10 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
                                              b0, a_full, once);
                     }
                 }
-                const uint32_t s = it % Cf::kStages;
-                if (!wait(&empty[s], (it / Cf::kStages & 1) ^ 1)) break;
-                uint8_t *st = ring + s * Cf::kStage;
-                ptx::mbar_arrive_expect_tx(&full[s], kTmaX ? Cf::kStage : Cf::kStage - Cf::kXBytes);
-#pragma unroll 1
-                for (int i = 0; i < n; ++i) {
-                    tma_load_3d(st + Cf::kBBytes + i * (kTok * Cf::GB), &maps.g, c0, i, b0, &full[s], once);
-                    if constexpr (kTmaX)
-                        tma_load_3d(st + Cf::kBBytes + Cf::kGBytes + i * (kTok * W), &maps.x, c0, i, b0,
-                                    &full[s], once);
-                }
-                ptx::bulk_load(st, phi_img + static_cast<int64_t>(un.chunk) * Cf::kBBytes, Cf::kBBytes,
-                               &full[s], keep);
-                ptx::tma_load_2d(st + Cf::kBBytes + Cf::kGBytes + Cf::kXBytes, &maps.f, c0, b0, &full[s], once);
+                if (!wait(&phi_empty[p], (it / Cf::kPhi & 1) ^ 1)) break;
+                ptx::mbar_arrive_expect_tx(&phi_full[p], Cf::kBBytes);
+                ptx::bulk_load(phi + p * Cf::kBBytes, phi_img + static_cast<int64_t>(un.chunk) * Cf::kBBytes,
+                               Cf::kBBytes, &phi_full[p], keep);
             }
             // after an abort a copy may still be in flight: wait by the clock, far
             // longer than any copy takes
@@ -410,22 +418,23 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
                     if (!(ok = wait(a_full, tiles & 1))) break;
                     ++tiles;
                 }
-                const uint32_t s = it % Cf::kStages, a = it % Cf::kAcc;
+                const uint32_t p = it % Cf::kPhi, a = it % Cf::kAcc;
                 if (!(ok = wait(&acc_empty[a], (it / Cf::kAcc & 1) ^ 1))) break;
-                if (!(ok = wait(&full[s], it / Cf::kStages & 1))) break;
+                if (!(ok = wait(&phi_full[p], it / Cf::kPhi & 1))) break;
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>(a * Cf::NC);
                 const uint64_t ad = desc_k_major<Cf::RB>(ptx::smem_u32(a_tile));
-                const uint64_t bd = desc_k_major<Cf::RB>(ptx::smem_u32(ring + s * Cf::kStage));
+                const uint64_t bd = desc_k_major<Cf::RB>(ptx::smem_u32(phi + p * Cf::kBBytes));
                 constexpr int kMain = Cf::RB2 != 0 ? 4 : Cf::kCols / 16;
 #pragma unroll
                 for (int k = 0; k < kMain; ++k) ptx::mma_bf16(d, ad + 2 * k, bd + 2 * k, idesc, k > 0);
                 if constexpr (Cf::RB2 != 0)
                     ptx::mma_bf16(d, desc_k_major<32>(ptx::smem_u32(a_tile + kLanes * Cf::RB)),
-                                  desc_k_major<32>(ptx::smem_u32(ring + s * Cf::kStage + Cf::NC * Cf::RB)),
+                                  desc_k_major<32>(ptx::smem_u32(phi + p * Cf::kBBytes + Cf::NC * Cf::RB)),
                                   idesc, 1);
+                if (it + Cf::kPhi < count) ptx::mma_commit(&phi_empty[p]);
+                if (it + 1 < count && un.chunk + 1 == chunks) ptx::mma_commit(a_empty);
                 ptx::mma_commit(&acc_full[a]);
-                if (it + 1 == count || un.chunk + 1 == chunks) ptx::mma_commit(a_empty);
             }
             if (!ok || *abort) {  // every MMA issued has to end before TMEM is freed
                 ptx::mma_commit(drain);
@@ -444,7 +453,7 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
 #pragma unroll 1
                 for (int j = 0; j < n; ++j)
                     tma_store_3d(&maps.dx, c0, j, static_cast<int32_t>(un.tile * kTok),
-                                 ring + s * Cf::kStage + Cf::kBBytes + j * (kTok * Cf::GB));
+                                 ring + s * Cf::kStage + j * (kTok * Cf::GB));
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 ptx::mbar_arrive(&empty[s]);
