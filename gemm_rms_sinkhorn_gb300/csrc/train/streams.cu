@@ -252,16 +252,25 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         float h[n * n], hp[n], sx = 0.f;  // h[j·n + i] = H_res[i][j]
         int64_t have_tile = -1;
-        // the next unit, whose scales are loaded a turn ahead
+        // The next unit's scales, loaded a turn ahead; four blocks at a time where a row
+        // of them can be read in words (a byte each touches as many lines).
+        const bool words = nb % 4 == 0;
         Unit at_E(u0, chunks);
         uint32_t E[n], it_E = 0;
         const auto load_E = [&] {
             const int64_t b = at_E.tile * kTok + row;
-            const int64_t blk = (at_E.chunk * W + ch0) / 32;
+            const int blk = (at_E.chunk * W + ch0) / 32;
+            if (!words || it_E == 0 || blk % 4 < (W + 31) / 32) {
+                const bool in = it_E < count && b < B && blk < nb;
+                const int64_t at = b * n * nb + (words ? blk / 4 * 4 : blk);
 #pragma unroll
-            for (int j = 0; j < n; ++j)
-                E[j] = it_E < count && b < B && blk < nb && in_range(1241, (b * n + j) * nb + blk, 1, B * n * nb)
-                           ? __ldg(Xs + (b * n + j) * nb + blk) : kept::kScaleMin;
+                for (int j = 0; j < n; ++j) {
+                    E[j] = kept::kScaleMin * 0x01010101u;
+                    if (in && in_range(1241, at + j * nb, words ? 4 : 1, B * n * nb))
+                        E[j] = words ? __ldg(reinterpret_cast<const uint32_t *>(Xs + at + j * nb))
+                                     : __ldg(Xs + at + j * nb);
+                }
+            }
             at_E.step(1);
             ++it_E;
         };
@@ -279,9 +288,10 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
                 for (int k = 0; k < n; ++k) hp[k] = in ? __ldg(mix + (n * n + k) * Bp + b) : 0.f;
                 sx = in ? __ldg(mix + (n * n + n) * Bp + b) : 0.f;
             }
+            const int byte = words ? (chunk * W + ch0) / 32 % 4 * 8 : 0;
             float sc[n];
 #pragma unroll
-            for (int j = 0; j < n; ++j) sc[j] = sx * kept::scale_value(E[j]);
+            for (int j = 0; j < n; ++j) sc[j] = sx * kept::scale_value(E[j] >> byte & 0xFF);
             load_E();
             const uint32_t s = it % Cf::kStages, a = it % Cf::kAcc;
             const bool ok = wait(&full[s], it / Cf::kStages & 1) && wait(&acc_full[a], it / Cf::kAcc & 1);
