@@ -8,8 +8,9 @@
 // contiguous range of units, the channels of a token tile in order.
 //
 //   warp 8    TMA loads of a unit into a stage of the ring: G and the codes (a
-//             box per stream), dF, and φ for those n·W channels (one bulk copy of
-//             an image laid out beforehand);
+//             box per stream) and dF; and φ for those n·W channels (one bulk copy of
+//             an image laid out beforehand) into a buffer of its own, which is free
+//             again after the product;
 //   warp 9    tcgen05.mma, N = n·W channels, K = N_coef padded to 16: dY·φ into
 //             TMEM, whose lanes are the tokens, each twice (M = 128): lanes 0-63
 //             are read for the lower half of the channels, 64-127 for the upper;
@@ -19,18 +20,23 @@
 //             nothing is exchanged.  dX overwrites G in the stage;
 //   warp 10   TMA stores of dX, and hands the stage back.
 //
-// How it came to this (dX alone at B=16384, n=4, C=7168, against 385 us for its
-// bytes).  With the operands read from global memory in the layout of warp-level
-// products, a 128-bit request touches 8 lines and L1 is at its limit: 623 us.
-// With 128 tokens × 32 channels by TMA, rows are 64 bytes (32 of codes): L2 lines
-// were evicted between a row's chunks under evict_first (2.5 GB read in place of
-// 1.7): 640 us, and 490 without that hint.  Now 445; the copies alone, with the
-// mixing taken out, take 416.  Copying with cp.async in four warps in place of TMA:
-// 494.  A warp of its own for the scales, in place of a byte per thread and stream:
-// no faster (n = 8: 478 against 418 us).
+// Time: B=16384, n=4, C=7168 420-450 us (385 for its bytes; the copies alone, without
+// the mixing, 416-438); B=8191, n=8, C=4096 335-355 us (208 for its bytes, the copies
+// alone 260).  At n = 4 memory is the bound.  At n = 8 the copies take 1600 rows of 32
+// or 64 bytes a unit, at 2.8 clocks a row, and three stages do not hide a unit's load,
+// mixing and store from one another: 7/8 less arithmetic gave 28 us, no codes 31.
+//
+// How it came to this (B=16384, n=4, C=7168).  With the operands read from global
+// memory in the layout of warp-level products, a 128-bit request touches 8 lines and
+// L1 is at its limit: 623 us.  With 128 tokens × 32 channels by TMA, rows are 64 bytes
+// (32 of codes): L2 lines were evicted between a row's chunks under evict_first (2.5 GB
+// read in place of 1.7): 640 us, and 490 without that hint; 64 × 64: 450.  Copying with
+// cp.async in four warps in place of TMA: 494.  A warp of its own for the scales was no
+// faster; words of four scales were (n = 8: 355 -> 349), and φ outside the stages, which
+// left room for a third (n = 8: 374 -> 355).
 //
 // For n >= 6 a mixing thread needs more than its share of registers (H_res is 64 of
-// them at n = 8), and the other warps give theirs up (n = 8: 654 -> 418 us); up to
+// them at n = 8), and the other warps give theirs up (n = 8: 654 -> 418 us then); up to
 // n = 5 it does not, and the exchange costs 10 %.
 //
 // Codes can only be copied by TMA where C % 16 == 0 (16-byte row strides);
