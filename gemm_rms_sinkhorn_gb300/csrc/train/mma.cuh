@@ -29,15 +29,6 @@ __device__ __forceinline__ void mma_16816_new(float (&d)[4], uint32_t a0, uint32
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// With 8 k, without an addend: A rows g (a0) and g + 8 (a1) at k = 2t, 2t+1, B as b0.
-__device__ __forceinline__ void mma_1688_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0)
-{
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
-                 "{%4,%5}, {%6}, {%7,%7,%7,%7};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
-}
-
 // An 8 × 8 matrix of 16-bit values, row g at lanes 4g .. 4g+3 in column pairs,
 // to its transpose in the same layout.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v)

@@ -19,8 +19,8 @@
 //           operands of mma.m16n8k16: X's rows and, below them, F_out's against
 //           G's columns give dH_res and dH_post, on values that are exact in
 //           bf16; the block's scale multiplies the product of its 32 channels.
-//           dF_out is a product too, of H_post (three bf16 terms, 2^-26) with G
-//           transposed in registers.  tcgen05's smallest tile is 128 rows and
+//           dF_out is a product too, of G transposed in registers with H_post in
+//           three bf16 terms (2^-26).  tcgen05's smallest tile is 128 rows and
 //           has its operands in shared memory; this work is 8 rows a token.
 #include <cuda_runtime.h>
 
@@ -175,10 +175,12 @@ __device__ __forceinline__ void split3(float v, uint32_t &hi, uint32_t &mid, uin
     low = pack_bf16_rn(r - bf16_lo(mid), 0.f);
 }
 
-// At B=8192, n=8, C=4096 184 us, 5.2 TB/s; its bytes take 140.  Three CTAs an SM (80
-// registers) and two neighbouring channel groups read together; with a warp's groups
-// apart 206, and then two CTAs with two or four groups in flight 255 and 237, four
-// with one 211.  What bounds it is the latency of its loads at 24 warps an SM.
+// At B=8192, n=8, C=4096 180 us, 5.3 TB/s; its bytes take 140.  Three CTAs an SM (80
+// registers) and two neighbouring channel groups read together (two CTAs with four
+// groups 197, four with one 216; with a warp's groups apart 24 more).  G as the left
+// operand of dF_out's product takes two products a group; as the right operand, of
+// which H_post fills one row in 16, eight: 189.  What bounds it is the latency of its
+// loads at 24 warps an SM: a third fewer L1 wavefronts for the scales gained nothing.
 template <int n, typename FT>
 __global__ void __launch_bounds__(kWarps * 32, 3)
 post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *__restrict__ Xq,
@@ -201,18 +203,11 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
     const uint16_t *g_row = dX_next + (b * n + g) * C + t * 8;
     const uint8_t *q_row = Xq + (b * n + g) * C + t * 8, *s_row = Xs + (b * n + g) * nb;
     const FT *f_row = F_out + b * C + t * 8;
-    FT *df_row = dF_out + b * C + t * 8;
+    FT *df_row = dF_out + b * C;
 
-    // H_post as row 0 of a product's left operand: hi at k = 0 .. 7, mid at 8 .. 15; low apart
-    uint32_t h_hi = 0, h_mid = 0, h_low = 0;
-    if (g == 0 && have_tok) {
-        uint32_t a[3], c[3] = {0, 0, 0};
-        split3(2 * t < n ? __ldg(H_post + b * n + 2 * t) : 0.f, a[0], a[1], a[2]);
-        if (2 * t + 1 < n) split3(__ldg(H_post + b * n + 2 * t + 1), c[0], c[1], c[2]);
-        h_hi = __byte_perm(a[0], c[0], 0x5410);
-        h_mid = __byte_perm(a[1], c[1], 0x5410);
-        h_low = __byte_perm(a[2], c[2], 0x5410);
-    }
+    const float hp0 = have_tok && 2 * t < n ? __ldg(H_post + b * n + 2 * t) : 0.f;
+    const float hp1 = have_tok && 2 * t + 1 < n ? __ldg(H_post + b * n + 2 * t + 1) : 0.f;
+    const int c_out = g / 2 * 8 + t * 2 + g % 2;  // the channel of a group that the lane writes
 
     // kDepth groups are in flight: a slot is loaded again as soon as it is used
     struct Slot {
@@ -248,6 +243,16 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
             if (in && have_f) load_raw(x.f, f_row + cg * 32);
         }
     };
+    if (have_tok)
+#pragma unroll
+        for (int x = 0; x < kDepth; ++x) load(slots[x], warp * kDepth + x);
+    // H_post as a product's right operand: the even columns hi at k = 0 .. 7 and mid at
+    // 8 .. 15, the odd ones low, so that a lane's two columns add up to dF_out
+    uint32_t a[3], e[3];
+    split3(hp0, a[0], a[1], a[2]);
+    split3(hp1, e[0], e[1], e[2]);
+    const uint32_t h0 = g % 2 == 0 ? __byte_perm(a[0], e[0], 0x5410) : __byte_perm(a[2], e[2], 0x5410);
+    const uint32_t h1 = g % 2 == 0 ? __byte_perm(a[1], e[1], 0x5410) : 0;
     float acc[2] = {0.f, 0.f}, post[2] = {0.f, 0.f};
     const auto use = [&](Slot &s, int cg) {
         const uint4 x = kept::codes8_bf16(s.q);
@@ -275,25 +280,28 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
         }
         acc[0] = fmaf(d[0], scale, acc[0]);
         acc[1] = fmaf(d[1], scale, acc[1]);
-        // dF_out: word w of the group's lanes, channels 8t + 2w, + 1, transposed
+        // dF_out: G transposed is the left operand, its row r of word w the channel
+        // 8·(r/2) + 2w + r%2, against which every column pair holds H_post
+        uint32_t m[4];
         const uint32_t word[4] = {gw.x, gw.y, gw.z, gw.w};
-        float o[4][4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t m = transpose_8x8(word[w]);
-            mma_1688_new(o[w], h_low, 0u, m);
-            mma_16816(o[w], h_hi, 0u, h_mid, 0u, m, m);
-        }
-        if (g == 0 && cg * 32 + t * 8 < C) {
-            uint64_t df[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) df[w] = f2_pack(o[w][0], o[w][1]);
-            store8(df_row + cg * 32, df);
+        for (int w = 0; w < 4; ++w) m[w] = transpose_8x8(word[w]);
+        float o[2][4];
+        mma_16816_new(o[0], m[0], m[1], m[0], m[1], h0, h1);
+        mma_16816_new(o[1], m[2], m[3], m[2], m[3], h0, h1);
+        const float lo = t < 2 ? o[0][0] + o[0][1] : o[1][0] + o[1][1];
+        const float hi = t < 2 ? o[0][2] + o[0][3] : o[1][2] + o[1][3];
+        const float v = t % 2 == 0 ? lo : hi;  // word t
+        const int c = cg * 32 + c_out;
+        if constexpr (kF32) {
+            if (c < C) __stcs(df_row + c, v);
+        } else {
+            const float next = __shfl_xor_sync(0xffffffffu, v, 4);
+            if (g % 2 == 0 && c < C)
+                __stcs(reinterpret_cast<uint32_t *>(df_row + c), pack_bf16_rn(v, next));
         }
     };
     if (have_tok) {
-#pragma unroll
-        for (int x = 0; x < kDepth; ++x) load(slots[x], warp * kDepth + x);
         for (int cg = warp * kDepth; cg < groups; cg += kDepth * kWarps)
 #pragma unroll
             for (int x = 0; x < kDepth; ++x)

@@ -370,7 +370,8 @@ int mhc_gemm_rms_noalloc(const mhc_bf16 *X, const mhc_bf16 *phi_t, int64_t B, in
  * dphi_t, dbias, dalpha) fp32: with accumulate == 0 they are written whole,
  * otherwise added to.  B == 0 launches no kernel; it sets the weights'
  * gradients to zero when accumulate == 0.  All sums are fp32 in a fixed order:
- * results are bitwise reproducible for a given device and shape.
+ * results are bitwise reproducible for a given device and shape.  An infinity
+ * in an incoming gradient makes what depends on it infinite or NaN.
  */
 
 /*
