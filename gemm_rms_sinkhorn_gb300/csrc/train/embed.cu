@@ -24,6 +24,11 @@
 //
 // All sums are fp32 in the order of the positions, so results do not depend on
 // timing.  There are no atomics on sums.
+//
+// Both are bound by memory.  X at B=16384, n=4, C=7168 from 32000 fp32 rows: 170 us
+// (207 for its bytes if no id came twice; repeated rows come from L2); a token 1.7 us.
+// dT at B=16384, n=4, C=4096, V=32000: 190 us, its bytes take 156: sort with the zero
+// rows 75, sum 92, join 15 and the gaps between the launches; 64 tokens 9 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>

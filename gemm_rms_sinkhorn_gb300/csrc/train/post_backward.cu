@@ -13,7 +13,8 @@
 // do not depend on timing:
 //
 //   n <= 4  a lane takes 8 channels of all streams: n² + 2n packed multiply-adds
-//           a channel pair, accumulators in registers.
+//           a channel pair, accumulators in registers.  B=4096, n=4, C=4096, F in fp32:
+//           57 us, its bytes take 50; a token 4 us.
 //   n >= 5  those would be n² register pairs.  Here a warp takes 32 channels of
 //           all streams, stream g at lanes 4g .. 4g+3, 8 channels a lane, as the
 //           operands of mma.m16n8k16: X's rows and, below them, F_out's against
