@@ -45,15 +45,16 @@ namespace {
 
 // Bound by the codes' bytes.  A lane takes 8 channels of all n streams, so dF is
 // widened once for them; a block's scale multiplies its partial sum, not its
-// values.  W warps share a token.  B=16384, n=4, C=7168: 110 us, 6.5 TB/s; B=8191,
-// n=8, C=4096: 68 us with coefs beside it (its bytes take 50), at three CTAs an SM (80
-// registers); two 76, four, which spill, 77.
+// values.  W warps share a token.  As many CTAs an SM as spill next to nothing: B=16384,
+// n=4, C=7168 110 us, 6.5 TB/s, with five (48 registers), 147 with two; B=8191, n=8,
+// C=4096 68 us with three and coefs beside it (its bytes take 50), 76 with two, 77
+// with four, which spill.
 constexpr int kDotWarps = 8;
 
 //
 // The CTAs past the tokens' lay φ_t [N][K] out for the product dY·φ (train.h).
 template <int n, int W>
-__global__ void __launch_bounds__(kDotWarps * 32, n <= 4 ? 1 : 3)
+__global__ void __launch_bounds__(kDotWarps * 32, n <= 4 ? 5 : n == 5 ? 4 : 3)
 dots_kernel(const uint16_t *__restrict__ dF, const uint8_t *__restrict__ Xq,
             const uint8_t *__restrict__ Xs, const uint16_t *__restrict__ phi_t, int64_t B,
             int64_t C, unsigned dot_ctas, float *__restrict__ dH_pre,
