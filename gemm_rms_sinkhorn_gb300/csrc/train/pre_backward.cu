@@ -175,7 +175,7 @@ inline size_t coef_smem(int n, int iters, bool with_hist)
 
 struct CoefOut {
     float *mix;          // [mix_vals][padded tokens] (train.h)
-    uint16_t *dY_rows;   // [padded tokens][dy_cols] bf16, zeros past N
+    uint16_t *dY_rows;   // [kRowTerms][padded tokens][dy_cols] bf16, zeros past N
     uint16_t *dY_terms;  // bf16 terms of dY (train.h)
     float *part;         // [CTAs][N + 3]: Σ dH̃ by column, then by α
     float *hist;         // u_t, v_t: [CTAs][iters][2n][threads], or NULL: in shared memory
@@ -332,6 +332,7 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
         }
         float *mix = o.mix + b;
         uint4 *row = reinterpret_cast<uint4 *>(o.dY_rows + b * kCols);
+        uint4 *row_mid = reinterpret_cast<uint4 *>(o.dY_rows + (Bp + b) * kCols);
         const bool in = b < Bp && in_range(1212, b, 1, Bp);
         if (in) {
 #pragma unroll
@@ -340,10 +341,10 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
                 for (int j = 0; j < n; ++j) mix[(j * n + i) * Bp] = live ? row_H[i * n + j] : 0.f;
         }
         float sx = 0.f, da[3] = {0.f, 0.f, 0.f};
-        uint32_t packed[4] = {0, 0, 0, 0};
+        uint32_t packed[4] = {0, 0, 0, 0}, packed_mid[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < kCols; ++k) {
-            uint32_t hi = 0;
+            uint32_t hi = 0, mid = 0;
             if (k < N) {
                 float d = 0.f;  // dH̃ of column k
                 if (k < n) {
@@ -363,11 +364,12 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
                 const float dy = alpha * d * inv_r;
                 sx = fmaf(-dy, yk, sx);
                 sums[k * kS + threadIdx.x] = d;
-                // dY as one bf16 for dX, whose own rounding is as large, and as three
-                // for dφ, which is kept in fp32
+                // dY as two bf16 terms for dX, to 2^-16, where the sum that it enters is
+                // rounded to bf16 (one term, 2^-8, would show wherever φ's rows cancel),
+                // and as three for dφ, which is kept in fp32
                 hi = pack_bf16_rn(dy, 0.f) & 0xFFFFu;
                 const float rest = dy - bf16_lo(hi);
-                const uint32_t mid = pack_bf16_rn(rest, 0.f) & 0xFFFFu;
+                mid = pack_bf16_rn(rest, 0.f) & 0xFFFFu;
                 const uint32_t low = pack_bf16_rn(rest - bf16_lo(mid), 0.f) & 0xFFFFu;
                 if (in) {
                     uint16_t *dst = o.dY_terms + static_cast<int64_t>(phi_term_row(k, 0)) * Bp + b;
@@ -376,8 +378,13 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
                     dst[32 * Bp] = static_cast<uint16_t>(low);
                 }
             }
-            packed[k % 8 / 2] = k % 2 == 0 ? hi : packed[k % 8 / 2] | (hi << 16);
-            if (k % 8 == 7 && in) row[k / 8] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+            const int w = k % 8 / 2;
+            packed[w] = k % 2 == 0 ? hi : packed[w] | (hi << 16);
+            packed_mid[w] = k % 2 == 0 ? mid : packed_mid[w] | (mid << 16);
+            if (k % 8 == 7 && in) {
+                row[k / 8] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+                row_mid[k / 8] = make_uint4(packed_mid[0], packed_mid[1], packed_mid[2], packed_mid[3]);
+            }
         }
         if (in) mix[(n * n + n) * Bp] = sx * inv_r * inv_r * inv_K;
 #pragma unroll
@@ -435,7 +442,7 @@ Ws carve(void *base, int64_t B, int n, int64_t C, int iters, int num_sms)
     w.dH_pre = reinterpret_cast<float *>(take(static_cast<size_t>(B) * n * 4));
     w.mix = reinterpret_cast<float *>(take(static_cast<size_t>(Bp) * mix_vals(n) * 4));
     w.part = reinterpret_cast<float *>(take(static_cast<size_t>(w.ctas) * (N + 3) * 4));
-    w.dY_rows = reinterpret_cast<uint16_t *>(take(static_cast<size_t>(Bp) * dy_cols(n) * 2));
+    w.dY_rows = reinterpret_cast<uint16_t *>(take(static_cast<size_t>(Bp) * kRowTerms * dy_cols(n) * 2));
     w.phi_img = take(static_cast<size_t>((C + streams_width(n) - 1) / streams_width(n) *
                                          phi_image_bytes(n)));
     w.dY_terms = reinterpret_cast<uint16_t *>(take(static_cast<size_t>(Bp) * phi_term_rows(N) * 2));

@@ -8,10 +8,11 @@
 // contiguous range of units, the channels of a token tile in order.
 //
 //   warp 8    TMA loads of a unit into a stage of the ring: G and the codes (a
-//             box per stream) and dF; and φ for those n·W channels (one bulk copy of
-//             an image laid out beforehand) into a buffer of its own, which is free
-//             again after the product;
-//   warp 9    tcgen05.mma, N = n·W channels, K = N_coef padded to 16: dY·φ into
+//             box per stream) and dF;
+//   warp 11   φ for those n·W channels (one bulk copy of an image laid out beforehand)
+//             into a buffer of its own, which is free again after the product;
+//   warp 9    tcgen05.mma, N = n·W channels, K = N_coef padded to 16, for each of dY's
+//             two bf16 terms against the same φ: dY·φ into
 //             TMEM, whose lanes are the tokens, each twice (M = 128): lanes 0-63
 //             are read for the lower half of the channels, 64-127 for the upper;
 //   warps 0-7 two groups of four warps, each half of a lane's channels.  A thread
@@ -23,8 +24,14 @@
 // Time: B=16384, n=4, C=7168 420-450 us (385 for its bytes; the copies alone, without
 // the mixing, 416-438); B=8191, n=8, C=4096 335-355 us (208 for its bytes, the copies
 // alone 260).  At n = 4 memory is the bound.  At n = 8 the copies take 1600 rows of 32
-// or 64 bytes a unit, at 2.8 clocks a row, and three stages do not hide a unit's load,
+// or 64 bytes a unit, at 2.8 clocks a row, and the stages do not hide a unit's load,
 // mixing and store from one another: 7/8 less arithmetic gave 28 us, no codes 31.
+//
+// dY's second term (the first alone leaves 2^-8 of dY in the result) costs no time up to
+// n = 5 and 1 % of the backward at n = 6.  At n = 8 its rows take the third stage's
+// place; φ copied by a warp of its own, which no longer waits behind the stages, makes
+// up for that (the backward at B=8191, C=4096: 540 us with one term, three stages and
+// one warp for all copies, 518 so; φ in parts of two streams, with three stages, 586).
 //
 // How it came to this (B=16384, n=4, C=7168).  With the operands read from global
 // memory in the layout of warp-level products, a 128-bit request touches 8 lines and
@@ -32,8 +39,8 @@
 // (32 of codes): L2 lines were evicted between a row's chunks under evict_first (2.5 GB
 // read in place of 1.7): 640 us, and 490 without that hint; 64 × 64: 450.  Copying with
 // cp.async in four warps in place of TMA: 494.  A warp of its own for the scales was no
-// faster; words of four scales were (n = 8: 355 -> 349), and φ outside the stages, which
-// left room for a third (n = 8: 374 -> 355).
+// faster; words of four scales were (n = 8: 355 -> 349), and φ outside the stages
+// (n = 8: 374 -> 355).
 //
 // For n >= 6 a mixing thread needs more than its share of registers (H_res is 64 of
 // them at n = 8), and the other warps give theirs up (n = 8: 654 -> 418 us then); up to
@@ -82,7 +89,7 @@ struct Cfg {
     static constexpr int kXBytes = n * kTok * W, kFBytes = kTok * GB;
     static constexpr int kStage = kGBytes + kXBytes + kFBytes;
     static constexpr bool kShareRegs = n >= 6;
-    static constexpr int kABytes = kLanes * (RB + RB2);
+    static constexpr int kATerm = kLanes * (RB + RB2), kABytes = kRowTerms * kATerm;
     // buffers of φ: two where that costs no stage
     static constexpr int fit(int phi) { return (kRingBudget - kABytes - phi * kBBytes) / kStage; }
     static constexpr int kPhi = fit(2) == fit(1) || fit(2) >= 6 ? 2 : 1;
@@ -97,7 +104,7 @@ struct Cfg {
 };
 
 // Tensor maps: G and dX {C, n, B}, the codes {C, n, B}, dF {C, B} and dY {k,
-// tokens} (and from k = 64 on).
+// tokens, terms} (and from k = 64 on).
 struct Maps {
     CUtensorMap g, dx, x, f, y, y2;
 };
@@ -244,6 +251,14 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
         return false;
     };
 
+    // after an abort a copy may still be in flight: wait by the clock, far longer than
+    // any copy takes
+    const auto let_copies_land = [] {
+        const uint64_t t0 = ptx::globaltimer_ns();
+        for (int polls = 0; polls < (1 << 20) && ptx::globaltimer_ns() - t0 < 1000000; ++polls)
+            __nanosleep(200);
+    };
+
     if constexpr (Cf::kShareRegs) {
         if (warp < 8)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMix));
@@ -378,13 +393,13 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
     } else if (warp == 8) {
         // ------------------------------------------------------- TMA loads
         if (lane == 0) {
-            const uint64_t once = ptx::policy_evict_normal(), keep = ptx::policy_evict_last();
+            const uint64_t once = ptx::policy_evict_normal();
             int64_t have_tile = -1;
             uint32_t tiles = 0;
             Unit un(u0, chunks);
             for (uint32_t it = 0; it < count; ++it, un.step(1)) {
                 const int32_t c0 = un.chunk * W, b0 = static_cast<int32_t>(un.tile * kTok);
-                const uint32_t s = it % Cf::kStages, p = it % Cf::kPhi;
+                const uint32_t s = it % Cf::kStages;
                 if (!wait(&empty[s], (it / Cf::kStages & 1) ^ 1)) break;
                 uint8_t *st = ring + s * Cf::kStage;
                 ptx::mbar_arrive_expect_tx(&full[s], kTmaX ? Cf::kStage : Cf::kStage - Cf::kXBytes);
@@ -400,25 +415,30 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
                     if (!wait(a_empty, (tiles & 1) ^ 1)) break;
                     ++tiles;
                     ptx::mbar_arrive_expect_tx(a_full, Cf::kABytes);
-                    for (int h = 0; h < 2; ++h) {
-                        ptx::tma_load_2d(a_tile + h * kTok * Cf::RB, &maps.y, 0, b0, a_full, once);
+                    for (int h = 0; h < 2 * kRowTerms; ++h) {  // each term's rows, twice
+                        uint8_t *a = a_tile + h / 2 * Cf::kATerm;
+                        tma_load_3d(a + h % 2 * kTok * Cf::RB, &maps.y, 0, b0, h / 2, a_full, once);
                         if constexpr (Cf::RB2 != 0)
-                            ptx::tma_load_2d(a_tile + kLanes * Cf::RB + h * kTok * Cf::RB2, &maps.y2, 64,
-                                             b0, a_full, once);
+                            tma_load_3d(a + kLanes * Cf::RB + h % 2 * kTok * Cf::RB2, &maps.y2, 64, b0,
+                                        h / 2, a_full, once);
                     }
                 }
+            }
+            if (*abort) let_copies_land();
+        }
+    } else if (warp == 11) {
+        // ----------------------------------------------------- copies of φ
+        if (lane == 0) {
+            const uint64_t keep = ptx::policy_evict_last();
+            Unit un(u0, chunks);
+            for (uint32_t it = 0; it < count; ++it, un.step(1)) {
+                const uint32_t p = it % Cf::kPhi;
                 if (!wait(&phi_empty[p], (it / Cf::kPhi & 1) ^ 1)) break;
                 ptx::mbar_arrive_expect_tx(&phi_full[p], Cf::kBBytes);
                 ptx::bulk_load(phi + p * Cf::kBBytes, phi_img + static_cast<int64_t>(un.chunk) * Cf::kBBytes,
                                Cf::kBBytes, &phi_full[p], keep);
             }
-            // after an abort a copy may still be in flight: wait by the clock, far
-            // longer than any copy takes
-            if (*abort) {
-                const uint64_t t0 = ptx::globaltimer_ns();
-                for (int polls = 0; polls < (1 << 20) && ptx::globaltimer_ns() - t0 < 1000000; ++polls)
-                    __nanosleep(200);
-            }
+            if (*abort) let_copies_land();
         }
     } else if (warp == 9) {
         // ------------------------------------------------------------- MMA
@@ -439,15 +459,20 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
                 if (!(ok = wait(&phi_full[p], it / Cf::kPhi & 1))) break;
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>(a * Cf::NC);
-                const uint64_t ad = desc_k_major<Cf::RB>(ptx::smem_u32(a_tile));
-                const uint64_t bd = desc_k_major<Cf::RB>(ptx::smem_u32(phi + p * Cf::kBBytes));
+                const uint32_t b_at = ptx::smem_u32(phi + p * Cf::kBBytes);
+                const uint64_t bd = desc_k_major<Cf::RB>(b_at);
                 constexpr int kMain = Cf::RB2 != 0 ? 4 : Cf::kCols / 16;
 #pragma unroll
-                for (int k = 0; k < kMain; ++k) ptx::mma_bf16(d, ad + 2 * k, bd + 2 * k, idesc, k > 0);
-                if constexpr (Cf::RB2 != 0)
-                    ptx::mma_bf16(d, desc_k_major<32>(ptx::smem_u32(a_tile + kLanes * Cf::RB)),
-                                  desc_k_major<32>(ptx::smem_u32(phi + p * Cf::kBBytes + Cf::NC * Cf::RB)),
-                                  idesc, 1);
+                for (int term = kRowTerms - 1; term >= 0; --term) {  // the small one first
+                    const uint32_t a_at = ptx::smem_u32(a_tile + term * Cf::kATerm);
+                    const uint64_t ad = desc_k_major<Cf::RB>(a_at);
+#pragma unroll
+                    for (int k = 0; k < kMain; ++k)
+                        ptx::mma_bf16(d, ad + 2 * k, bd + 2 * k, idesc, term < kRowTerms - 1 || k > 0);
+                    if constexpr (Cf::RB2 != 0)
+                        ptx::mma_bf16(d, desc_k_major<32>(a_at + kLanes * Cf::RB),
+                                      desc_k_major<32>(b_at + Cf::NC * Cf::RB), idesc, 1);
+                }
                 if (it + Cf::kPhi < count) ptx::mma_commit(&phi_empty[p]);
                 if (it + 1 < count && un.chunk + 1 == chunks) ptx::mma_commit(a_empty);
                 ptx::mma_commit(&acc_full[a]);
@@ -493,13 +518,14 @@ cudaError_t launch_n(const StreamsArgs &s, int num_sms, cudaStream_t stream)
     using Cf = Cfg<n>;
     const bool tma_x = s.C % 16 == 0;
     Maps m;
-    const int64_t g_dims[3] = {s.C, n, s.B}, f_dims[2] = {s.C, s.B}, y_dims[2] = {Cf::kCols, s.Bp};
+    const int64_t g_dims[3] = {s.C, n, s.B}, f_dims[2] = {s.C, s.B};
+    const int64_t y_dims[3] = {Cf::kCols, s.Bp, kRowTerms};
     const int g_box[3] = {Cf::W, 1, kTok}, f_box[2] = {Cf::W, kTok};
-    const int y_box[2] = {Cf::RB / 2, kTok}, y2_box[2] = {16, kTok};
+    const int y_box[3] = {Cf::RB / 2, kTok, 1}, y2_box[3] = {16, kTok, 1};
     bool ok = encode_tensor(&m.g, 2, 3, s.dX_next, g_dims, g_box) && encode_tensor(&m.dx, 2, 3, s.dX, g_dims, g_box) &&
-              encode_tensor(&m.f, 2, 2, s.dF, f_dims, f_box) && encode_tensor(&m.y, 2, 2, s.dY_rows, y_dims, y_box);
+              encode_tensor(&m.f, 2, 2, s.dF, f_dims, f_box) && encode_tensor(&m.y, 2, 3, s.dY_rows, y_dims, y_box);
     if (ok && tma_x) ok = encode_tensor(&m.x, 1, 3, s.Xq, g_dims, g_box);
-    if (ok && Cf::RB2 != 0) ok = encode_tensor(&m.y2, 2, 2, s.dY_rows, y_dims, y2_box);
+    if (ok && Cf::RB2 != 0) ok = encode_tensor(&m.y2, 2, 3, s.dY_rows, y_dims, y2_box);
     if (!ok) return cudaErrorInvalidValue;
     if (!tma_x) m.x = m.g;  // not used
     if (Cf::RB2 == 0) m.y2 = m.y;

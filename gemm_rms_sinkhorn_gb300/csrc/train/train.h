@@ -99,6 +99,8 @@ __host__ __device__ constexpr int64_t phi_image_bytes(int n)  // of a chunk
 {
     return static_cast<int64_t>(n) * streams_width(n) * (phi_image_row(n) + phi_image_row2(n));
 }
+// dY as two bf16 terms that add up to it to 2^-16 of its size.
+constexpr int kRowTerms = 2;
 // What a row's 16-byte piece numbers are XORed with, in rows of `bytes`.
 __host__ __device__ constexpr int swizzle_xor(int bytes, int row)
 {
@@ -107,7 +109,7 @@ __host__ __device__ constexpr int swizzle_xor(int bytes, int row)
 struct StreamsArgs {
     const uint16_t *dX_next, *dF;
     const uint8_t *phi_img;    // [chunks][phi_image_bytes]
-    const uint16_t *dY_rows;   // [Bp][dy_cols], zeros past N
+    const uint16_t *dY_rows;   // [kRowTerms][Bp][dy_cols], zeros past N
     const uint8_t *Xq, *Xs;
     const float *mix;          // [mix_vals][Bp]
     int64_t B, Bp, C;          // Bp: tokens, padded

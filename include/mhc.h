@@ -441,7 +441,8 @@ int mhc_post_res_apply_backward_f32(const mhc_bf16 *dX_next, const uint8_t *Xq, 
  *   dX[j]     = Σ_i H_res[i][j]·dX_next[i] + H_pre[j]·dF_pre + Σ_k dY[k]·φ[k] + s·X[j]
  *   dphi_t[k] = Σ_b dY[b][k]·X[b],  dbias = Σ_b dH̃,  dalpha = Σ_b Σ_seg dH̃·Y/r
  * with X as it was kept, and Y, r, H_* as the forward wrote them for the same
- * phi_t, alphas, bias and iters.  dalpha is [3]: pre, post, res.  dX may be
+ * phi_t, alphas, bias and iters.  The products with dY are on the tensor cores, dY
+ * as bf16 terms that add up to it to 2^-16 for dX and 2^-25 for dphi_t.  dalpha is [3]: pre, post, res.  dX may be
  * exactly dX_next.  A token with r = 0 has gradients that are not finite, as
  * its coefficients are.  workspace: mhc_pre_backward_workspace_bytes on the
  * current device.
