@@ -360,7 +360,7 @@ decode_pre_kernel(const __grid_constant__ CUtensorMap tm_x,
         // while the Sinkhorn iteration runs; token_coeffs forms the same bits
         if (threadIdx.x < cnt * n) {
             const int j = threadIdx.x / n, i = threadIdx.x - j * n;
-            hps[threadIdx.x] = pre_coeff(yv[j * V + i], 1.0f / yv[j * V + N], a_pre, bias_s[i]);
+            hps[threadIdx.x] = pre_coeff(yv[j * V + i], inv_norm(yv[j * V + N]), a_pre, bias_s[i]);
         }
         __syncthreads();
         if (warp == kThreads / 32 - 1) {

@@ -430,7 +430,7 @@ fused_pre_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             if (pt < nrows * n) {
                 const int tk = pt / n, i = pt - (pt / n) * n;
                 const float *yrow = rows_buf + (rb * kMaxRows + tk) * stride;
-                hp_buf[tk * 8 + i] = pre_coeff(yrow[i], 1.0f / yrow[N], a_pre, bias[i]);
+                hp_buf[tk * 8 + i] = pre_coeff(yrow[i], inv_norm(yrow[N]), a_pre, bias[i]);
             }
             if (!pipe::group_sync(p, pre_bar, pre_phase)) break;
             if (pt == 0) ptx::mbar_arrive(&rows_empty[rb]);

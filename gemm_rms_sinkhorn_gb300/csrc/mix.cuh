@@ -35,8 +35,12 @@ __device__ __forceinline__ float sigmoid(float x)
     return recip_approx(fminf(1.0f + expf(-x), 3.0e38f));
 }
 
+// A token's 1/r.  A token of zeros has r = 0 and no direction: y/r is then taken as
+// 0, so its coefficients are those of the bias and padding stays finite.
+__device__ __forceinline__ float inv_norm(float r) { return r != 0.f ? 1.0f / r : 0.f; }
+
 // §2.3 + §2.4 for one pre entry: H_pre = σ(α_pre·y·(1/r) + b).  inv_r is the
-// token's 1/r; every caller forms it as 1.0f / r, so all get the same bits.
+// token's inv_norm(r) with every caller, so all get the same bits.
 __device__ __forceinline__ float pre_coeff(float y, float inv_r, float a_pre, float b)
 {
     return sigmoid(a_pre * y * inv_r + b);
@@ -71,7 +75,7 @@ __device__ __forceinline__ void token_coeffs(const float *y, float rb, const flo
                                              float a_pre, float a_post, float a_res, int iters,
                                              float (&hp)[n], float (&hq)[n], float (&m)[n][n])
 {
-    const float inv_r = 1.0f / rb;
+    const float inv_r = inv_norm(rb);
 #pragma unroll
     for (int i = 0; i < n; ++i) {
         hp[i] = pre_coeff(y[i], inv_r, a_pre, bias[i]);
@@ -173,7 +177,7 @@ __device__ __forceinline__ void token_coeffs_pair(const float *y, float rb, cons
     constexpr int h0 = n / 2, kR = n - n / 2;  // rows of half 0; rows of half 1
     const int i0 = half ? h0 : 0;
     const int cnt = half ? kR : h0;
-    const float inv_r = 1.0f / rb;
+    const float inv_r = inv_norm(rb);
     // the other half's partial of a column sum, added in tree_sum<n>'s order
     const auto col_total = [&](const float (&p)[kR]) {
         const float own = half ? tree_sum<kR>(p) : tree_sum<h0>(p);

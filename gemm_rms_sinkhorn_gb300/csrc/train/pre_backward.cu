@@ -9,7 +9,8 @@
 //           dH̃_post = dH_post·H_post·(1 − H_post/2)
 //           dH̃_res  = the Sinkhorn iteration's (below)
 //           dbias = Σ_b dH̃,  dα_seg = Σ_b Σ_{k in seg} dH̃·Y/r
-//           dY = α·dH̃/r,     s = −Σ_k dY·Y/(K·r²)       (r = sqrt(Σx²/K))
+//           dY = α·dH̃/r,     s = −Σ_k dY·Y/(K·r²)       (r = sqrt(Σx²/K);
+//                                                        r = 0: below)
 //   streams dX[j] = Σ_i H_res[i][j]·G[i] + H_pre[j]·dF + Σ_k dY[k]·φ[k] + s·X[j]
 //           (streams.cu)
 //   phi     dφ_t[k] = Σ_b dY[b][k]·X[b]                  (phi_grad.cu)
@@ -223,7 +224,7 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
          b0 += static_cast<int64_t>(gridDim.x) * kCoefThreads) {
         const int64_t b = b0 + threadIdx.x;
         const bool live = b < a.B && in_range(1211, b, 1, a.B);
-        const float inv_r = live ? 1.0f / __ldg(a.r + b) : 0.f;
+        const float r = live ? __ldg(a.r + b) : 0.f, inv_r = inv_norm(r);
         stage(b0);
         const float *y = rows + threadIdx.x * kRow, *row_D = y + N, *row_H = row_D + n * n;
         const float *row_hp = row_H + n * n, *row_hq = row_hp + n, *row_dq = row_hq + n;
@@ -386,7 +387,17 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
                 row_mid[k / 8] = make_uint4(packed_mid[0], packed_mid[1], packed_mid[2], packed_mid[3]);
             }
         }
-        if (in) mix[(n * n + n) * Bp] = sx * inv_r * inv_r * inv_K;
+        sx = sx * inv_r * inv_r * inv_K;
+        // A token of zeros (padding): the forward takes Y/r as 0, so φ and the α get nothing
+        // from it.  Its coefficients jump at X = 0; where they are asked to move, dX has no
+        // value, and nowhere else.
+        if (live && r == 0.f) {
+            bool moved = false;
+            for (int k = 0; k < N; ++k)
+                moved |= (k < n ? a.a_pre : k < 2 * n ? a.a_post : a.a_res) * sums[k * kS + threadIdx.x] != 0.f;
+            if (moved) sx = __int_as_float(0x7FC00000);
+        }
+        if (in) mix[(n * n + n) * Bp] = sx;
 #pragma unroll
         for (int e = 0; e < 3; ++e) sums[(N + e) * kS + threadIdx.x] = da[e];
         __syncthreads();

@@ -108,7 +108,7 @@ size_t mhc_workspace_bytes(int64_t B, int n, int64_t C);
  * X is read from HBM once: the square-sum is taken from the same on-chip
  * tiles that feed the tensor cores.  Results are bitwise reproducible for a
  * given device and shape (fixed split-K summation order).  A token whose row
- * is all zero gets r = 0 (its coefficients are then not finite).
+ * is all zero gets r = 0.
  */
 int mhc_gemm_rms(const mhc_bf16 *X, const mhc_bf16 *phi_t, int64_t B, int n, int64_t C,
                  float *Y, float *r, void *workspace, size_t workspace_bytes,
@@ -116,7 +116,8 @@ int mhc_gemm_rms(const mhc_bf16 *X, const mhc_bf16 *phi_t, int64_t B, int n, int
 
 /*
  * Steps 2–3 — coefficients (§2.3, §2.4; fusions §3.2, §3.3).
- *   H̃[b][k]   = α_seg·Y[b][k]/r[b] + bias[k]   (α_pre / α_post / α_res by column segment)
+ *   H̃[b][k]   = α_seg·Y[b][k]/r[b] + bias[k]   (α_pre / α_post / α_res by column segment;
+ *               bias[k] where r[b] = 0, a token of zeros)
  *   H_pre     = 1/(1+e^{-H̃_pre}),  H_post = 2/(1+e^{-H̃_post})
  *   H_res     = Sinkhorn–Knopp: start from exp(H̃_res) as an n×n matrix, then
  *               `iters` times divide each row by its sum, then each column
@@ -380,9 +381,9 @@ int mhc_gemm_rms_noalloc(const mhc_bf16 *X, const mhc_bf16 *phi_t, int64_t B, in
  *   table [V][C] bf16 (mhc_embed_f32: fp32), ids [B] int64, X [B][n][C] bf16
  * An id outside [0, V) is padding: its streams are zero.  scale finite and
  * V >= 1 (MHC_ERR_INVALID), V < 2^31 (MHC_ERR_UNSUPPORTED).
- * An all-zero token has r = 0, for which steps 1-4a and their backward are not
- * finite, and the gradients of the weights are sums over the batch: leave
- * padding out of the batch that the layers see.
+ * Padding may stay in the batch that the layers see: its coefficients are the
+ * bias's (r = 0, see mhc_coeffs), and where no gradient comes in for it, it adds
+ * nothing to the gradients of the weights.
  */
 int mhc_embed(const mhc_bf16 *table, const int64_t *ids, float scale, int64_t V, int64_t B, int n,
               int64_t C, mhc_bf16 *X, mhc_stream_t stream);
@@ -443,9 +444,10 @@ int mhc_post_res_apply_backward_f32(const mhc_bf16 *dX_next, const uint8_t *Xq, 
  * with X as it was kept, and Y, r, H_* as the forward wrote them for the same
  * phi_t, alphas, bias and iters.  The products with dY are on the tensor cores, dY
  * as bf16 terms that add up to it to 2^-16 for dX and 2^-25 for dphi_t.  dalpha is [3]: pre, post, res.  dX may be
- * exactly dX_next.  A token with r = 0 has gradients that are not finite, as
- * its coefficients are.  workspace: mhc_pre_backward_workspace_bytes on the
- * current device.
+ * exactly dX_next.  A token with r = 0 (zeros: padding) has dY = 0 and adds its dH̃
+ * to dbias alone; its dX is NaN if α·dH̃ is not zero there, for its coefficients
+ * jump at X = 0, and the first two terms otherwise.  workspace:
+ * mhc_pre_backward_workspace_bytes on the current device.
  */
 size_t mhc_pre_backward_workspace_bytes(int64_t B, int n, int64_t C, int iters);
 int mhc_pre_backward(const mhc_bf16 *dX_next, const mhc_bf16 *dF_pre, const uint8_t *Xq,
