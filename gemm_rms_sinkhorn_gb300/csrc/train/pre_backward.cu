@@ -20,14 +20,20 @@
 //
 // Sinkhorn.  With A = exp(H̃_res) (rows shifted by their maximum, which changes
 // no iterate), the iteration is u_t = 1/(A·v_{t−1}), v_t = 1/(Aᵀ·u_t), v_0 = 1,
-// H_res = diag(u_T)·A·diag(v_T).  The forward is run again, keeping the u_t and
-// v_t (2n values a step, not the n² of the iterate), and each step is undone:
+// H_res = diag(u_T)·A·diag(v_T).  With R_t = diag(u_t)·A·diag(v_{t−1}), whose rows
+// sum to 1, and P_t = diag(u_t)·A·diag(v_t), whose columns do, the gradients α of
+// log u and β of log v are undone step by step into E = dH̃_res:
 //
-//   dA = u·v·dH_res,  ū_i = Σ_j A·v·dH_res,  v̄_j = Σ_i u·A·dH_res
-//   for t = T … 1:  c̄ = −v̄·v_t²,            dA += u_t ⊗ c̄
-//                   r̄ = −(ū + A·c̄)·u_t²,    dA += r̄ ⊗ v_{t−1}
-//                   v̄ = Aᵀ·r̄,  ū = 0
-//   dH̃_res = dA·A                            (T = 0: dA = dH_res)
+//   E = P_T·dH_res,  α_i = Σ_j E,  β_j = Σ_i E
+//   for t = T … 1:  E −= P_t·β_j,   α_i −= Σ_j P_t·β_j
+//                   E −= R_t·α_i,   β_j = −Σ_i R_t·α_i,   α = 0
+//   (T = 0: E = A·dH_res)
+//
+// All factors are entries of the iterates, at most 1: wherever the forward is finite
+// so is this (in terms of u, v and A alone, u·v and the squares of u and v overflow
+// where H̃_res spreads by some 80).  The forward is run again, in the form that it has
+// for this n, and what it goes through is kept: up to n = 4 the R_t (P_t is R_t over
+// its column sums), else u_t and v_t, 2n values a step.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -160,18 +166,21 @@ dots_kernel(const uint16_t *__restrict__ dF, const uint8_t *__restrict__ Xq,
 // every request touches 32 lines), and the sums over tokens go back through it: by
 // shuffles, five dependent ones per column, they took as long as the iteration.  Up
 // to dH_pre nothing here depends on dots, so all that runs beside it.
-// (B=8191, n=8, in the backward: 42 us read from global memory, 37 so.)
+// (B=8191, n=8, in the backward: 42 us read from global memory, 37 so; 40 with the
+// iterates in place of u and v.)
 constexpr int kCoefThreads = 64;
 constexpr int kSmemMost = 200 * 1024;
 
 // A token's staged row: Y, dH_res, H_res, H_pre, H_post, dH_post.
 __host__ __device__ constexpr int coef_row(int n) { return (n * n + 2 * n + 2 * n * n + 3 * n) | 1; }
-// dH̃ by column and the α's sums, by token; and u_t, v_t of the iteration.
+// dH̃ by column and the α's sums, by token.
 __host__ __device__ constexpr int coef_sums(int n) { return (n * n + 2 * n + 3) * (kCoefThreads + 1); }
+// What is kept of a step: R_t, or u_t and v_t.
+__host__ __device__ constexpr int hist_vals(int n) { return n <= 4 ? n * n : 2 * n; }
 inline size_t coef_smem(int n, int iters, bool with_hist)
 {
     return sizeof(float) * (static_cast<size_t>(kCoefThreads) * coef_row(n) + coef_sums(n) +
-                            (with_hist ? static_cast<size_t>(iters) * 2 * n * kCoefThreads : 0));
+                            (with_hist ? static_cast<size_t>(iters) * hist_vals(n) * kCoefThreads : 0));
 }
 
 struct CoefOut {
@@ -179,7 +188,7 @@ struct CoefOut {
     uint16_t *dY_rows;   // [kRowTerms][padded tokens][dy_cols] bf16, zeros past N
     uint16_t *dY_terms;  // bf16 terms of dY (train.h)
     float *part;         // [CTAs][N + 3]: Σ dH̃ by column, then by α
-    float *hist;         // u_t, v_t: [CTAs][iters][2n][threads], or NULL: in shared memory
+    float *hist;         // [CTAs][iters][hist_vals][threads], or NULL: in shared memory
 };
 
 template <int n>
@@ -190,11 +199,10 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
     constexpr int kS = kCoefThreads + 1;
     extern __shared__ float smem_f[];
     float *rows = smem_f, *sums = rows + kCoefThreads * kRow;  // sums: [N + 3][kS]
-    float *hist = o.hist ? o.hist + static_cast<int64_t>(blockIdx.x) * a.iters * 2 * n * kCoefThreads
+    float *hist = o.hist ? o.hist + static_cast<int64_t>(blockIdx.x) * a.iters * hist_vals(n) * kCoefThreads
                          : sums + coef_sums(n);
     hist += threadIdx.x;
-    const auto u_at = [&](int t, int i) -> float & { return hist[(t * 2 * n + i) * kCoefThreads]; };
-    const auto v_at = [&](int t, int j) -> float & { return hist[(t * 2 * n + n + j) * kCoefThreads]; };
+    const auto h_at = [&](int t, int k) -> float & { return hist[(t * hist_vals(n) + k) * kCoefThreads]; };
     float total[(N + 3 + kCoefThreads - 1) / kCoefThreads] = {};  // of columns threadIdx.x, + 64
 
     // the rows of a token block, element by element in the order of global memory
@@ -228,7 +236,7 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
         stage(b0);
         const float *y = rows + threadIdx.x * kRow, *row_D = y + N, *row_H = row_D + n * n;
         const float *row_hp = row_H + n * n, *row_hq = row_hp + n, *row_dq = row_hq + n;
-        float A[n][n], dA[n][n];
+        float A[n][n], E[n][n];  // E: dH_res, then dH̃_res
         if (live) {
 #pragma unroll
             for (int i = 0; i < n; ++i)
@@ -236,7 +244,7 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
                 for (int j = 0; j < n; ++j) {
                     const int k = 2 * n + i * n + j;
                     A[i][j] = a.a_res * y[k] * inv_r + __ldg(a.bias + k);
-                    dA[i][j] = row_D[i * n + j];
+                    E[i][j] = row_D[i * n + j];
                 }
             if (a.iters > 0) {
 #pragma unroll
@@ -247,83 +255,156 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
 #pragma unroll
                     for (int j = 0; j < n; ++j) A[i][j] = expf(A[i][j] - mx);
                 }
-                float u[n], v[n], bu[n], bv[n];
+                // back from the iterate P = u·A·v: α and β are the gradients of log u and log v
+                float al[n], be[n];
+                const auto row_col_sums = [&] {
 #pragma unroll
-                for (int j = 0; j < n; ++j) v[j] = 1.0f;
-                for (int t = 0; t < a.iters; ++t) {
-#pragma unroll
-                    for (int i = 0; i < n; ++i) {
-                        float p[n];
-#pragma unroll
-                        for (int j = 0; j < n; ++j) p[j] = A[i][j] * v[j];
-                        u[i] = recip_approx(tree_sum<n>(p));
-                        u_at(t, i) = u[i];
-                    }
+                    for (int i = 0; i < n; ++i) al[i] = tree_sum<n>(E[i]);
 #pragma unroll
                     for (int j = 0; j < n; ++j) {
                         float p[n];
 #pragma unroll
-                        for (int i = 0; i < n; ++i) p[i] = u[i] * A[i][j];
-                        v[j] = recip_approx(tree_sum<n>(p));
-                        v_at(t, j) = v[j];
+                        for (int i = 0; i < n; ++i) p[i] = E[i][j];
+                        be[j] = tree_sum<n>(p);
                     }
-                }
-#pragma unroll
-                for (int i = 0; i < n; ++i) bu[i] = 0.f;
-#pragma unroll
-                for (int j = 0; j < n; ++j) bv[j] = 0.f;
-#pragma unroll
-                for (int i = 0; i < n; ++i)
-#pragma unroll
-                    for (int j = 0; j < n; ++j) {
-                        const float d = dA[i][j], av = A[i][j] * v[j];
-                        bu[i] = fmaf(av, d, bu[i]);
-                        bv[j] = fmaf(u[i] * A[i][j], d, bv[j]);
-                        dA[i][j] = u[i] * v[j] * d;
-                    }
-                for (int t = a.iters - 1; t >= 0; --t) {
-                    float c[n];
-#pragma unroll
-                    for (int j = 0; j < n; ++j) {
-                        const float vj = v_at(t, j);
-                        c[j] = -bv[j] * vj * vj;
-                    }
-#pragma unroll
-                    for (int j = 0; j < n; ++j) v[j] = t > 0 ? v_at(t - 1, j) : 1.0f;
-#pragma unroll
-                    for (int i = 0; i < n; ++i) {
-                        const float ui = u_at(t, i);
-                        float p[n];
-#pragma unroll
-                        for (int j = 0; j < n; ++j) {
-                            p[j] = A[i][j] * c[j];
-                            dA[i][j] = fmaf(ui, c[j], dA[i][j]);
-                        }
-                        u[i] = -(bu[i] + tree_sum<n>(p)) * ui * ui;  // r̄
-                        bu[i] = 0.f;
-                    }
-#pragma unroll
-                    for (int j = 0; j < n; ++j) {
-                        float p[n];
+                };
+                if constexpr (n <= 4) {
+                    for (int t = 0; t < a.iters; ++t) {
 #pragma unroll
                         for (int i = 0; i < n; ++i) {
-                            p[i] = A[i][j] * u[i];
-                            dA[i][j] = fmaf(u[i], v[j], dA[i][j]);
+                            const float inv = recip_approx(tree_sum<n>(A[i]));
+#pragma unroll
+                            for (int j = 0; j < n; ++j) h_at(t, i * n + j) = A[i][j] *= inv;
                         }
-                        bv[j] = tree_sum<n>(p);
+#pragma unroll
+                        for (int j = 0; j < n; ++j) {
+                            float p[n];
+#pragma unroll
+                            for (int i = 0; i < n; ++i) p[i] = A[i][j];
+                            const float inv = recip_approx(tree_sum<n>(p));
+#pragma unroll
+                            for (int i = 0; i < n; ++i) A[i][j] *= inv;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < n; ++i)
+#pragma unroll
+                        for (int j = 0; j < n; ++j) E[i][j] *= A[i][j];
+                    row_col_sums();
+                    float N_R[n][n], N_inv[n];  // R_t and 1 over its column sums, a step ahead
+                    const auto next = [&](int t) {
+#pragma unroll
+                        for (int i = 0; i < n; ++i)
+#pragma unroll
+                            for (int j = 0; j < n; ++j) N_R[i][j] = h_at(t, i * n + j);
+#pragma unroll
+                        for (int j = 0; j < n; ++j) {
+                            float p[n];
+#pragma unroll
+                            for (int i = 0; i < n; ++i) p[i] = N_R[i][j];
+                            N_inv[j] = recip_approx(tree_sum<n>(p));
+                        }
+                    };
+                    next(a.iters - 1);
+                    for (int t = a.iters - 1; t >= 0; --t) {
+                        float R[n][n], g[n];
+#pragma unroll
+                        for (int j = 0; j < n; ++j) {
+                            g[j] = N_inv[j] * be[j];
+#pragma unroll
+                            for (int i = 0; i < n; ++i) R[i][j] = N_R[i][j];
+                        }
+                        next(t > 0 ? t - 1 : 0);
+#pragma unroll
+                        for (int i = 0; i < n; ++i) {
+                            float p[n];
+#pragma unroll
+                            for (int j = 0; j < n; ++j) p[j] = R[i][j] * g[j];
+                            al[i] -= tree_sum<n>(p);
+#pragma unroll
+                            for (int j = 0; j < n; ++j) E[i][j] = fmaf(-R[i][j], g[j] + al[i], E[i][j]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < n; ++j) {
+                            float p[n];
+#pragma unroll
+                            for (int i = 0; i < n; ++i) p[i] = R[i][j] * al[i];
+                            be[j] = -tree_sum<n>(p);
+                        }
+#pragma unroll
+                        for (int i = 0; i < n; ++i) al[i] = 0.f;
+                    }
+                } else {
+                    float u[n], v[n];
+#pragma unroll
+                    for (int j = 0; j < n; ++j) v[j] = 1.0f;
+                    for (int t = 0; t < a.iters; ++t) {
+#pragma unroll
+                        for (int i = 0; i < n; ++i) {
+                            float p[n];
+#pragma unroll
+                            for (int j = 0; j < n; ++j) p[j] = A[i][j] * v[j];
+                            h_at(t, i) = u[i] = recip_approx(tree_sum<n>(p));
+                        }
+#pragma unroll
+                        for (int j = 0; j < n; ++j) {
+                            float p[n];
+#pragma unroll
+                            for (int i = 0; i < n; ++i) p[i] = __fmul_rn(u[i], A[i][j]);
+                            h_at(t, n + j) = v[j] = recip_approx(tree_sum<n>(p));
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < n; ++i)
+#pragma unroll
+                        for (int j = 0; j < n; ++j) E[i][j] *= (u[i] * A[i][j]) * v[j];
+                    row_col_sums();
+                    for (int t = a.iters - 1; t >= 0; --t) {
+                        // u and v are u_t and v_t; (u·A)·v before the gradient's factor, as u
+                        // and v may be large
+                        float to_v[n], to_u[n];
+#pragma unroll
+                        for (int k = 0; k < n; ++k) {
+                            to_v[k] = t > 0 ? h_at(t - 1, n + k) : 1.0f;
+                            to_u[k] = h_at(t > 0 ? t - 1 : 0, k);
+                        }
+#pragma unroll
+                        for (int i = 0; i < n; ++i)
+#pragma unroll
+                            for (int j = 0; j < n; ++j) {
+                                const float P = (u[i] * A[i][j]) * v[j];
+                                E[i][j] = fmaf(-P, be[j], E[i][j]);
+                                al[i] = fmaf(-P, be[j], al[i]);
+                            }
+#pragma unroll
+                        for (int j = 0; j < n; ++j) be[j] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < n; ++i)
+#pragma unroll
+                            for (int j = 0; j < n; ++j) {
+                                const float R = (u[i] * A[i][j]) * to_v[j];
+                                E[i][j] = fmaf(-R, al[i], E[i][j]);
+                                be[j] = fmaf(-R, al[i], be[j]);
+                            }
+#pragma unroll
+                        for (int k = 0; k < n; ++k) {
+                            al[k] = 0.f;
+                            v[k] = to_v[k];
+                            u[k] = to_u[k];
+                        }
                     }
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < n; ++i)
 #pragma unroll
-                    for (int j = 0; j < n; ++j) A[i][j] = expf(A[i][j]);
+                    for (int j = 0; j < n; ++j) E[i][j] *= expf(A[i][j]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < n; ++i)
 #pragma unroll
-                for (int j = 0; j < n; ++j) A[i][j] = dA[i][j] = 0.f;
+                for (int j = 0; j < n; ++j) E[i][j] = 0.f;
         }
 
         if (!waited) {
@@ -357,7 +438,7 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
                 } else if (k < 2 * n) {
                     if (live) d = row_dq[k - n] * row_hq[k - n] * (1.0f - 0.5f * row_hq[k - n]);
                 } else {
-                    d = dA[(k - 2 * n) / n][(k - 2 * n) % n] * A[(k - 2 * n) / n][(k - 2 * n) % n];
+                    d = E[(k - 2 * n) / n][(k - 2 * n) % n];
                 }
                 const float yk = live ? y[k] : 0.f;
                 const float alpha = k < n ? a.a_pre : k < 2 * n ? a.a_post : a.a_res;
@@ -444,7 +525,7 @@ Ws carve(void *base, int64_t B, int n, int64_t C, int iters, int num_sms)
     uint8_t *p = static_cast<uint8_t *>(base);
     size_t at = 0;
     const auto take = [&](size_t bytes) { uint8_t *r = p + at; at += up(bytes); return r; };
-    const size_t hist = static_cast<size_t>(iters) * 2 * n * kCoefThreads * sizeof(float);
+    const size_t hist = static_cast<size_t>(iters) * hist_vals(n) * kCoefThreads * sizeof(float);
     const bool in_smem = coef_smem(n, iters, true) <= static_cast<size_t>(kSmemMost);
     w.coef_smem = coef_smem(n, iters, in_smem);
     const int64_t most = (in_smem ? 16 : 2) * static_cast<int64_t>(num_sms);
