@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kCoefThreads)
 coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, CoefOut o)
 {
     constexpr int N = n * n + 2 * n, kCols = dy_cols(n), kRow = coef_row(n);
+    static_assert(int64_t{kMaxBackwardIters} * hist_vals(n) * kCoefThreads < int64_t{1} << 31, "h_at");
     constexpr int kS = kCoefThreads + 1;
     extern __shared__ float smem_f[];
     float *rows = smem_f, *sums = rows + kCoefThreads * kRow;  // sums: [N + 3][kS]

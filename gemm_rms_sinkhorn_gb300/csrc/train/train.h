@@ -76,6 +76,8 @@ struct PreBackwardArgs {
     uint16_t *dX;
     float *dphi_t, *dbias, *dalpha;
 };
+// The Sinkhorn steps' history, indexed in 32 bits, takes up to 16 values a step and thread of 64.
+constexpr int kMaxBackwardIters = (1 << 21) - 1;
 size_t pre_backward_workspace_bytes(int64_t B, int n, int64_t C, int iters, int num_sms);
 cudaError_t launch_pre_backward(const PreBackwardArgs &a, void *workspace, int num_sms,
                                 cudaStream_t stream);

@@ -223,7 +223,8 @@ int mhc_post_res_apply_backward_f32(const mhc_bf16 *dX_next, const uint8_t *Xq, 
 size_t mhc_pre_backward_workspace_bytes(int64_t B, int n, int64_t C, int iters)
 {
     DeviceInfo info;
-    if (check_shape(B, n, C, true) != MHC_OK || iters < 0 || B == 0) return 0;
+    if (check_shape(B, n, C, true) != MHC_OK || iters < 0 || iters > kMaxBackwardIters || B == 0)
+        return 0;
     if (current_device_info(&info) != cudaSuccess) return 0;
     return pre_backward_workspace_bytes(B, n, C, iters, info.num_sms);
 }
@@ -238,6 +239,7 @@ int mhc_pre_backward(const mhc_bf16 *dX_next, const mhc_bf16 *dF_pre, const uint
 {
     MHC_TRY(check_shape(B, n, C, true));
     if (iters < 0) return MHC_ERR_INVALID;
+    if (iters > kMaxBackwardIters) return MHC_ERR_UNSUPPORTED;
     const int N = num_coeffs(n);
     const int64_t K = n * C;
     Buf outs[] = {{dphi_t, f32_bytes(int64_t{N} * K)}, {dbias, f32_bytes(N)}, {dalpha, f32_bytes(3)},

@@ -442,8 +442,9 @@ int mhc_post_res_apply_backward_f32(const mhc_bf16 *dX_next, const uint8_t *Xq, 
  *   dX[j]     = Σ_i H_res[i][j]·dX_next[i] + H_pre[j]·dF_pre + Σ_k dY[k]·φ[k] + s·X[j]
  *   dphi_t[k] = Σ_b dY[b][k]·X[b],  dbias = Σ_b dH̃,  dalpha = Σ_b Σ_seg dH̃·Y/r
  * with X as it was kept, and Y, r, H_* as the forward wrote them for the same
- * phi_t, alphas, bias and iters.  The products with dY are on the tensor cores, dY
- * as bf16 terms that add up to it to 2^-16 for dX and 2^-25 for dphi_t.  dalpha is [3]: pre, post, res.  dX may be
+ * phi_t, alphas, bias and iters (iters < 2^21, else MHC_ERR_UNSUPPORTED).  The
+ * products with dY are on the tensor cores, dY as bf16 terms that add up to it to
+ * 2^-16 for dX and 2^-25 for dphi_t.  dalpha is [3]: pre, post, res.  dX may be
  * exactly dX_next.  A token with r = 0 (zeros: padding) has dY = 0 and adds its dH̃
  * to dbias alone; its dX is NaN if α·dH̃ is not zero there, for its coefficients
  * jump at X = 0, and the first two terms otherwise.  workspace:
