@@ -3,6 +3,7 @@
 // exception crosses this boundary and nothing here allocates device memory.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "host/args.h"
@@ -72,7 +73,7 @@ int zero_grads(const Buf *outs, int count, int accumulate, mhc_stream_t stream)
 int check_table(int64_t V, int64_t B, int n, int64_t C, float scale)
 {
     MHC_TRY(check_shape(B, n, C, true));
-    if (V < 1 || !(scale >= -3.0e38f && scale <= 3.0e38f)) return MHC_ERR_INVALID;
+    if (V < 1 || !std::isfinite(scale)) return MHC_ERR_INVALID;
     if (V >= (int64_t{1} << 31)) return MHC_ERR_UNSUPPORTED;
     return MHC_OK;
 }
