@@ -10,7 +10,12 @@
 // number, in fp32 and in bf16: the smallest step is 2^-9 · 2^-117 = 2^-126;
 // with 4 significant bits each is exact in bf16.  At the upper end a magnitude
 // over 240·2^120 is kept as that, for the next code would stand for 2^128, which
-// is infinite in both.  A block that holds an infinity or a NaN gets E = 255 and NaN codes: the whole block reads as NaN.
+// is infinite in both.  A block that holds an infinity or a NaN gets E = 255 and NaN
+// codes: the whole block reads as NaN.
+//
+// Off by at most: 2^-4 of a magnitude from 2^-6 times the scale on, below that (e4m3's
+// subnormals) 2^-10 times the scale.  With E > 10 amax is over 224 times the scale, so
+// the first holds within 2^-13 of amax (2^-6/224 = 2^-13.8), not further.
 #pragma once
 
 #include <cstdint>

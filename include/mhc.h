@@ -362,9 +362,10 @@ int mhc_gemm_rms_noalloc(const mhc_bf16 *X, const mhc_bf16 *phi_t, int64_t B, in
  * A value stands for code·2^(E-127); E is the smallest in [10, 247] with
  * amax <= 448·2^(E-127) over its block, so nothing saturates (but magnitudes over
  * 240·2^120, next to the end of bf16's range, which are kept as that) and every
- * value stood for is finite and exact in bf16.  Codes round to nearest even (relative 2^-4 at
- * most, for values within 2^-15 of the block's largest).  A block that holds an
- * infinity or a NaN is kept as NaN throughout (E = 255).
+ * value stood for is finite and exact in bf16.  Codes round to nearest even: a
+ * magnitude of 2^-6·2^(E-127) or more (with E > 10, all within 2^-13 of the block's
+ * largest) is off by 2^-4 of itself at most, a smaller one by 2^-10·2^(E-127).  A
+ * block that holds an infinity or a NaN is kept as NaN throughout (E = 255).
  *
  * Rules, layouts and status codes are those of the forward calls.  Gradients
  * have the types of what they are the gradients of, those of weights (dtable,
