@@ -100,6 +100,9 @@ _SIGS = {
     "mhc_testing_forward_decode_stalled": ([_vp, _vp, _vp, _f32, _f32, _f32, _vp, _i32, _i64,
                                             _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                             _sz, _vp, ctypes.c_uint64], _i32),
+    "mhc_testing_pre_backward_stalled": ([_vp, _vp, _vp, _vp, _vp, _f32, _f32, _f32, _vp, _i32] + [_vp] * 7 +
+                                         [_i32, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp,
+                                          _i32, _i64, ctypes.c_uint64], _i32),
     "mhc_testing_recip": ([_vp, _vp, _i64, _vp], _i32),
     "mhc_testing_host_chunks": ([_i64, _vp, _i64, ctypes.POINTER(_i64)], _i32),
     "mhc_testing_memory_checks": ([_i32], _i32),

@@ -78,6 +78,15 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     }
 }
 
+// For a kernel that gave up a wait: asynchronous copies that it issued may still be on
+// their way into shared memory, and a barrier whose other arrivals are missing cannot
+// tell.  Waits a millisecond by the clock, far longer than any copy takes.
+__device__ __forceinline__ void let_copies_land()
+{
+    const uint64_t t0 = globaltimer_ns();
+    for (int polls = 0; polls < (1 << 20) && globaltimer_ns() - t0 < 1000000; ++polls) __nanosleep(200);
+}
+
 // ------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ uint64_t policy_evict_first()

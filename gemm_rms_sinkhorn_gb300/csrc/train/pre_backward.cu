@@ -548,7 +548,8 @@ Ws carve(void *base, int64_t B, int n, int64_t C, int iters, int num_sms)
 }
 
 template <int n>
-cudaError_t launch_n(const PreBackwardArgs &a, const Ws &w, int num_sms, cudaStream_t stream)
+cudaError_t launch_n(const PreBackwardArgs &a, const Ws &w, int num_sms, cudaStream_t stream,
+                     const Waits &waits)
 {
     const int64_t Bp = phi_grad_padded_tokens(a.B);
     // a warp a token once there are tokens for some warps on every SM, else a CTA a token
@@ -571,11 +572,11 @@ cudaError_t launch_n(const PreBackwardArgs &a, const Ws &w, int num_sms, cudaStr
                    w.coef_smem, stream, a, w.dH_pre, Bp, o);
     if (e != cudaSuccess) return e;
     e = launch_streams(StreamsArgs{a.dX_next, a.dF_pre, w.phi_img, w.dY_rows, a.Xq, a.Xs, w.mix, a.B,
-                                   Bp, a.C, a.dX}, n, num_sms, stream);
+                                   Bp, a.C, a.dX}, n, num_sms, stream, waits);
     if (e != cudaSuccess) return e;
     const BiasSums bs{w.part, static_cast<int>(w.ctas), a.dbias, a.dalpha};
     return launch_phi_grad(a.Xq, a.Xs, w.dY_terms, a.B, n, a.C, a.accumulate, a.dphi_t, w.phi, bs,
-                           num_sms, stream);
+                           num_sms, stream, waits);
 }
 
 }  // namespace
@@ -586,12 +587,12 @@ size_t pre_backward_workspace_bytes(int64_t B, int n, int64_t C, int iters, int 
 }
 
 cudaError_t launch_pre_backward(const PreBackwardArgs &a, void *workspace, int num_sms,
-                                cudaStream_t stream)
+                                cudaStream_t stream, const Waits &waits)
 {
     const Ws w = carve(workspace, a.B, a.n, a.C, a.iters, num_sms);
     switch (a.n) {
 #define MHC_CASE(k) \
-    case k: return launch_n<k>(a, w, num_sms, stream);
+    case k: return launch_n<k>(a, w, num_sms, stream, waits);
         MHC_CASE(1) MHC_CASE(2) MHC_CASE(3) MHC_CASE(4) MHC_CASE(5) MHC_CASE(6) MHC_CASE(7)
         MHC_CASE(8)
 #undef MHC_CASE

@@ -60,6 +60,13 @@ cudaError_t launch_post_backward(const uint16_t *dX_next, const uint8_t *Xq, con
                                  FT *dF_out, float *dH_res, float *dH_post, int num_sms,
                                  cudaStream_t stream);
 
+// Every wait of the dX and dφ kernels gives up after limit_ns of GPU time.  For tests of
+// that, CTA 0 of one of them leaves its unit of this number without its copies.
+struct Waits {
+    uint64_t limit_ns = kWaitLimitNs;
+    int64_t stall_dx = -1, stall_dphi = -1;
+};
+
 // ---- backward of steps 1-4a (pre_backward.cu)
 struct PreBackwardArgs {
     const uint16_t *dX_next, *dF_pre;
@@ -80,7 +87,7 @@ struct PreBackwardArgs {
 constexpr int kMaxBackwardIters = (1 << 21) - 1;
 size_t pre_backward_workspace_bytes(int64_t B, int n, int64_t C, int iters, int num_sms);
 cudaError_t launch_pre_backward(const PreBackwardArgs &a, void *workspace, int num_sms,
-                                cudaStream_t stream);
+                                cudaStream_t stream, const Waits &waits);
 
 // ---- dX (streams.cu)
 // k of the product dY·φ, padded to the tensor instruction's 16
@@ -117,7 +124,8 @@ struct StreamsArgs {
     int64_t B, Bp, C;          // Bp: tokens, padded
     uint16_t *dX;
 };
-cudaError_t launch_streams(const StreamsArgs &s, int n, int num_sms, cudaStream_t stream);
+cudaError_t launch_streams(const StreamsArgs &s, int n, int num_sms, cudaStream_t stream,
+                           const Waits &waits);
 cudaError_t read_and_clear_streams_status(int *status);
 
 // ---- dφ (phi_grad.cu)
@@ -146,7 +154,8 @@ struct BiasSums {
 size_t phi_grad_workspace_bytes(int64_t B, int n, int64_t C, int num_sms);
 cudaError_t launch_phi_grad(const uint8_t *Xq, const uint8_t *Xs, const uint16_t *dY_terms,
                             int64_t B, int n, int64_t C, int accumulate, float *dphi_t,
-                            void *workspace, const BiasSums &bs, int num_sms, cudaStream_t stream);
+                            void *workspace, const BiasSums &bs, int num_sms, cudaStream_t stream,
+                            const Waits &waits);
 cudaError_t read_and_clear_phi_grad_status(int *status);
 
 // ---- token ids to streams and back (embed.cu)

@@ -8,6 +8,7 @@
 
 #include "host/args.h"
 #include "mhc.h"
+#include "mhc_testing.h"
 #include "train.h"
 
 using namespace mhc;
@@ -127,6 +128,33 @@ int post_backward_checked(const mhc_bf16 *dX_next, const uint8_t *Xq, const uint
                                             dH_res, dH_post, info.num_sms, cu(stream)));
 }
 
+int pre_backward_checked(const PreBackwardArgs &a, void *workspace, size_t workspace_bytes,
+                         mhc_stream_t stream, const Waits &waits)
+{
+    const int64_t B = a.B, C = a.C;
+    const int n = a.n;
+    MHC_TRY(check_shape(B, n, C, true));
+    if (a.iters < 0) return MHC_ERR_INVALID;
+    if (a.iters > kMaxBackwardIters) return MHC_ERR_UNSUPPORTED;
+    const int N = num_coeffs(n);
+    const int64_t K = n * C;
+    Buf outs[] = {{a.dphi_t, f32_bytes(int64_t{N} * K)}, {a.dbias, f32_bytes(N)},
+                  {a.dalpha, f32_bytes(3)}, {a.dX, bf16_bytes(B * K)}};
+    if (B == 0) return zero_grads(outs, 3, a.accumulate, stream);
+    const Buf ins[] = {{a.dX_next, bf16_bytes(B * K)}, {a.dF_pre, bf16_bytes(B * C)},
+                       {a.Xq, codes_bytes(B, n, C)}, {a.Xs, scales_bytes(B, n, C)},
+                       {a.phi_t, bf16_bytes(int64_t{N} * K)}, {a.bias, f32_bytes(N)},
+                       {a.Y, f32_bytes(B * N)}, {a.r, f32_bytes(B)}, {a.H_pre, f32_bytes(B * n)},
+                       {a.H_post, f32_bytes(B * n)}, {a.H_res, f32_bytes(B * n * n)},
+                       {a.dH_res, f32_bytes(B * n * n)}, {a.dH_post, f32_bytes(B * n)}};
+    Buf ws = {workspace, workspace_bytes};
+    DeviceInfo info;
+    MHC_TRY(check_buffers(
+        ins, 13, outs, 4, a.dX, a.dX_next, &ws,
+        [&](int sms) { return pre_backward_workspace_bytes(B, n, C, a.iters, sms); }, &info));
+    return cuda_status(launch_pre_backward(a, workspace, info.num_sms, cu(stream), waits));
+}
+
 }  // namespace
 
 extern "C" {
@@ -230,37 +258,35 @@ size_t mhc_pre_backward_workspace_bytes(int64_t B, int n, int64_t C, int iters)
     return pre_backward_workspace_bytes(B, n, C, iters, info.num_sms);
 }
 
-int mhc_pre_backward(const mhc_bf16 *dX_next, const mhc_bf16 *dF_pre, const uint8_t *Xq,
-                     const uint8_t *Xs, const mhc_bf16 *phi_t, float alpha_pre, float alpha_post,
-                     float alpha_res, const float *bias, int iters, const float *Y, const float *r,
-                     const float *H_pre, const float *H_post, const float *H_res,
-                     const float *dH_res, const float *dH_post, int accumulate, int64_t B, int n,
-                     int64_t C, mhc_bf16 *dX, float *dphi_t, float *dbias, float *dalpha,
-                     void *workspace, size_t workspace_bytes, mhc_stream_t stream)
+#define MHC_PRE_BACKWARD_ARGS                                                                     \
+    const mhc_bf16 *dX_next, const mhc_bf16 *dF_pre, const uint8_t *Xq, const uint8_t *Xs,        \
+        const mhc_bf16 *phi_t, float alpha_pre, float alpha_post, float alpha_res,                \
+        const float *bias, int iters, const float *Y, const float *r, const float *H_pre,         \
+        const float *H_post, const float *H_res, const float *dH_res, const float *dH_post,       \
+        int accumulate, int64_t B, int n, int64_t C, mhc_bf16 *dX, float *dphi_t, float *dbias,   \
+        float *dalpha, void *workspace, size_t workspace_bytes, mhc_stream_t stream
+#define MHC_PRE_BACKWARD_PASS                                                                     \
+    PreBackwardArgs{dX_next, dF_pre, Xq, Xs, phi_t, alpha_pre, alpha_post, alpha_res, bias,       \
+                    iters, Y, r, H_pre, H_post, H_res, dH_res, dH_post, accumulate != 0, B, n, C, \
+                    dX, dphi_t, dbias, dalpha},                                                   \
+        workspace, workspace_bytes, stream
+
+int mhc_pre_backward(MHC_PRE_BACKWARD_ARGS)
 {
-    MHC_TRY(check_shape(B, n, C, true));
-    if (iters < 0) return MHC_ERR_INVALID;
-    if (iters > kMaxBackwardIters) return MHC_ERR_UNSUPPORTED;
-    const int N = num_coeffs(n);
-    const int64_t K = n * C;
-    Buf outs[] = {{dphi_t, f32_bytes(int64_t{N} * K)}, {dbias, f32_bytes(N)}, {dalpha, f32_bytes(3)},
-                  {dX, bf16_bytes(B * K)}};
-    if (B == 0) return zero_grads(outs, 3, accumulate, stream);
-    const Buf ins[] = {{dX_next, bf16_bytes(B * K)}, {dF_pre, bf16_bytes(B * C)},
-                       {Xq, codes_bytes(B, n, C)}, {Xs, scales_bytes(B, n, C)},
-                       {phi_t, bf16_bytes(int64_t{N} * K)}, {bias, f32_bytes(N)},
-                       {Y, f32_bytes(B * N)}, {r, f32_bytes(B)}, {H_pre, f32_bytes(B * n)},
-                       {H_post, f32_bytes(B * n)}, {H_res, f32_bytes(B * n * n)},
-                       {dH_res, f32_bytes(B * n * n)}, {dH_post, f32_bytes(B * n)}};
-    Buf ws = {workspace, workspace_bytes};
-    DeviceInfo info;
-    MHC_TRY(check_buffers(
-        ins, 13, outs, 4, dX, dX_next, &ws,
-        [&](int sms) { return pre_backward_workspace_bytes(B, n, C, iters, sms); }, &info));
-    const PreBackwardArgs a{dX_next, dF_pre, Xq, Xs, phi_t, alpha_pre, alpha_post, alpha_res, bias,
-                            iters, Y, r, H_pre, H_post, H_res, dH_res, dH_post, accumulate != 0,
-                            B, n, C, dX, dphi_t, dbias, dalpha};
-    return cuda_status(launch_pre_backward(a, workspace, info.num_sms, cu(stream)));
+    return pre_backward_checked(MHC_PRE_BACKWARD_PASS, Waits{});
 }
+
+int mhc_testing_pre_backward_stalled(MHC_PRE_BACKWARD_ARGS, int kernel, int64_t stall_unit,
+                                     uint64_t wait_limit_ns)
+{
+    constexpr uint64_t lo = 1000000;
+    Waits w;
+    w.limit_ns = wait_limit_ns < lo ? lo : wait_limit_ns > kWaitLimitNs ? kWaitLimitNs : wait_limit_ns;
+    (kernel == 0 ? w.stall_dx : w.stall_dphi) = stall_unit;
+    return pre_backward_checked(MHC_PRE_BACKWARD_PASS, w);
+}
+
+#undef MHC_PRE_BACKWARD_ARGS
+#undef MHC_PRE_BACKWARD_PASS
 
 }  // extern "C"

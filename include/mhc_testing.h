@@ -31,6 +31,23 @@ int mhc_testing_gemm_rms_stalled(const mhc_bf16 *X, const mhc_bf16 *phi_t, int64
                                  uint64_t wait_limit_ns, mhc_stream_t stream);
 
 /*
+ * mhc_pre_backward with two changes of the same kind: CTA 0 of the dX kernel
+ * (kernel == 0) or of the dphi kernel (otherwise) leaves unit number `stall_unit`
+ * of its run without its copies (of dX_next, the codes and dF_pre, or of dY), and
+ * the waits of both give up after `wait_limit_ns` (clamped to [1 ms, 4 s]).  Status
+ * and context as above; the outputs are then not valid.  Argument rules and return
+ * codes are those of mhc_pre_backward; stall_unit < 0 stalls nothing.
+ */
+int mhc_testing_pre_backward_stalled(
+    const mhc_bf16 *dX_next, const mhc_bf16 *dF_pre, const uint8_t *Xq, const uint8_t *Xs,
+    const mhc_bf16 *phi_t, float alpha_pre, float alpha_post, float alpha_res, const float *bias,
+    int iters, const float *Y, const float *r, const float *H_pre, const float *H_post,
+    const float *H_res, const float *dH_res, const float *dH_post, int accumulate, int64_t B, int n,
+    int64_t C, mhc_bf16 *dX, float *dphi_t, float *dbias, float *dalpha, void *workspace,
+    size_t workspace_bytes, mhc_stream_t stream, int kernel, int64_t stall_unit,
+    uint64_t wait_limit_ns);
+
+/*
  * mhc_forward with steps 1-4a in one persistent kernel that reads X from HBM
  * once for both the projection GEMM and the pre-mixing: chunks of token tiles
  * small enough to stay in L2, several CTAs per tile with a deterministic
