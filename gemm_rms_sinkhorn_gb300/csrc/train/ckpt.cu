@@ -73,7 +73,7 @@ post_res_ckpt_kernel(const uint16_t *X, const FT *__restrict__ F_out,
         __syncthreads();  // the previous token's coefficients are no longer read
         for (int t = threadIdx.x; t < n * n + n; t += blockDim.x)
             if (tok_ok)
-                hs[t] = t < n * n ? __ldg(H_res + b * n * n + t) : __ldg(H_post + b * n + (t - n * n));
+                hs[t] = t < n * n ? ptx::ld_dep(H_res + b * n * n + t) : ptx::ld_dep(H_post + b * n + (t - n * n));
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < n; ++j) keep8(xv[j], ok, b * n + j, c8, C, nb, Xq, Xs);
@@ -134,7 +134,7 @@ ckpt_unpack_kernel(const uint8_t *__restrict__ Xq, const uint8_t *__restrict__ X
             E[k] = kept::kScaleMin;
             if (!ok[k]) continue;
             q[k] = kept::ld_stream_v2(Xq + (row + k) * C + c8 * 8);
-            E[k] = __ldg(Xs + (row + k) * nb + (c8 >> 2));
+            E[k] = ptx::ld_dep(Xs + (row + k) * nb + (c8 >> 2));
         }
 #pragma unroll
         for (int k = 0; k < kRows; ++k)

@@ -51,17 +51,18 @@ constexpr int kMostChunk = 32;  // sorted positions of a summing CTA, at most
 __device__ __forceinline__ uint4 scaled8(const uint16_t *p, float scale)
 {
     float f[8];
-    unpack8(__ldg(reinterpret_cast<const uint4 *>(p)), f);
+    unpack8(ptx::ld_dep_v4(p), f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] *= scale;
     return pack8(f);
 }
 __device__ __forceinline__ uint4 scaled8(const float *p, float scale)
 {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    const float f[8] = {a.x * scale, a.y * scale, a.z * scale, a.w * scale,
-                        b.x * scale, b.y * scale, b.z * scale, b.w * scale};
+    const uint4 a = ptx::ld_dep_v4(p), b = ptx::ld_dep_v4(p + 4);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(w[e]) * scale;
     return pack8(f);
 }
 
@@ -77,7 +78,7 @@ embed_kernel(const T *__restrict__ table, const int64_t *__restrict__ ids, float
     if (c8 >= C8) return;
     for (int64_t b = blockIdx.y; b < B; b += gridDim.y) {
         if (!in_range(1401, b, 1, B)) continue;
-        const int64_t id = __ldg(ids + b);
+        const int64_t id = ptx::ld_dep(ids + b);
         uint4 v = make_uint4(0, 0, 0, 0);
         if (id >= 0 && id < V) v = scaled8(table + id * C + c8 * 8, scale);
         uint16_t *x = X + b * n * C + c8 * 8;
@@ -146,7 +147,7 @@ embed_sort_kernel(const int64_t *__restrict__ ids, int64_t V, int64_t B, int64_t
     int below = 0, mine = 0;
 #pragma unroll 4
     for (int64_t b = lo + lane; b < hi; b += 32) {
-        const int64_t id = __ldg(ids + b);
+        const int64_t id = ptx::ld_dep(ids + b);
         below += id >= 0 && id < v0;
         if (id >= v0 && id < v1) {
             atomicAdd(&hist[warp][static_cast<int>(id - v0)], 1);
@@ -196,7 +197,7 @@ embed_sort_kernel(const int64_t *__restrict__ ids, int64_t V, int64_t B, int64_t
     if (mine > 0) {
         for (int64_t b0 = lo; b0 < hi; b0 += 32) {
             const int64_t b = b0 + lane;
-            const int64_t id = b < hi ? __ldg(ids + b) : -1;
+            const int64_t id = b < hi ? ptx::ld_dep(ids + b) : -1;
             const bool in = id >= v0 && id < v1;
             if (__ballot_sync(0xffffffffu, in) == 0) continue;
             const int key = in ? static_cast<int>(id - v0) : -1;
@@ -303,6 +304,13 @@ embed_sum_kernel(const uint16_t *__restrict__ dX, float scale, int accumulate, i
     }
 }
 
+__device__ __forceinline__ float4 stream_f4(const float *p)
+{
+    const uint4 v = ptx::ld_stream_v4(p);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                       __uint_as_float(v.w));
+}
+
 // A warp per cut run and 128 columns.  Most cut runs are two or three pieces, so a
 // run is a short chain of loads and what counts is how many run at once; the pieces
 // of a long one (a thousand positions are 64) are loaded eight at a time.
@@ -339,12 +347,11 @@ embed_join_kernel(float scale, int accumulate, int64_t V, int64_t B, int64_t C, 
                 const int64_t k = k0 + static_cast<int64_t>(at) * gridDim.y, last = lasts[at];
                 const int v = ws.row[(k + 1) * chunk];
                 if (c >= C || !in_range(1431, v, 1, V) || !in_range(1432, last, 1, chunks_of(B, ws.chunk))) continue;
-                const float4 *piece = reinterpret_cast<const float4 *>(ws.part + (2 * k + 2) * C + c);
-                const int64_t step = C / 2;  // float4s between the pieces of chunks
-                float4 s = __ldcs(reinterpret_cast<const float4 *>(ws.part + (2 * k + 1) * C + c));
+                const float *piece = ws.part + (2 * k + 2) * C + c;
+                float4 s = stream_f4(ws.part + (2 * k + 1) * C + c);
 #pragma unroll 8
-                for (int64_t kk = k + 1; kk <= last; ++kk, piece += step) {
-                    const float4 a = __ldcs(piece);
+                for (int64_t kk = k + 1; kk <= last; ++kk, piece += 2 * C) {
+                    const float4 a = stream_f4(piece);
                     s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
                 }
                 float4 *d = reinterpret_cast<float4 *>(dtable + v * C + c);

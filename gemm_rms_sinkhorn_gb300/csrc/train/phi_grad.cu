@@ -179,7 +179,7 @@ phi_grad_kernel(const __grid_constant__ CUtensorMap tm_y,
             for (int e = 0; e < kRowsEach; ++e, l_q += row_q, l_E += row_E) {
                 const bool ok = l_left > 0 && l_in && warp + kLoadWarps * e < rows &&
                                 in_range(1301, l_q - Xq, 8, B * K);
-                E[e] = ok ? __ldg(l_E) : kept::kScaleMin;
+                E[e] = ok ? ptx::ld_dep(l_E) : kept::kScaleMin;
                 if constexpr (!kTma) q[e] = ok ? kept::ld_stream_v2(l_q) : make_uint2(0, 0);
             }
             --l_left;
@@ -372,7 +372,7 @@ phi_join_kernel(const float *__restrict__ part, int N, int64_t K, Units un, int 
         const int k = blockIdx.y * 2 * kJoinCols + threadIdx.y * 2 + (threadIdx.x >> 5);
         if (k >= N + 3 || !in_range(1313, k, 1, N + 3)) return;
         float s = 0.f;
-        for (int c = lane; c < bs.ctas; c += 32) s += __ldcg(bs.part + static_cast<int64_t>(c) * (N + 3) + k);
+        for (int c = lane; c < bs.ctas; c += 32) s += ptx::ld_dep(bs.part + static_cast<int64_t>(c) * (N + 3) + k);
 #pragma unroll
         for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
         if (lane != 0) return;
@@ -392,9 +392,9 @@ phi_join_kernel(const float *__restrict__ part, int N, int64_t K, Units un, int 
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int c = first; c <= last; ++c) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                part + ((c + strip) * N + k) * kStrip + threadIdx.x * 4));
-            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            const uint4 v = ptx::ld_dep_v4(part + ((c + strip) * N + k) * kStrip + threadIdx.x * 4);
+            s.x += __uint_as_float(v.x); s.y += __uint_as_float(v.y);
+            s.z += __uint_as_float(v.z); s.w += __uint_as_float(v.w);
         }
         float4 *dst = reinterpret_cast<float4 *>(dphi_t + k * K + q);
         if (accumulate) {

@@ -97,7 +97,7 @@ post_backward_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *__rest
     const FT *f_row = F_out + b * C;
     float h[n];
 #pragma unroll
-    for (int i = 0; i < n; ++i) h[i] = have ? __ldg(H_post + b * n + i) : 0.f;
+    for (int i = 0; i < n; ++i) h[i] = have ? ptx::ld_dep(H_post + b * n + i) : 0.f;
 
     uint64_t acc[n][n], post[n];
 #pragma unroll
@@ -117,7 +117,7 @@ post_backward_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *__rest
         for (int i = 0; i < n; ++i) {
             gv[i] = ptx::ld_stream_v4(g_row + i * C + c8 * 8);
             q[i] = kept::ld_stream_v2(q_row + i * C + c8 * 8);
-            E[i] = __ldg(s_row + i * nb + (c8 >> 2));
+            E[i] = ptx::ld_dep(s_row + i * nb + (c8 >> 2));
         }
         load_raw(fr, f_row + c8 * 8);
         uint64_t g[n][4], f[4], df[4];
@@ -206,8 +206,8 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
     const FT *f_row = F_out + b * C + t * 8;
     FT *df_row = dF_out + b * C;
 
-    const float hp0 = have_tok && 2 * t < n ? __ldg(H_post + b * n + 2 * t) : 0.f;
-    const float hp1 = have_tok && 2 * t + 1 < n ? __ldg(H_post + b * n + 2 * t + 1) : 0.f;
+    const float hp0 = have_tok && 2 * t < n ? ptx::ld_dep(H_post + b * n + 2 * t) : 0.f;
+    const float hp1 = have_tok && 2 * t + 1 < n ? ptx::ld_dep(H_post + b * n + 2 * t + 1) : 0.f;
     const int c_out = g / 2 * 8 + t * 2 + g % 2;  // the channel of a group that the lane writes
 
     // kDepth groups are in flight: a slot is loaded again as soon as it is used
@@ -231,7 +231,7 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
             if (have) {
                 x.g = ptx::ld_stream_v4(g_row + cg * 32);
                 x.q = kept::ld_stream_v2(q_row + cg * 32);
-                x.E = __ldg(s_row + cg);
+                x.E = ptx::ld_dep(s_row + cg);
             }
             if (have_f) load_raw(x.f, f_row + cg * 32);
         } else if (cg < groups) {
@@ -239,7 +239,7 @@ post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *_
             x.g = in && have ? ptx::ld_stream_v4(g_row + cg * 32) : make_uint4(0, 0, 0, 0);
             x.q = in && have ? kept::ld_stream_v2(q_row + cg * 32) : make_uint2(0, 0);
             // every lane scales its row's sums, also where its own channels are past C
-            x.E = have ? __ldg(s_row + cg) : kept::kScaleMin;
+            x.E = have ? ptx::ld_dep(s_row + cg) : kept::kScaleMin;
             x.f.a = x.f.b = make_uint4(0, 0, 0, 0);
             if (in && have_f) load_raw(x.f, f_row + cg * 32);
         }

@@ -78,16 +78,19 @@ dots_kernel(const uint16_t *__restrict__ dF, const uint8_t *__restrict__ Xq,
         const int64_t j = q / C, c = q - j * C;
         const int row = static_cast<int>(j) * W + static_cast<int>(c % W);
         uint8_t *img = phi_img + c / W * phi_image_bytes(n);
+        uint32_t w[kCols / 2];  // all loads before the first store
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) {
+            const uint32_t v = k < N ? ptx::ld_dep(phi_t + k * K + q) : 0u;
+            w[k / 2] = k % 2 == 0 ? v : w[k / 2] | v << 16;
+        }
 #pragma unroll
         for (int k8 = 0; k8 < kCols / 8; ++k8) {
-            uint32_t v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = k8 * 8 + e < N ? __ldg(phi_t + (k8 * 8 + e) * K + q) : 0u;
             uint8_t *dst = k8 * 16 < RB ? img + row * RB + (k8 ^ swizzle_xor(RB, row)) * 16
                                         : img + n * W * RB + row * 32 +
                                               ((k8 - RB / 16) ^ swizzle_xor(32, row)) * 16;
             *reinterpret_cast<uint4 *>(dst) =
-                make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+                make_uint4(w[k8 * 4], w[k8 * 4 + 1], w[k8 * 4 + 2], w[k8 * 4 + 3]);
         }
         return;
     }
@@ -110,7 +113,7 @@ dots_kernel(const uint16_t *__restrict__ dF, const uint8_t *__restrict__ Xq,
 #pragma unroll
         for (int i = 0; i < n; ++i) {
             q[i] = in ? kept::ld_stream_v2(q_row + i * C + c8 * 8) : make_uint2(0, 0);
-            E[i] = in ? __ldg(s_row + i * nb + (c8 >> 2)) : kept::kScaleMin;
+            E[i] = in ? ptx::ld_dep(s_row + i * nb + (c8 >> 2)) : kept::kScaleMin;
         }
     };
     float s[n];
@@ -225,7 +228,7 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
         __syncthreads();
     };
     // (inputs: the kernel before this one does not write them, and lets this one start only
-    // when what preceded the call had finished)
+    // when what preceded the call had finished, so they may be read ahead of the wait)
     bool waited = false;
 
     const float inv_K = 1.0f / (static_cast<float>(n) * static_cast<float>(a.C));
@@ -413,6 +416,9 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
             ptx::pdl_trigger();
             waited = true;
         }
+        float dh[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i) dh[i] = live ? ptx::ld_dep(dH_pre + b * n + i) : 0.f;
         float *mix = o.mix + b;
         uint4 *row = reinterpret_cast<uint4 *>(o.dY_rows + b * kCols);
         uint4 *row_mid = reinterpret_cast<uint4 *>(o.dY_rows + (Bp + b) * kCols);
@@ -434,7 +440,7 @@ coefs_kernel(PreBackwardArgs a, const float *__restrict__ dH_pre, int64_t Bp, Co
                     if (live) {
                         const float h = row_hp[k];
                         mix[(n * n + k) * Bp] = h;
-                        d = __ldg(dH_pre + b * n + k) * h * (1.0f - h);
+                        d = dh[k] * h * (1.0f - h);
                     }
                 } else if (k < 2 * n) {
                     if (live) d = row_dq[k - n] * row_hq[k - n] * (1.0f - 0.5f * row_hq[k - n]);

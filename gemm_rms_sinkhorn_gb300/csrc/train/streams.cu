@@ -280,8 +280,8 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
                 for (int j = 0; j < n; ++j) {
                     E[j] = kept::kScaleMin * 0x01010101u;
                     if (in && in_range(1241, at + j * nb, words ? 4 : 1, B * n * nb))
-                        E[j] = words ? __ldg(reinterpret_cast<const uint32_t *>(Xs + at + j * nb))
-                                     : __ldg(Xs + at + j * nb);
+                        E[j] = words ? ptx::ld_dep(reinterpret_cast<const uint32_t *>(Xs + at + j * nb))
+                                     : ptx::ld_dep(Xs + at + j * nb);
                 }
             }
             at_E.step(1);
@@ -296,10 +296,10 @@ streams_kernel(const __grid_constant__ Maps maps, const uint8_t *__restrict__ ph
                 have_tile = un.tile;
                 const bool in = b < Bp && in_range(1242, b, 1, Bp);
 #pragma unroll
-                for (int k = 0; k < n * n; ++k) h[k] = in ? __ldg(mix + k * Bp + b) : 0.f;
+                for (int k = 0; k < n * n; ++k) h[k] = in ? ptx::ld_dep(mix + k * Bp + b) : 0.f;
 #pragma unroll
-                for (int k = 0; k < n; ++k) hp[k] = in ? __ldg(mix + (n * n + k) * Bp + b) : 0.f;
-                sx = in ? __ldg(mix + (n * n + n) * Bp + b) : 0.f;
+                for (int k = 0; k < n; ++k) hp[k] = in ? ptx::ld_dep(mix + (n * n + k) * Bp + b) : 0.f;
+                sx = in ? ptx::ld_dep(mix + (n * n + n) * Bp + b) : 0.f;
             }
             const int byte = words ? (chunk * W + ch0) / 32 % 4 * 8 : 0;
             float sc[n];
