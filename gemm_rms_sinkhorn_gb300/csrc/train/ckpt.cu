@@ -10,8 +10,10 @@
 // A thread owns 8 channels of one token in all n streams (128-bit accesses),
 // so four neighbouring lanes hold a block of 32 channels and find its largest
 // magnitude with two shuffles.  All kernels are bound by memory: at B=16384, n=4,
-// C=7168 the update with the codes takes 400 us, 6.5 TB/s (a copy runs at 6.8), and
-// unpacking 200, 7.1 TB/s.
+// C=7168 the update with the codes takes 384-400 us, 6.5-6.8 TB/s (a copy runs at 6.8),
+// unpacking 200, 7.1 TB/s, packing 206, 6.9.  At n >= 5 the update with the codes is
+// further from that: B=8192, n=8, C=4096 271 us, 5.2 TB/s (256 with F_out in fp32; the
+// update alone, whose kernel walks tokens, 170): a CTA a token and two an SM.
 #include <cuda_runtime.h>
 
 #include <cstdint>

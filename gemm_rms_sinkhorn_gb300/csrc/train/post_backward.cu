@@ -182,6 +182,7 @@ __device__ __forceinline__ void split3(float v, uint32_t &hi, uint32_t &mid, uin
 // operand of dF_out's product takes two products a group; as the right operand, of
 // which H_post fills one row in 16, eight: 189.  What bounds it is the latency of its
 // loads at 24 warps an SM: a third fewer L1 wavefronts for the scales gained nothing.
+// With F_out in fp32 215 us, its bytes take 160: every stream's lanes load F_out again.
 template <int n, typename FT>
 __global__ void __launch_bounds__(kWarps * 32, 3)
 post_backward_wide_kernel(const uint16_t *__restrict__ dX_next, const uint8_t *__restrict__ Xq,

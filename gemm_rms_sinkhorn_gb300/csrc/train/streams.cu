@@ -21,11 +21,12 @@
 //             nothing is exchanged.  dX overwrites G in the stage;
 //   warp 10   TMA stores of dX, and hands the stage back.
 //
-// Time: B=16384, n=4, C=7168 420-450 us (385 for its bytes; the copies alone, without
-// the mixing, 416-438); B=8191, n=8, C=4096 335-355 us (208 for its bytes, the copies
+// Time: B=16384, n=4, C=7168 421-445 us (385 for its bytes; the copies alone, without
+// the mixing, 416-438); B=8191, n=8, C=4096 315-319 us (208 for its bytes, the copies
 // alone 260).  At n = 4 memory is the bound.  At n = 8 the copies take 1600 rows of 32
-// or 64 bytes a unit, at 2.8 clocks a row, and the stages do not hide a unit's load,
-// mixing and store from one another: 7/8 less arithmetic gave 28 us, no codes 31.
+// or 64 bytes a unit, at 2.8 clocks a row, and two stages do not hide a unit's load,
+// mixing and store from one another (with three, when one warp made all copies, 7/8 less
+// arithmetic gave 28 us of 350, no codes 31).
 //
 // dY's second term (the first alone leaves 2^-8 of dY in the result) costs no time up to
 // n = 5 and 1 % of the backward at n = 6.  At n = 8 its rows take the third stage's
@@ -47,7 +48,8 @@
 // n = 5 it does not, and the exchange costs 10 %.
 //
 // Codes can only be copied by TMA where C % 16 == 0 (16-byte row strides);
-// otherwise the threads read them from global memory.
+// otherwise the threads read them from global memory (the backward at B=8192: C=4104
+// 555-565 us at n=4 and 797-800 at n=8, C=4096 222-228 and 519-524).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
