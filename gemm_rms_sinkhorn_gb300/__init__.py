@@ -87,6 +87,19 @@ _SIGS = {
     "mhc_pre_backward_workspace_bytes": ([_i64, _i32, _i64, _i32], _sz),
     "mhc_pre_backward": ([_vp, _vp, _vp, _vp, _vp, _f32, _f32, _f32, _vp, _i32] + [_vp] * 7 +
                          [_i32, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "mhc_pre_apply_rmsnorm": ([_vp, _vp, _vp, _f32, _i64, _i32, _i64, _vp, _vp, _vp, _vp], _i32),
+    "mhc_pre_apply_rmsnorm_q8": ([_vp, _vp, _vp, _f32, _i64, _i32, _i64, _vp, _vp, _vp, _vp, _vp],
+                                 _i32),
+    "mhc_add_rmsnorm": ([_vp, _vp, _vp, _f32, _i64, _i64, _vp, _vp, _vp, _vp], _i32),
+    "mhc_add_rmsnorm_q8": ([_vp, _vp, _vp, _f32, _i64, _i64, _vp, _vp, _vp, _vp, _vp], _i32),
+    "mhc_rmsnorm_backward_workspace_bytes": ([_i64, _i64], _sz),
+    "mhc_rmsnorm_backward": ([_vp] * 5 + [_i32, _i64, _i64, _vp, _vp, _vp, _sz, _vp], _i32),
+    "mhc_distill_loss": ([_vp, _i64, _vp, _vp, _vp, _f32, _i64, _i64, _i32, _vp, _vp], _i32),
+    "mhc_distill_loss_f32": ([_vp, _i64, _vp, _vp, _vp, _f32, _i64, _i64, _i32, _vp, _vp], _i32),
+    "mhc_distill_loss_backward": ([_vp, _i64, _vp, _vp, _vp, _f32, _vp, _i64, _i64, _i32, _vp, _vp,
+                                   _vp], _i32),
+    "mhc_distill_loss_backward_f32": ([_vp, _i64, _vp, _vp, _vp, _f32, _vp, _i64, _i64, _i32, _vp,
+                                       _vp, _vp], _i32),
     # test hook (include/mhc_testing.h), not part of the stable API
     "mhc_testing_gemm_rms_stalled": ([_vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp, _sz, _i64,
                                       ctypes.c_uint64, _vp], _i32),
@@ -575,6 +588,103 @@ def mhc_pre_backward(dX_next, dF_pre, Xq, Xs, phi_t, alpha_pre, alpha_post, alph
         _ptr(dH_post, f, "dH_post"), int(accumulate), B, n, C, _ptr(dX, bf, "dX"),
         _ptr(dphi_t, f, "dphi_t"), _ptr(dbias, f, "dbias"), _ptr(dalpha, f, "dalpha"), p, nb,
         _stream(stream)), "mhc_pre_backward")
+
+
+# ------------------------------------------------ the entry of F, the model's end
+
+
+def mhc_pre_apply_rmsnorm(X, H_pre, gain, eps, B, n, C, F_pre, rstd, Z, stream=None):
+    """F_pre = sum_i H_pre[i] * X[i] and its RMS norm Z (bf16); F_pre, rstd may be None."""
+    bf, f = torch.bfloat16, torch.float32
+    _check(_lib.mhc_pre_apply_rmsnorm(_ptr(X, bf, "X"), _ptr(H_pre, f, "H_pre"),
+                                      _ptr(gain, f, "gain"), eps, B, n, C, _ptr(F_pre, bf, "F_pre"),
+                                      _ptr(rstd, f, "rstd"), _ptr(Z, bf, "Z"), _stream(stream)),
+           "mhc_pre_apply_rmsnorm")
+
+
+def mhc_pre_apply_rmsnorm_q8(X, H_pre, gain, eps, B, n, C, F_pre, rstd, Zq, Zs, stream=None):
+    """The same with Z in 8 bits (``alloc_kept(B, 1, C)``)."""
+    bf, f = torch.bfloat16, torch.float32
+    _check(_lib.mhc_pre_apply_rmsnorm_q8(_ptr(X, bf, "X"), _ptr(H_pre, f, "H_pre"),
+                                         _ptr(gain, f, "gain"), eps, B, n, C,
+                                         _ptr(F_pre, bf, "F_pre"), _ptr(rstd, f, "rstd"),
+                                         _ptr8(Zq, "Zq"), _ptr(Zs, torch.uint8, "Zs"),
+                                         _stream(stream)),
+           "mhc_pre_apply_rmsnorm_q8")
+
+
+def mhc_add_rmsnorm(A, R, gain, eps, B, C, H, rstd, Z, stream=None):
+    """H = A + R (may be A or R) and its RMS norm Z; R, H, rstd may be None."""
+    bf, f = torch.bfloat16, torch.float32
+    _check(_lib.mhc_add_rmsnorm(_ptr(A, bf, "A"), _ptr(R, bf, "R"), _ptr(gain, f, "gain"), eps, B,
+                                C, _ptr(H, bf, "H"), _ptr(rstd, f, "rstd"), _ptr(Z, bf, "Z"),
+                                _stream(stream)),
+           "mhc_add_rmsnorm")
+
+
+def mhc_add_rmsnorm_q8(A, R, gain, eps, B, C, H, rstd, Zq, Zs, stream=None):
+    """The same with Z in 8 bits (``alloc_kept(B, 1, C)``)."""
+    bf, f = torch.bfloat16, torch.float32
+    _check(_lib.mhc_add_rmsnorm_q8(_ptr(A, bf, "A"), _ptr(R, bf, "R"), _ptr(gain, f, "gain"), eps,
+                                   B, C, _ptr(H, bf, "H"), _ptr(rstd, f, "rstd"), _ptr8(Zq, "Zq"),
+                                   _ptr(Zs, torch.uint8, "Zs"), _stream(stream)),
+           "mhc_add_rmsnorm_q8")
+
+
+def rmsnorm_backward_workspace(B: int, C: int, device=None) -> torch.Tensor:
+    """Workspace of ``mhc_rmsnorm_backward`` for (B, C)."""
+    nbytes = int(_lib.mhc_rmsnorm_backward_workspace_bytes(B, C))
+    return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device or "cuda")
+
+
+def mhc_rmsnorm_backward(dZ, H, gain, rstd, dH_skip, accumulate, B, C, dH, dgain, ws, stream=None):
+    """dH (may be dZ or dH_skip) and dgain of the norms; dH_skip may be None."""
+    bf, f = torch.bfloat16, torch.float32
+    p, nb = _ws(ws)
+    _check(_lib.mhc_rmsnorm_backward(_ptr(dZ, bf, "dZ"), _ptr(H, bf, "H"), _ptr(gain, f, "gain"),
+                                     _ptr(rstd, f, "rstd"), _ptr(dH_skip, bf, "dH_skip"),
+                                     int(accumulate), B, C, _ptr(dH, bf, "dH"),
+                                     _ptr(dgain, f, "dgain"), p, nb, _stream(stream)),
+           "mhc_rmsnorm_backward")
+
+
+def _distill(name, zt, z, ld, ids, t, t_lse, inv_tau, B, V, K, loss, stream):
+    f = torch.float32
+    _check(getattr(_lib, name)(_ptr(z, zt, "z"), ld, _ptr(ids, torch.int64, "ids"), _ptr(t, f, "t"),
+                               _ptr(t_lse, f, "t_lse"), inv_tau, B, V, K, _ptr(loss, f, "loss"),
+                               _stream(stream)), name)
+
+
+def mhc_distill_loss(z, ld, ids, t, t_lse, inv_tau, B, V, K, loss, stream=None):
+    """loss [B] of logits z [B, ld] (bf16) against a teacher's kept logits t [B, K] at ids [B, K];
+    t_lse may be None."""
+    _distill("mhc_distill_loss", torch.bfloat16, z, ld, ids, t, t_lse, inv_tau, B, V, K, loss, stream)
+
+
+def mhc_distill_loss_f32(z, ld, ids, t, t_lse, inv_tau, B, V, K, loss, stream=None):
+    """mhc_distill_loss of fp32 logits."""
+    _distill("mhc_distill_loss_f32", torch.float32, z, ld, ids, t, t_lse, inv_tau, B, V, K, loss,
+             stream)
+
+
+def _distill_backward(name, zt, z, ld, ids, t, t_lse, inv_tau, dloss, B, V, K, loss, dz, stream):
+    f = torch.float32
+    _check(getattr(_lib, name)(_ptr(z, zt, "z"), ld, _ptr(ids, torch.int64, "ids"), _ptr(t, f, "t"),
+                               _ptr(t_lse, f, "t_lse"), inv_tau, _ptr(dloss, f, "dloss"), B, V, K,
+                               _ptr(loss, f, "loss"), _ptr(dz, zt, "dz"), _stream(stream)), name)
+
+
+def mhc_distill_loss_backward(z, ld, ids, t, t_lse, inv_tau, dloss, B, V, K, loss, dz, stream=None):
+    """dz (may be z) for the gradient dloss [B] of each row's loss, and the loss (may be None)."""
+    _distill_backward("mhc_distill_loss_backward", torch.bfloat16, z, ld, ids, t, t_lse, inv_tau,
+                      dloss, B, V, K, loss, dz, stream)
+
+
+def mhc_distill_loss_backward_f32(z, ld, ids, t, t_lse, inv_tau, dloss, B, V, K, loss, dz,
+                                  stream=None):
+    """mhc_distill_loss_backward of fp32 logits."""
+    _distill_backward("mhc_distill_loss_backward_f32", torch.float32, z, ld, ids, t, t_lse, inv_tau,
+                      dloss, B, V, K, loss, dz, stream)
 
 
 def mhc_device_status() -> int:

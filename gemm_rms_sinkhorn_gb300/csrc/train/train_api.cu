@@ -21,55 +21,6 @@ size_t scales_bytes(int64_t B, int n, int64_t C)
     return static_cast<size_t>(B * n * kept_blocks(C));
 }
 
-// The checks that follow the shape rules, in the order of the other calls:
-// pointers, overlaps, device, memory.  `ws` (may be NULL): the workspace, which
-// needs `need(num_sms)` bytes.
-template <typename Need>
-int check_buffers(const Buf *ins, int n_in, Buf *outs, int n_out, const void *alias_out,
-                  const void *alias_in, Buf *ws, Need need, DeviceInfo *info)
-{
-    MHC_TRY(check_ptrs(ins, n_in));
-    MHC_TRY(check_ptrs(outs, n_out));
-    MHC_TRY(check_overlap(outs, n_out, ins, n_in, alias_out, alias_in));
-    MHC_TRY(check_device(info));
-    MHC_TRY(check_on_device(ins, n_in, *info));
-    MHC_TRY(check_on_device(outs, n_out, *info));
-    if (ws != nullptr) {
-        const size_t bytes = need(info->num_sms);
-        if (ws->p == nullptr || ws->bytes < bytes) return MHC_ERR_WORKSPACE;
-        const Buf w = {ws->p, bytes};
-        MHC_TRY(check_ptrs(&w, 1));
-        MHC_TRY(check_overlap(&w, 1, ins, n_in, nullptr, nullptr));
-        MHC_TRY(check_overlap(&w, 1, outs, n_out, nullptr, nullptr));
-        MHC_TRY(check_on_device(&w, 1, *info));
-    }
-    return MHC_OK;
-}
-
-int check_buffers(const Buf *ins, int n_in, Buf *outs, int n_out, const void *alias_out,
-                  const void *alias_in, DeviceInfo *info)
-{
-    return check_buffers(ins, n_in, outs, n_out, alias_out, alias_in, nullptr,
-                         [](int) { return size_t{0}; }, info);
-}
-
-cudaStream_t cu(mhc_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
-
-// Gradients of weights that no token touches: zero unless they are added to.
-int zero_grads(const Buf *outs, int count, int accumulate, mhc_stream_t stream)
-{
-    if (accumulate) return MHC_OK;
-    MHC_TRY(check_ptrs(outs, count));
-    DeviceInfo info;
-    MHC_TRY(check_device(&info));
-    MHC_TRY(check_on_device(outs, count, info));
-    for (int i = 0; i < count; ++i)
-        if (cudaMemsetAsync(const_cast<void *>(outs[i].p), 0, outs[i].bytes, cu(stream)) !=
-            cudaSuccess)
-            return MHC_ERR_CUDA;
-    return MHC_OK;
-}
-
 // Shape rules of the token table.
 int check_table(int64_t V, int64_t B, int n, int64_t C, float scale)
 {

@@ -23,6 +23,8 @@
  *   mhc_*_e4m3          the fp8 e4m3 precision variant (§4)
  *   mhc_embed*, mhc_ckpt_*, mhc_post_res_apply_ckpt*, mhc_*_backward*
  *                       training: token ids to streams, X kept in 8 bits, gradients
+ *   mhc_*_rmsnorm*      F's input normed as it is formed, in bf16 or 8 bits; the backward
+ *   mhc_distill_*       distillation from a teacher's kept logits, with the gradient
  *
  * Shapes: B tokens (batch × sequence), expansion n, hidden size C,
  * K = n·C, N = n² + 2n.
@@ -459,6 +461,98 @@ int mhc_pre_backward(const mhc_bf16 *dX_next, const mhc_bf16 *dF_pre, const uint
                      const float *dH_res, const float *dH_post, int accumulate, int64_t B, int n,
                      int64_t C, mhc_bf16 *dX, float *dphi_t, float *dbias, float *dalpha,
                      void *workspace, size_t workspace_bytes, mhc_stream_t stream);
+
+/*
+ * The entry of the layer function F: root-mean-square norms.
+ *
+ *   mhc_pre_apply_rmsnorm   H = Σ_i H_pre[b][i]·X[b][i]     (step 4a: H is F_pre)
+ *   mhc_add_rmsnorm         H = A + R                       (a residual inside F)
+ *   both                    rstd[b] = 1/sqrt(Σ_c H[b][c]²/C + eps)
+ *                           Z[b][c] = H[b][c]·rstd[b]·gain[c]
+ *
+ *   A, R, H, F_pre, Z [B][C] bf16, gain [C] fp32, rstd [B] fp32
+ * Everything is formed from the fp32 H; F_pre has the bits of mhc_pre_apply's.  With H_pre
+ * all 1/n the first is the norm of the streams' mean, at the model's end.  _q8: Z in the
+ * 8-bit form that X is kept in, Zq [B][C] and Zs [B][ceil(C/32)] (mhc_ckpt_unpack with
+ * n = 1 reads it): e4m3 codes, a power-of-two scale for each 32 channels.
+ *
+ * H and rstd may each be NULL where they are not wanted (the backward needs both).  R may
+ * be NULL: the norm of A alone; H then has to be NULL.  H may be exactly A or exactly R.
+ * Rules, layouts and status codes otherwise as the calls above, and C <= 16384
+ * (MHC_ERR_UNSUPPORTED); eps finite and >= 0 (MHC_ERR_INVALID).  Squares are summed in
+ * fp32.  A row of zeros with eps = 0 has rstd = 0 and Z = 0.
+ */
+int mhc_pre_apply_rmsnorm(const mhc_bf16 *X, const float *H_pre, const float *gain, float eps,
+                          int64_t B, int n, int64_t C, mhc_bf16 *F_pre, float *rstd, mhc_bf16 *Z,
+                          mhc_stream_t stream);
+int mhc_pre_apply_rmsnorm_q8(const mhc_bf16 *X, const float *H_pre, const float *gain, float eps,
+                             int64_t B, int n, int64_t C, mhc_bf16 *F_pre, float *rstd, uint8_t *Zq,
+                             uint8_t *Zs, mhc_stream_t stream);
+int mhc_add_rmsnorm(const mhc_bf16 *A, const mhc_bf16 *R, const float *gain, float eps, int64_t B,
+                    int64_t C, mhc_bf16 *H, float *rstd, mhc_bf16 *Z, mhc_stream_t stream);
+int mhc_add_rmsnorm_q8(const mhc_bf16 *A, const mhc_bf16 *R, const float *gain, float eps, int64_t B,
+                       int64_t C, mhc_bf16 *H, float *rstd, uint8_t *Zq, uint8_t *Zs,
+                       mhc_stream_t stream);
+
+/*
+ * Their backward, from H and rstd as the forward wrote them:
+ *   t        = gain·dZ
+ *   dH       = rstd·(t - H·rstd²·Σ_c t·H/C) + dH_skip
+ *   dgain[c] (+)= Σ_b dZ[b][c]·H[b][c]·rstd[b]           fp32 [C]
+ * dH_skip (bf16, may be NULL) is the gradient that reaches H past the norm.  dH may be
+ * exactly dZ or exactly dH_skip.  dH is the gradient of F_pre, for mhc_pre_backward, or of
+ * both A and R.  8 bits: the rounding counts as the identity.  accumulate, B == 0, the
+ * fixed order of sums and NaN as for the training calls; workspace:
+ * mhc_rmsnorm_backward_workspace_bytes on the current device.
+ */
+size_t mhc_rmsnorm_backward_workspace_bytes(int64_t B, int64_t C);
+int mhc_rmsnorm_backward(const mhc_bf16 *dZ, const mhc_bf16 *H, const float *gain, const float *rstd,
+                         const mhc_bf16 *dH_skip, int accumulate, int64_t B, int64_t C, mhc_bf16 *dH,
+                         float *dgain, void *workspace, size_t workspace_bytes, mhc_stream_t stream);
+
+/*
+ * The model's end: distillation from a teacher of which K logits a row are kept.
+ *
+ *   z [B][ld] bf16 (_f32: fp32)    the student's logits, V of each ld
+ *   ids [B][K] int64, t [B][K] fp32   the teacher's kept logits and where they belong
+ *   t_lse [B] fp32, or NULL
+ * An entry whose id lies outside [0, V) or whose t is -inf is absent.  With
+ * q = softmax(z·inv_tau) over the row, x_k = t_k·inv_tau and sums over the entries present:
+ *   t_lse NULL   p_k = exp(x_k)/Σ exp(x);  p_rest = 0
+ *   t_lse given  p_k = exp(x_k - t_lse), t_lse being the logarithm of the teacher's sum over
+ *                its whole vocabulary at that temperature;  p_rest = max(0, 1 - Σ p_k),
+ *                held against q_rest, the sum of q over all that is not kept; p_rest = 0
+ *                where nothing (or only z = -inf) is left over
+ *   loss = Σ_k p_k·(log p_k - log q_k) + p_rest·(log p_rest - log q_rest)
+ *   dz_j = dloss·inv_tau·(M·q_j - p_j)               for kept j, M = Σ p_k + p_rest
+ *   dz_j = dloss·inv_tau·q_j·(M - p_rest/q_rest)     for the others
+ * An id that comes more than once has its p added up.  K = 1 without t_lse is cross
+ * entropy.  A row without entries has loss 0 and dz 0, whatever its z (padding).  z may hold
+ * -inf (a masked vocabulary); where a kept id with p > 0 has it, the loss is +inf.  Any
+ * other row with a NaN or +inf in z, or with z = -inf throughout, has loss and dz NaN; one
+ * with a NaN or +inf in t or t_lse has loss NaN.
+ *
+ * The backward works from z alone, in one pass: a training step that knows dloss [B] fp32
+ * (1/rows, times tau² where that is wanted) needs no forward call.  Its loss may be NULL.
+ * dz [B][ld] has z's type and may be exactly z; columns from V on are neither read for
+ * their value nor written.  Results are bitwise reproducible.
+ *
+ * Rules as for the calls above, and: V >= 1, K >= 1, ld >= V, inv_tau finite and > 0
+ * (MHC_ERR_INVALID); B < 2^31, V <= 2^18, K <= 1024, ld % 8 == 0 and ld <= 2^24
+ * (MHC_ERR_UNSUPPORTED).
+ */
+int mhc_distill_loss(const mhc_bf16 *z, int64_t ld, const int64_t *ids, const float *t,
+                     const float *t_lse, float inv_tau, int64_t B, int64_t V, int K, float *loss,
+                     mhc_stream_t stream);
+int mhc_distill_loss_f32(const float *z, int64_t ld, const int64_t *ids, const float *t,
+                         const float *t_lse, float inv_tau, int64_t B, int64_t V, int K, float *loss,
+                         mhc_stream_t stream);
+int mhc_distill_loss_backward(const mhc_bf16 *z, int64_t ld, const int64_t *ids, const float *t,
+                              const float *t_lse, float inv_tau, const float *dloss, int64_t B,
+                              int64_t V, int K, float *loss, mhc_bf16 *dz, mhc_stream_t stream);
+int mhc_distill_loss_backward_f32(const float *z, int64_t ld, const int64_t *ids, const float *t,
+                                  const float *t_lse, float inv_tau, const float *dloss, int64_t B,
+                                  int64_t V, int K, float *loss, float *dz, mhc_stream_t stream);
 
 /*
  * Reads and clears the device status word of the current device: MHC_OK, or
