@@ -11,12 +11,22 @@
 // cancel), and relative to its own largest value, so it does not underflow where the kept
 // logits are far above the rest.
 //
-// A row is read once: a cluster of up to 8 blocks holds it in shared memory, each a
-// segment.  A block copies its segment in, takes out the kept entries (they are summed
-// apart and leave -inf behind), forms the largest value and the sum of the rest, and the
-// blocks exchange those through distributed shared memory.  The gradient is then formed
-// from the segment and written once; dz may be z.  Every block works out the K entries
-// for itself.
+// A row is read once and its gradient written once: the blocks of a cluster of up to 8 hold
+// a segment each, a thread up to 64 values in registers, and walk the rows.  A thread's
+// pieces of the next row are copied into shared memory meanwhile; only it reads them, so
+// nothing else has to wait for them.
+//
+// Two more warps keep all else away from those.  One takes the K entries, a row ahead: it
+// works out the teacher's sums, fetches the student's logits there and marks the kept ids in
+// a bit map, a word a thread; the thread overwrites its marked values with -inf before it
+// reads them.  The other joins a row's sums, over warps and then over the cluster through
+// distributed shared memory, and answers with the factor of the gradient.  What is due at
+// the kept ids is written a row later, behind what the row's threads wrote there.  dz may be
+// z: a row is written after all of the cluster has summed it up.
+//
+// Exponentials are exp2((z - m)·c), c = inv_tau·log2 e, m the largest z seen, two values at
+// a time.  As one fused multiply-add z·c - m·c they would be off by what m·c rounds away:
+// with a vocabulary masked by the type's lowest value m may be that.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -31,9 +41,11 @@
 namespace mhc {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 16;  // that hold a row; two more for the entries and for joining
+constexpr int kMaxThreads = kMaxWarps * 32;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxBits = 64;  // values a thread
+constexpr int kMaxItems = 8;  // pieces a thread, but where 8 blocks do not reach
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float v)
@@ -43,362 +55,609 @@ __device__ __forceinline__ float exp2_fast(float v)
     return r;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive()
+__device__ __forceinline__ void cluster_arrive_release() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Barriers of the block by number, of `count` threads: one that waits, one that does not.
+__device__ __forceinline__ void block_sync(int id, int count)
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
-__device__ __forceinline__ void cluster_wait()
+__device__ __forceinline__ void block_arrive(int id, int count)
 {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
-// 16 bytes at `p`'s place in the shared memory of block `rank` of the cluster.
-__device__ __forceinline__ float4 ld_cluster(const float4 *p, uint32_t rank)
+// 16 bytes to `p`'s place in the shared memory of block `rank` of the cluster.
+__device__ __forceinline__ void st_cluster(float4 *p, uint32_t rank, float4 v)
 {
     uint32_t at;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(at)
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w)
                  : "memory");
-    return v;
+}
+__device__ __forceinline__ void cp_async16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
 }
 
-// ---- the logits' types: 16 bytes as fp32, and back
+// ---- the logits' types, by pieces of 16 bytes
 template <typename T>
 struct Logit;
 template <>
 struct Logit<uint16_t> {
     static constexpr int kVec = 8;
-    __device__ static float value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+    static constexpr uint32_t kLowest = 0xFF80FF80u;
     __device__ static uint16_t from(float f) { return static_cast<uint16_t>(pack_bf16_rn(f, 0.f)); }
-    __device__ static uint16_t tag(int k) { return static_cast<uint16_t>(k); }
-    __device__ static int tag_of(uint16_t v) { return v; }
-    __device__ static uint16_t lowest() { return 0xFF80u; }
-    __device__ static void unpack(const uint4 &v, float (&f)[8]) { unpack8(v, f); }
+    __device__ static void pairs(const uint4 &v, uint64_t (&f)[4]) { unpack8_pairs(v, f); }
     __device__ static uint4 pack(const float (&f)[8]) { return pack8(f); }
-    __device__ static uint16_t load(const uint16_t *p) { return static_cast<uint16_t>(ptx::ld_dep(p)); }
+    // what cp_async4 brought of the 4 bytes that value i of a row lies in
+    __device__ static float word(uint32_t w, int i) { return i & 1 ? bf16_hi(w) : bf16_lo(w); }
+    static constexpr int kWord = 2;  // values
+    __device__ static uint16_t lowest() { return 0xFF80u; }
+    // the largest value of `items` pieces; a NaN is passed over (the sum meets it)
+    template <int ITEMS>
+    __device__ static float largest(const uint4 (&v)[ITEMS])
+    {
+        uint32_t m = kLowest;
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int p = 0; p < 4; ++p) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[p]));
+        }
+        return fmaxf(bf16_lo(m), bf16_hi(m));
+    }
 };
 template <>
 struct Logit<float> {
     static constexpr int kVec = 4;
-    __device__ static float value(float v) { return v; }
+    static constexpr uint32_t kLowest = 0xFF800000u;
     __device__ static float from(float f) { return f; }
-    __device__ static float tag(int k) { return __int_as_float(k); }
-    __device__ static int tag_of(float v) { return __float_as_int(v); }
-    __device__ static float lowest() { return -INFINITY; }
-    __device__ static void unpack(const uint4 &v, float (&f)[4])
+    __device__ static void pairs(const uint4 &v, uint64_t (&f)[2])
     {
-        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
-        f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+        f[0] = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
+        f[1] = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
     }
     __device__ static uint4 pack(const float (&f)[4])
     {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                           __float_as_uint(f[3]));
     }
-    __device__ static float load(const float *p) { return ptx::ld_dep(p); }
+    __device__ static float word(uint32_t w, int) { return __uint_as_float(w); }
+    static constexpr int kWord = 1;
+    __device__ static float lowest() { return -INFINITY; }
+    template <int ITEMS>
+    __device__ static float largest(const uint4 (&v)[ITEMS])
+    {
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(v[j].x), __uint_as_float(v[j].y)),
+                               fmaxf(__uint_as_float(v[j].z), __uint_as_float(v[j].w))));
+        }
+        return m;
+    }
 };
 
-// A sum of exp((v - m)·c), c > 0, kept with its largest v.  Nothing yet: (-inf, 0).
+// A sum of exp2((z - m)·c) with its largest z.  Nothing yet: (-inf, 0).
 struct Peak {
     float m, s;
 };
-__device__ __forceinline__ Peak merge(Peak a, Peak b, float c2)
-{
-    const float m = fmaxf(a.m, b.m);
-    if (m == -INFINITY) return {m, a.s + b.s};
-    return {m, a.s * exp2_fast((a.m - m) * c2) + b.s * exp2_fast((b.m - m) * c2)};
-}
-
-struct Shared {
-    float4 mine;               // (rest.m, rest.s, top.m, top.s) of this block, read by the cluster
-    float4 all[kMaxCluster];
-    float a[kWarps], b[kWarps], c[kWarps];
-};
-
-// Reductions over the block; every thread gets the result.  Between two that use the
-// same array there has to be a barrier after the first one's last read: callers alternate.
-__device__ __forceinline__ float block_sum(float v, float *red)
-{
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = (threadIdx.x & 31) < kWarps ? red[threadIdx.x & 31] : 0.f;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
-}
-__device__ __forceinline__ float block_max(float v, float *red)
-{
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = (threadIdx.x & 31) < kWarps ? red[threadIdx.x & 31] : -INFINITY;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
-}
-
 // -inf, where nothing or only -inf was seen, as a reference that -inf may be taken from.
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
 
-template <typename T, bool GRAD>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs<T> a, int seg, int S)
+__device__ __forceinline__ Peak merge(Peak a, Peak b, float c)
+{
+    const float m = fmaxf(a.m, b.m), r = reference(m);
+    return {m, a.s * exp2_fast((a.m - r) * c) + b.s * exp2_fast((b.m - r) * c)};
+}
+// Over the lanes of a warp, the same in each of them.
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+__device__ __forceinline__ Peak warp_merge(Peak a, float c)
+{
+    const float m = warp_max(a.m);
+    return {m, warp_sum(a.s * exp2_fast((a.m - reference(m)) * c))};
+}
+// exp2((z - r)·c) of a pair of values.
+__device__ __forceinline__ void exp2_pair(uint64_t z, uint64_t minus_r, uint64_t c, float &lo, float &hi)
+{
+    f2_unpack(f2_mul(f2_add(z, minus_r), c), lo, hi);
+    lo = exp2_fast(lo);
+    hi = exp2_fast(hi);
+}
+
+// The first n values of a piece: a row's last one, which a vector would overrun.
+template <typename T>
+__device__ __noinline__ void store_some(T *p, uint4 v, int n)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    constexpr int per = 4 / sizeof(T);
+#pragma unroll
+    for (int e = 0; e < 4 * per; ++e)
+        if (e < n) {
+            if constexpr (per == 2)
+                p[e] = static_cast<uint16_t>(w[e / 2] >> (e % 2 * 16));
+            else
+                p[e] = __uint_as_float(w[e]);
+        }
+}
+
+struct Shared {
+    float4 row[2][kMaxCluster];   // (rest.m, rest.s, kept.m, kept.s) by block
+    float4 entry;                 // of the row's entries: kept.m, kept.s, Σ p, dloss·inv_tau
+    float4 whole;                 // the row's: rest.m, rest.s, and of both together
+    float4 out;                   // the gradient: what to multiply by, the reference, whether there is one
+    float2 rest[2][kMaxWarps];    // peaks by warp
+    uint2 marks[2][kMaxThreads];  // bit j·VEC + e: value e of the thread's piece j is kept
+    int flags;
+};
+constexpr int kSome = 1, kTwice = 2;  // entries are present; an id comes more than once here
+// The block's barriers.  A row's sums, entries and the next row's marks are there: the
+// joining warp waits for it, without a gradient the others, too.  The row is joined: those
+// that have to do with the answer wait.  The last row is written: the entries' warp waits.
+constexpr int kSummed = 1, kAnswered = 2, kWritten = 3;
+
+template <typename T, bool GRAD, int ITEMS>
+__global__ void __launch_bounds__(kMaxThreads + 64, ITEMS > 8 ? 1 : 2)
+distill_kernel(const DistillArgs<T> a, int seg, int S)
 {
     using L = Logit<T>;
     constexpr int VEC = L::kVec;
+    static_assert(ITEMS * VEC <= kMaxBits, "a thread's values have a bit each");
     __shared__ Shared sh;
-    extern __shared__ __align__(16) uint8_t dyn[];
-    T *buf = reinterpret_cast<T *>(dyn);                                // [seg]
-    float *lp = reinterpret_cast<float *>(dyn + static_cast<size_t>(seg) * sizeof(T));  // log p [K]
-    float *zk = lp + a.K;                                               // the student's logit there
-    int *idk = reinterpret_cast<int *>(zk + a.K);                       // -1: absent
+    // pieces [warps][ITEMS][32], a warp's one after another; then the entries
+    extern __shared__ __align__(16) uint4 dyn[];
+    constexpr int kWarpPieces = ITEMS * 32;
 
-    const int tid = threadIdx.x;
+    const int threads = blockDim.x - 64, warps = threads >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int answered = GRAD ? threads + 64 : 64;  // threads at that barrier
     const uint32_t rank = S > 1 ? cluster_rank() : 0;
     const int lo = static_cast<int>(rank) * seg;
-    const int count = min(a.V - lo, seg) > 0 ? min(a.V - lo, seg) : 0;
-    const int chunks = (count + VEC - 1) / VEC;
-    const float c2 = a.inv_tau * kLog2e;
-    const uint32_t buf_at = ptx::smem_u32(buf);
-    bool waiting = false;  // for the cluster to have read `mine`
-
-    ptx::pdl_wait();
-    ptx::pdl_trigger();
-    for (int64_t b = blockIdx.x / S; b < a.B; b += gridDim.x / S) {
-        if (!in_range(1601, b, 1, a.B)) break;
-        const T *row = a.z + b * a.ld + lo;
-        for (int i = tid; i < chunks; i += kThreads)
-            if (in_range(1602, lo + i * VEC, VEC, a.ld)) cp_async16(buf_at + i * 16, row + i * VEC);
-        ptx::cp_async_commit();
-
-        // the teacher's entries
-        int some = 0;
-        float tm = -INFINITY;
-        for (int k = tid; k < a.K; k += kThreads) {
-            const int64_t id = ptx::ld_dep(a.ids + b * a.K + k);
-            const float t = ptx::ld_dep(a.t + b * a.K + k);
-            const bool here = id >= 0 && id < a.V && t != -INFINITY;
-            idk[k] = here ? static_cast<int>(id) : -1;
-            lp[k] = t * a.inv_tau;
-            if (!here) continue;
-            some = 1;
-            tm = fmaxf(tm, t * a.inv_tau);
-            if (rank == 0) zk[k] = L::value(L::load(a.z + b * a.ld + id));
-        }
-        if (!__syncthreads_or(some)) {
-            if (rank == 0 && tid == 0 && a.loss != nullptr) a.loss[b] = 0.f;
-            if constexpr (GRAD) {
-                T *out = a.dz + b * a.ld + lo;
-                for (int i = tid; i < count; i += kThreads) out[i] = L::from(0.f);
-            }
-            ptx::cp_async_wait_all();
-            __syncthreads();
-            continue;
-        }
-        float base = 0.f, mass = 0.f;
-        if (a.t_lse != nullptr) {
-            base = ptx::ld_dep(a.t_lse + b);
-            for (int k = tid; k < a.K; k += kThreads) {
-                lp[k] -= base;
-                if (idk[k] >= 0) mass += expf(lp[k]);
-            }
-            mass = block_sum(mass, sh.b);
-        } else {
-            tm = block_max(tm, sh.a);
-            float s = 0.f;
-            for (int k = tid; k < a.K; k += kThreads) {
-                lp[k] -= tm;
-                if (idk[k] >= 0) s += expf(lp[k]);
-            }
-            base = logf(block_sum(s, sh.b));
-            for (int k = tid; k < a.K; k += kThreads) lp[k] -= base;
-            mass = 1.f;
-        }
-
-        // the segment: what is past its end, and the kept entries, become -inf
-        ptx::cp_async_wait_all();
-        __syncthreads();
-        if (tid < chunks * VEC - count) buf[count + tid] = L::lowest();
-        for (int k = tid; k < a.K; k += kThreads) {
-            const int j = idk[k] - lo;
-            if (idk[k] >= 0 && j >= 0 && j < count) zk[k] = L::value(buf[j]);
-        }
-        __syncthreads();
-        for (int k = tid; k < a.K; k += kThreads) {
-            const int j = idk[k] - lo;
-            if (idk[k] >= 0 && j >= 0 && j < count) buf[j] = L::tag(k);
-        }
-        __syncthreads();
-        int twice = 0;  // whether an id comes more than once
-        for (int k = tid; k < a.K; k += kThreads) {
-            const int j = idk[k] - lo;
-            if (idk[k] >= 0 && j >= 0 && j < count) twice |= L::tag_of(buf[j]) != k;
-        }
-        twice = __syncthreads_or(twice);
-        Peak top = {-INFINITY, 0.f};
-        for (int k = tid; k < a.K; k += kThreads) {
-            const int j = idk[k] - lo;
-            if (idk[k] < 0 || j < 0 || j >= count) continue;
-            buf[j] = L::lowest();
-            bool first = true;
-            if (twice)
-                for (int i = 0; i < k; ++i) first = first && idk[i] != idk[k];
-            const float one = zk[k] == -INFINITY ? 0.f : zk[k] != zk[k] ? zk[k] : 1.f;
-            if (first) top = merge(top, {zk[k], one}, c2);
-        }
-        __syncthreads();
-
-        // the rest's largest value and sum
-        float m = -INFINITY;
-        const uint4 *chunk = reinterpret_cast<const uint4 *>(buf);
-        for (int i = tid; i < chunks; i += kThreads) {
-            float f[VEC];
-            L::unpack(chunk[i], f);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) m = fmaxf(m, f[e]);
-        }
-        m = block_max(m, sh.c);
-        const float ref = reference(m);
-        float s = 0.f;
-        for (int i = tid; i < chunks; i += kThreads) {
-            float f[VEC];
-            L::unpack(chunk[i], f);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s += exp2_fast((f[e] - ref) * c2);
-        }
-        Peak rest = {m, block_sum(s, sh.a)};
-        const float topm = block_max(top.m, sh.b);
-        // sum of the kept entries, relative to their largest
-        top.s = block_sum(topm == -INFINITY ? top.s : top.s * exp2_fast((top.m - topm) * c2), sh.c);
-        top.m = topm;
-
+    const int count = max(min(a.V - lo, seg), 0);
+    const int pieces = (count + VEC - 1) / VEC;
+    const float c = a.inv_tau * kLog2e;
+    const int64_t step = gridDim.x / S, first = blockIdx.x / S;
+    // A row's barrier of the cluster, for the warps that do not wait for the others' sums:
+    // they take part a row behind.
+    const auto pass = [&](int64_t b) {
         if (S > 1) {
-            if (waiting) cluster_wait();
-            if (tid == 0) sh.mine = make_float4(rest.m, rest.s, top.m, top.s);
-            cluster_arrive();
-            cluster_wait();
-            if (tid < S) sh.all[tid] = ld_cluster(&sh.mine, tid);
-            cluster_arrive();
-            waiting = true;
-            __syncthreads();
-            rest = {-INFINITY, 0.f};
-            top = {-INFINITY, 0.f};
-            for (int r = 0; r < S; ++r) {
-                const float4 v = sh.all[r];
-                rest = merge(rest, {v.x, v.y}, c2);
-                top = merge(top, {v.z, v.w}, c2);
-            }
+            if (b != first) cluster_wait();
+            cluster_arrive_relaxed();
         }
-        const Peak whole = merge(rest, top, c2);
-        const float ln_s = logf(whole.s);
-        const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - mass, 0.f) : 0.f;
+    };
 
-        if (rank == 0 && a.loss != nullptr) {
-            float part = 0.f;
-            for (int k = tid; k < a.K; k += kThreads) {
-                if (idk[k] < 0) continue;
-                const float p = expf(lp[k]);
-                if (p != 0.f) part += p * (lp[k] - ((zk[k] - whole.m) * a.inv_tau - ln_s));
-            }
-            part = block_sum(part, sh.a);
-            if (tid == 0) {
-                if (p_rest > 0.f)
-                    part += p_rest * (logf(p_rest) - ((rest.m - whole.m) * a.inv_tau + logf(rest.s) - ln_s));
-                a.loss[b] = part;
-            }
-        }
-        if constexpr (GRAD) {
-            const float w = ptx::ld_dep(a.dloss + b) * a.inv_tau, all = mass + p_rest;
-            // q_rest·(M - p_rest/q_rest) = M·q_rest - p_rest, shared out by exp over the rest's sum
-            const float q_rest = rest.s == 0.f ? 0.f : rest.s * exp2_fast((rest.m - whole.m) * c2) / whole.s;
-            const float scale = rest.s != 0.f ? w * (all * q_rest - p_rest) / rest.s
-                                              : whole.s != 0.f ? 0.f : NAN;
-            const float at = reference(rest.m);
-            T *out = a.dz + b * a.ld + lo;
-            for (int i = tid; i < chunks; i += kThreads) {
-                float f[VEC];
-                L::unpack(chunk[i], f);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) f[e] = exp2_fast((f[e] - at) * c2) * scale;
-                if ((i + 1) * VEC <= count) {
-                    if (in_range(1603, lo + i * VEC, VEC, a.ld)) ptx::st_stream_v4(out + i * VEC, L::pack(f));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (i * VEC + e < count) out[i * VEC + e] = L::from(f[e]);
-                }
-            }
-            __syncthreads();  // the kept entries' places hold 0 until here
-            for (int k = tid; k < a.K; k += kThreads) {
-                const int j = idk[k] - lo;
-                if (idk[k] < 0 || j < 0 || j >= count) continue;
-                float p = expf(lp[k]);
-                if (twice) {
-                    p = 0.f;
-                    for (int i = 0; i < a.K; ++i)
-                        if (idk[i] == idk[k]) p += expf(lp[i]);
-                }
-                const float q = exp2_fast((zk[k] - whole.m) * c2) / whole.s;
-                out[j] = L::from(w * (all * q - p));
-            }
-        }
-        __syncthreads();  // the entries and the segment are no longer read
+    for (int i = tid; i < 2 * kMaxThreads; i += blockDim.x) (&sh.marks[0][0])[i] = make_uint2(0, 0);
+    // No early trigger: blocks of the next kernel that wait in the places of these cost more
+    // (4096 rows of 131072, back to back: 592 us, 473 without) than their start would save.
+    ptx::pdl_wait();
+    if (S > 1) {  // every block has started before another writes into it
+        cluster_arrive_relaxed();
+        cluster_wait();
     }
-    if (waiting) cluster_wait();
+    __syncthreads();
+
+    if (warp == warps) {  // ---- the entries
+        // [2][K] x = t·inv_tau, the word that z lies in, id; [K] what follows a row later
+        float *const x2 = reinterpret_cast<float *>(dyn + warps * kWarpPieces);
+        uint32_t *const word2 = reinterpret_cast<uint32_t *>(x2 + 2 * a.K);
+        int *const id2 = reinterpret_cast<int *>(word2 + 2 * a.K);
+        float *const later = reinterpret_cast<float *>(id2 + 2 * a.K);
+        int *const later_at = reinterpret_cast<int *>(later + a.K);  // -1: none
+
+        constexpr int kAhead = 4;  // entries a lane that are read another row ahead
+        int64_t id[kAhead];
+        float t[kAhead], lse = 0.f, dloss = 0.f;
+        const auto read = [&](int64_t b, int k0) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int k = k0 + 32 * u;
+                id[u] = k < a.K ? ptx::ld_dep(a.ids + b * a.K + k) : -1;
+                t[u] = k < a.K ? ptx::ld_dep(a.t + b * a.K + k) : 0.f;
+            }
+        };
+        const auto read_ahead = [&](int64_t b) {
+            read(b, lane);
+            if (a.t_lse != nullptr) lse = ptx::ld_dep(a.t_lse + b);
+            if constexpr (GRAD) dloss = ptx::ld_dep(a.dloss + b);
+        };
+        int flags = 0;
+        float base = 0.f, mass = 0.f, w = 0.f;
+        const auto prepare = [&](int64_t b, int turn) {  // after read_ahead(b)
+            float *x = x2 + turn * a.K;
+            uint32_t *word = word2 + turn * a.K;
+            int *idk = id2 + turn * a.K;
+            const T *row = a.z + b * a.ld;
+            float m = -INFINITY;
+            flags = 0;
+#pragma unroll 1
+            for (int k0 = lane; k0 < a.K; k0 += 32 * kAhead) {
+                if (k0 != lane) read(b, k0);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int k = k0 + 32 * u;
+                    if (k >= a.K) continue;
+                    const bool here = id[u] >= 0 && id[u] < a.V && t[u] != -INFINITY;
+                    const int i = here ? static_cast<int>(id[u]) : -1;
+                    idk[k] = i;
+                    x[k] = t[u] * a.inv_tau;
+                    if (!here) continue;
+                    flags |= kSome;
+                    m = fmaxf(m, x[k]);
+                    const int at = i - lo;
+                    const bool mine = at >= 0 && at < count;
+                    if (mine) {
+                        const int p = at / VEC, bit = p / 32 % ITEMS * VEC + at % VEC;
+                        uint32_t *mark = &sh.marks[turn][p / kWarpPieces * 32 + p % 32].x + (bit >> 5);
+                        if (atomicOr(mark, 1u << (bit & 31)) >> (bit & 31) & 1u) flags |= kTwice;
+                    }
+                    if ((rank == 0 || mine) && in_range(1605, i, 1, a.V))
+                        ptx::cp_async4(word + k, row + (i & -L::kWord));
+                }
+            }
+            ptx::cp_async_commit();
+            flags = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(flags)));
+            __syncwarp();
+            m = a.t_lse != nullptr ? lse : warp_max(m);
+            float s = 0.f;
+#pragma unroll 1
+            for (int k = lane; k < a.K; k += 32)
+                if (idk[k] >= 0) s += expf(x[k] - m);
+            s = warp_sum(s);
+            base = a.t_lse != nullptr ? m : m + logf(s);
+            mass = a.t_lse != nullptr ? s : 1.f;
+            w = dloss * a.inv_tau;
+        };
+        const auto write_later = [&](int64_t b) {
+            T *out = a.dz + b * a.ld + lo;
+#pragma unroll 1
+            for (int k = lane; k < a.K; k += 32)
+                if (later_at[k] >= 0 && in_range(1604, lo + later_at[k], 1, a.V)) out[later_at[k]] = L::from(later[k]);
+        };
+        if constexpr (GRAD)
+            for (int k = lane; k < a.K; k += 32) later_at[k] = -1;
+        read_ahead(first);
+        prepare(first, 0);
+        if (first + step < a.B) read_ahead(first + step);
+        __syncthreads();  // the first row's marks are there
+        int turn = 0;
+        for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
+            const float *x = x2 + turn * a.K;
+            const uint32_t *word = word2 + turn * a.K;
+            const int *idk = id2 + turn * a.K;
+            const int row_flags = flags;
+            const float row_base = base, row_mass = mass, row_w = w;
+            ptx::cp_async_wait_all();
+            __syncwarp();
+            Peak kept = {-INFINITY, 0.f};
+#pragma unroll 1
+            for (int k = lane; k < a.K; k += 32) {
+                const int at = idk[k] - lo;
+                if (idk[k] < 0 || at < 0 || at >= count) continue;
+                bool once = true;
+                if (row_flags & kTwice)
+#pragma unroll 1
+                    for (int i = 0; i < k; ++i) once = once && idk[i] != idk[k];
+                const float z = L::word(word[k], idk[k]), one = z == -INFINITY ? 0.f : z != z ? z : 1.f;
+                if (once) kept = merge(kept, {z, one}, c);
+            }
+            kept = warp_merge(kept, c);
+            if (b + step < a.B) prepare(b + step, turn ^ 1);
+            if (lane == 0) {
+                sh.entry = make_float4(kept.m, kept.s, row_mass, row_w);
+                sh.flags = row_flags;
+            }
+            __syncwarp();
+            block_arrive(kSummed, threads + 64);
+            pass(b);
+            if (b + 2 * step < a.B) read_ahead(b + 2 * step);
+            block_sync(kAnswered, answered);
+
+            const Peak rest = {sh.whole.x, sh.whole.y}, whole = {sh.whole.z, sh.whole.w};
+            const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - row_mass, 0.f) : 0.f;
+            if constexpr (GRAD) {
+                // everyone's stores of the row before precede this row's sums
+                if (b != first) write_later(b - step);
+#pragma unroll 1
+                for (int k = lane; k < a.K; k += 32) {
+                    const int at = idk[k] - lo;
+                    const bool mine = idk[k] >= 0 && at >= 0 && at < count;
+                    later_at[k] = mine ? at : -1;
+                    if (!mine) continue;
+                    float p = expf(x[k] - row_base);
+                    if (row_flags & kTwice) {
+                        p = 0.f;
+#pragma unroll 1
+                        for (int i = 0; i < a.K; ++i)
+                            if (idk[i] == idk[k]) p += expf(x[i] - row_base);
+                    }
+                    const float z = L::word(word[k], idk[k]);
+                    const float q = exp2_fast((z - reference(whole.m)) * c) / whole.s;
+                    later[k] = row_w * ((row_mass + p_rest) * q - p);
+                }
+            }
+            if (rank == 0 && a.loss != nullptr) {
+                const float ln_s = logf(whole.s);
+                float part = 0.f;
+#pragma unroll 1
+                for (int k = lane; k < a.K; k += 32) {
+                    if (idk[k] < 0) continue;
+                    const float lp = x[k] - row_base, p = expf(lp);
+                    const float z = L::word(word[k], idk[k]);
+                    if (p != 0.f) part += p * (lp - ((z - whole.m) * a.inv_tau - ln_s));
+                }
+                part = warp_sum(part);
+                if (lane == 0) {
+                    if (p_rest > 0.f)
+                        part += p_rest * (logf(p_rest) - ((rest.m - whole.m) * a.inv_tau + logf(rest.s) - ln_s));
+                    a.loss[b] = row_flags & kSome ? part : 0.f;
+                }
+            }
+            __syncwarp();
+        }
+        if (S > 1) cluster_wait();
+        if constexpr (GRAD) {
+            block_sync(kWritten, threads + 32);
+            write_later(first + (a.B - 1 - first) / step * step);
+        }
+        return;
+    }
+
+    if (warp > warps) {  // ---- joining
+        __syncthreads();
+        int turn = 0;
+        for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
+            block_sync(kSummed, threads + 64);
+            Peak rest = {-INFINITY, 0.f};
+            if (lane < warps) rest = {sh.rest[turn][lane].x, sh.rest[turn][lane].y};
+            const float4 entry = sh.entry;
+            const int flags = sh.flags;
+            rest = warp_merge(rest, c);
+            Peak kept = {entry.x, entry.y};
+            if (S > 1) {
+                if (lane < S) st_cluster(&sh.row[turn][rank], lane, make_float4(rest.m, rest.s, kept.m, kept.s));
+                cluster_arrive_release();
+                cluster_wait();
+                const float4 v = sh.row[turn][lane & (S - 1)];
+                rest = {v.x, lane < S ? v.y : 0.f};
+                kept = {v.z, lane < S ? v.w : 0.f};
+                rest = warp_merge(rest, c);
+                kept = warp_merge(kept, c);
+            }
+            const Peak whole = merge(rest, kept, c);
+            if (lane == 0) {
+                sh.whole = make_float4(rest.m, rest.s, whole.m, whole.s);
+                if constexpr (GRAD) {
+                    const float mass = entry.z, w = entry.w;
+                    const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - mass, 0.f) : 0.f;
+                    // q_rest·(M - p_rest/q_rest) = M·q_rest - p_rest, shared out by exp2 over the rest's sum
+                    const float q_rest = rest.s == 0.f ? 0.f : rest.s * exp2_fast((rest.m - whole.m) * c) / whole.s;
+                    const float scale = rest.s != 0.f ? w * ((mass + p_rest) * q_rest - p_rest) / rest.s
+                                                      : whole.s != 0.f ? 0.f : NAN;
+                    sh.out = make_float4(scale, reference(rest.m), flags & kSome ? 1.f : 0.f, 0.f);
+                }
+            }
+            __syncwarp();
+            block_arrive(kAnswered, answered);
+        }
+        return;
+    }
+
+    // ---- the row
+    const uint64_t cc = f2_pack(c, c);
+    const int at0 = warp * kWarpPieces + lane;  // this thread's first piece; the next ones 32 on
+    const int left = pieces - at0, full = count / VEC - at0;
+    // what lies past the segment's end in its last piece counts as kept, too
+    uint2 past = make_uint2(0, 0);
+    if (left > 0 && left != full && (left - 1) % 32 == 0 && left <= kWarpPieces) {
+        constexpr int per = 32 / VEC;
+        const int j = left / 32;
+        const uint32_t m = ((1u << VEC) - (1u << (count % VEC))) << (j % per * VEC);
+        (j < per ? past.x : past.y) = m;
+    }
+    const bool tail = (past.x | past.y) != 0;
+    uint4 *const mine = dyn + at0;
+    const auto fetch = [&](int64_t b) {
+        const T *row = a.z + b * a.ld + lo + at0 * VEC;
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j)
+            if (j * 32 < left && in_range(1602, lo + (at0 + j * 32) * VEC, VEC, a.ld))
+                cp_async16(mine + j * 32, row + j * 32 * VEC);
+        ptx::cp_async_commit();
+    };
+    const auto strike = [&](uint32_t bits, int from) {  // values from + 0..31 that have a bit become -inf
+        while (bits != 0) {
+            const int v = from + __ffs(static_cast<int>(bits)) - 1;
+            bits &= bits - 1;
+            reinterpret_cast<T *>(mine + v / VEC * 32)[v % VEC] = L::lowest();
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j)  // pieces past the end stay -inf
+        if (j * 32 >= left)
+            mine[j * 32] = make_uint4(L::kLowest, L::kLowest, L::kLowest, L::kLowest);
+    fetch(first);
+    __syncthreads();
+    int turn = 0;
+    for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
+        const uint2 marks = sh.marks[turn][tid];
+        if ((marks.x | marks.y) != 0) sh.marks[turn][tid] = make_uint2(0, 0);
+        ptx::cp_async_wait_all();
+        strike(marks.x | past.x, 0);
+        strike(marks.y | past.y, 32);
+        uint4 v[ITEMS];
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) v[j] = mine[j * 32];
+        if (b + step < a.B) fetch(b + step);
+
+        Peak rest;
+        rest.m = L::template largest<ITEMS>(v);
+        {
+            const float r = reference(rest.m);
+            const uint64_t minus_r = f2_pack(-r, -r);
+            uint64_t s = 0;
+#pragma unroll
+            for (int j = 0; j < ITEMS; ++j) {
+                uint64_t f[VEC / 2];
+                L::pairs(v[j], f);
+#pragma unroll
+                for (int e = 0; e < VEC / 2; ++e) {
+                    float l, h;
+                    exp2_pair(f[e], minus_r, cc, l, h);
+                    s = f2_add(s, f2_pack(l, h));
+                }
+            }
+            float l, h;
+            f2_unpack(s, l, h);
+            rest.s = l + h;
+        }
+        rest = warp_merge(rest, c);
+        if (lane == 0) sh.rest[turn][warp] = make_float2(rest.m, rest.s);
+        __syncwarp();
+        if constexpr (GRAD)
+            block_arrive(kSummed, threads + 64);
+        else
+            block_sync(kSummed, threads + 64);  // the next row's marks are there
+        pass(b);
+        if constexpr (GRAD) {
+            block_sync(kAnswered, answered);
+            const float4 o = sh.out;
+            const uint64_t minus_r = f2_pack(-o.y, -o.y), times = f2_pack(o.x, o.x);
+            T *out = a.dz + b * a.ld + lo;
+            if (o.z == 0.f) {  // no entries: zeros, whatever z holds
+                for (int i = tid; i < count; i += threads) out[i] = L::from(0.f);
+                continue;
+            }
+            out += at0 * VEC;
+#pragma unroll
+            for (int j = 0; j < ITEMS; ++j) {
+                uint64_t f[VEC / 2];
+                float g[VEC];
+                // unpacked again here, not held in registers since the sum
+                asm volatile("" : "+r"(v[j].x), "+r"(v[j].y), "+r"(v[j].z), "+r"(v[j].w));
+                L::pairs(v[j], f);
+#pragma unroll
+                for (int e = 0; e < VEC / 2; ++e) {
+                    float l, h;
+                    exp2_pair(f[e], minus_r, cc, l, h);
+                    f2_unpack(f2_mul(f2_pack(l, h), times), g[2 * e], g[2 * e + 1]);
+                }
+                if (j * 32 < full) {
+                    if (in_range(1603, lo + (at0 + j * 32) * VEC, VEC, a.V))
+                        ptx::st_stream_v4(out + j * 32 * VEC, L::pack(g));
+                } else if (tail && j == left / 32) {
+                    store_some(out + j * 32 * VEC, L::pack(g), count % VEC);
+                }
+            }
+        }
+    }
+    if (S > 1) cluster_wait();
+    if constexpr (GRAD) block_arrive(kWritten, threads + 32);
 }
 
-// Blocks a row: a segment of at most kSegBytes; and more where rows are so few that SMs
-// would be idle.
-constexpr int kSegBytes = 72 << 10;
-constexpr int kMinSeg = 4096;
+// Blocks a row (a power of two up to 8), warps a block and pieces a thread.
+struct Plan {
+    int S, seg, warps, items;
+};
+constexpr int kPieces = 4096;    // a block's most, but where 8 blocks do not reach
+constexpr int kMinPieces = 256;  // rows are split further only down to this
+
+template <typename T>
+Plan plan_of(int64_t B, int V, int num_sms)
+{
+    constexpr int VEC = Logit<T>::kVec;
+    const auto seg_of = [&](int s) { return ((V + s - 1) / s + 7) / 8 * 8; };
+    Plan p;
+    p.S = 1;
+    while (p.S < kMaxCluster && seg_of(p.S) / VEC > kPieces) p.S *= 2;
+    // few rows: more blocks, and a piece a thread where that is enough
+    while (p.S < kMaxCluster && B * p.S * 2 <= num_sms && seg_of(p.S) / VEC > kMinPieces) p.S *= 2;
+    p.seg = seg_of(p.S);
+    const int pieces = p.seg / VEC, each = B * p.S <= num_sms ? 1 : kMaxItems;
+    const int most = (pieces + 32 * each - 1) / (32 * each);
+    const int warps = most < kMaxWarps ? most : kMaxWarps;
+    p.items = 1;
+    while (warps * 32 * p.items < pieces) p.items *= 2;
+    p.warps = (pieces + 32 * p.items - 1) / (32 * p.items);
+    return p;
+}
+
+template <typename T, bool GRAD, int ITEMS>
+cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, int num_sms, cudaStream_t stream)
+{
+    // Clusters that are resident at once: by device, log2 of the cluster, warps, and whether the
+    // entries take much shared memory
+    static std::atomic<int> resident[64][4][kMaxWarps + 1][2];
+    constexpr int most = kMaxThreads * ITEMS * 16 + kDistillMaxK * 32;
+    constexpr int few = 128;
+    int dev = 0, log_s = 0;
+    const int many = a.K > few;
+    while (1 << log_s < p.S) ++log_s;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(p.warps * 32 + 64);
+    const size_t pieces = static_cast<size_t>(p.warps) * 32 * ITEMS * 16;
+    cfg.dynamicSmemBytes = pieces + (many ? kDistillMaxK : few) * 32;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.S);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    int clusters = dev < 64 ? resident[dev][log_s][p.warps][many].load(std::memory_order_acquire) : 0;
+    if (clusters == 0) {
+        if ((e = cudaFuncSetAttribute(distill_kernel<T, GRAD, ITEMS>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess)
+            return e;
+        cfg.gridDim = dim3(static_cast<unsigned>(p.S));
+        cfg.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&clusters, distill_kernel<T, GRAD, ITEMS>, &cfg)) != cudaSuccess)
+            return e;
+        if (clusters < 1) clusters = 1;
+        if (dev < 64) resident[dev][log_s][p.warps][many].store(clusters, std::memory_order_release);
+    }
+    const int64_t rows = a.B < clusters ? a.B : clusters;
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * p.S));
+    cfg.dynamicSmemBytes = pieces + static_cast<size_t>(a.K) * 32;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, distill_kernel<T, GRAD, ITEMS>, a, p.seg, p.S);
+}
 
 template <typename T, bool GRAD>
 cudaError_t launch_as(const DistillArgs<T> &a, int num_sms, cudaStream_t stream)
 {
-    int S = 1;
-    const auto seg_of = [&](int s) { return ((a.V + s - 1) / s + 7) / 8 * 8; };
-    while (S < kMaxCluster && (static_cast<int64_t>(seg_of(S)) * sizeof(T) > kSegBytes ||
-                               (a.B * S < num_sms && seg_of(S) > kMinSeg)))
-        S *= 2;
-    const int seg = seg_of(S);
-    const size_t smem = static_cast<size_t>(seg) * sizeof(T) + static_cast<size_t>(a.K) * 12;
-    static std::atomic<uint64_t> done{0};
-    constexpr int most = static_cast<int>(kDistillMaxV / kMaxCluster * 4 + kDistillMaxK * 12);
-    cudaError_t e = once_per_device(done, [] {
-        return cudaFuncSetAttribute(distill_kernel<T, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    });
-    if (e != cudaSuccess) return e;
-    const int64_t rows = a.B < (int64_t{1} << 24) ? a.B : int64_t{1} << 24;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows * S));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(S);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = S > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, distill_kernel<T, GRAD>, a, seg, S);
+    const Plan p = plan_of<T>(a.B, a.V, num_sms);
+    switch (p.items) {
+    case 1: return launch_items<T, GRAD, 1>(a, p, num_sms, stream);
+    case 2: return launch_items<T, GRAD, 2>(a, p, num_sms, stream);
+    case 4: return launch_items<T, GRAD, 4>(a, p, num_sms, stream);
+    case 8: return launch_items<T, GRAD, 8>(a, p, num_sms, stream);
+    default:
+        if constexpr (Logit<T>::kVec * 16 <= kMaxBits) return launch_items<T, GRAD, 16>(a, p, num_sms, stream);
+        return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace

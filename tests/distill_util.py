@@ -3,9 +3,9 @@
 Roundings of the kernels, u = U32 = 2^-24 each (relative to the value):
   - exp((z - m)·c), c = inv_tau·log2 e: the difference, c twice, the product, each off by u of the
     exponent, so e^(4u·|x|) at |x| = |z - m|·inv_tau; the exponential itself 2^-22 = 4u.
-  - a sum over V values: a thread adds ceil(V / 512 / blocks) of them in turn, then 5 + 5 levels of
-    a tree, 8 blocks and 2 peaks, each of which shifts the sums to another largest value by an
-    exponential of its own.
+  - a sum over V values: a thread adds at most 64 of them in two chains, then 5 levels of a tree over
+    lanes, at most 8 in turn and 5 levels over warps and blocks, and 2 peaks; three times the sums are
+    shifted to another largest value by an exponential.  Teacher: 32 lanes add K / 32 each, 5 levels.
 """
 import torch
 
@@ -30,21 +30,20 @@ def distill64(z, ids, t, t_lse, inv_tau, dloss=None):
         at, x = ids[b][here], t[b][here] * it
         if t_lse is None:
             base = torch.logsumexp(x, 0)
-            e_lp = (K / 512 + 20) * U32 + 3 * U32 * (x.abs() + x.max().abs() + base.abs())
+            e_lp = (K / 32 + 20) * U32 + 3 * U32 * (x.abs() + x.max().abs() + base.abs())
         else:
             base = t_lse[b].double()
             e_lp = 2 * U32 * (x.abs() + base.abs())
         lp = x - base
         p = torch.exp(lp)
         e_p = p * (torch.expm1(e_lp) + 4 * U32)
-        s = z[b] * it
-        top = s[torch.isfinite(s)].max() if bool(torch.isfinite(s).any()) else s.max()
-        lse = top + torch.log(torch.exp(s - top).sum())
+        s = (z[b] - z[b].max()) * it  # all that follows is the same for s shifted
+        lse = torch.log(torch.exp(s).sum())
         kept = torch.zeros(V, dtype=torch.bool)
         kept[at] = True
-        far = (s[torch.isfinite(s)] - top).abs().max() if bool(torch.isfinite(s).any()) else 0.0
-        rel = U32 * (V / 512 + 40 + 3 * 4 * float(far) + 6 * 4)  # of a sum, or of q
-        mass, e_mass = p.sum(), e_p.sum() + (K / 512 + 10) * U32 * p.sum()
+        far = s[s > -150].abs().max()  # below that e^s is 0 in fp32
+        rel = U32 * (32 + 40 + 3 * 4 * float(far) + 6 * 4)  # of a sum, or of q
+        mass, e_mass = p.sum(), e_p.sum() + (K / 32 + 10) * U32 * p.sum()
         if t_lse is None:
             e_mass = e_mass + (mass - 1).abs()
         left = s[~kept]
@@ -58,10 +57,10 @@ def distill64(z, ids, t, t_lse, inv_tau, dloss=None):
                 e_rest = e_mass + U32
         log_q = s[at] - lse
         terms = torch.where(p > 0, p * (lp - log_q), torch.zeros_like(p))
-        e_log_q = 3 * U32 * (s[at] - top).abs() + rel + 3 * U32 * (lse - top).abs() + U32 * log_q.abs()
+        e_log_q = 3 * U32 * s[at].abs() + rel + 3 * U32 * lse.abs() + U32 * log_q.abs()
         tol = (e_p * (lp - log_q).abs() + p * (e_lp + e_log_q + 2 * U32 * (lp.abs() + log_q.abs()))).sum()
         value = terms.sum()
-        tol = tol + (K / 512 + 14) * U32 * terms.abs().sum()
+        tol = tol + (K / 32 + 14) * U32 * terms.abs().sum()
         if p_rest > 0 or e_rest > 0:
             if left.numel():
                 near = torch.log((p_rest + e_rest).clamp_min(1e-12)) - log_q_rest
@@ -74,7 +73,10 @@ def distill64(z, ids, t, t_lse, inv_tau, dloss=None):
         M, e_M = mass + p_rest, e_mass + e_rest
         P = torch.zeros(V, dtype=F64).index_add_(0, at, p)
         e_P = torch.zeros(V, dtype=F64).index_add_(0, at, e_p + K * U32 * p)
-        share = torch.exp(s - lse - log_q_rest) if left.numel() else torch.zeros(V, dtype=F64)  # q / q_rest
+        share = torch.zeros(V, dtype=F64)  # q / q_rest
+        if left.numel():
+            share = torch.exp(s - left.max())
+            share = share / share[~kept].sum()
         d = torch.where(kept, M * q - P, M * q - p_rest * share)
         e_kept = M * q * (2 * rel + 4 * U32) + q * e_M + e_P + 2 * U32 * (M * q + P)
         e_left = M * q * (3 * rel + 6 * U32) + q * e_M + share * e_rest + (3 * rel + 4 * U32) * (M * q + p_rest * share)

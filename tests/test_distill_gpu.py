@@ -216,6 +216,24 @@ def test_large_logits_and_temperatures():
         check(d, out, dz, inv_tau)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_a_vocabulary_masked_by_the_lowest_value(dt):
+    """The type's lowest value in place of -inf: the rest's largest logit may be that."""
+    B, V, K = 5, 4100, 5
+    low = torch.finfo(dt).min
+    for rest in (False, True):
+        d = make(17, B, V, K, dt, rest, 0.5)
+        keep = torch.zeros(B, V, dtype=torch.bool).scatter_(1, d["ids"], True)
+        mask = torch.rand(B, V, generator=torch.Generator().manual_seed(1)) < 0.5
+        mask[1:3] = True
+        d["z"] = torch.where(mask & ~keep, torch.tensor(low, dtype=dt), d["z"])
+        d["z"][3] = low  # every logit
+        g = Guarded()
+        out, dz, _ = call(d, up8(V), 0.5, g)
+        g.check()
+        check(d, out, dz, 0.5)
+
+
 def test_one_entry_is_cross_entropy():
     B, V = 37, 513
     d = make(12, B, V, 1, F32, False)
