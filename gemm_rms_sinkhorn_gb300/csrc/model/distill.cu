@@ -256,11 +256,11 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
     __syncthreads();
 
     if (warp == warps) {  // ---- the entries
-        // [2][K] x = t·inv_tau, the word that z lies in, id; [K] what follows a row later
-        float *const x2 = reinterpret_cast<float *>(dyn + warps * kWarpPieces);
-        uint32_t *const word2 = reinterpret_cast<uint32_t *>(x2 + 2 * a.K);
-        int *const id2 = reinterpret_cast<int *>(word2 + 2 * a.K);
-        float *const later = reinterpret_cast<float *>(id2 + 2 * a.K);
+        // [3][K] x = t·inv_tau, the word that z lies in, id; [K] what follows later, and where
+        float *const x3 = reinterpret_cast<float *>(dyn + warps * kWarpPieces);
+        uint32_t *const word3 = reinterpret_cast<uint32_t *>(x3 + 3 * a.K);
+        int *const id3 = reinterpret_cast<int *>(word3 + 3 * a.K);
+        float *const later = reinterpret_cast<float *>(id3 + 3 * a.K);
         int *const later_at = reinterpret_cast<int *>(later + a.K);  // -1: none
 
         constexpr int kAhead = 4;  // entries a lane that are read another row ahead
@@ -281,10 +281,10 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
         };
         int flags = 0;
         float base = 0.f, mass = 0.f, w = 0.f;
-        const auto prepare = [&](int64_t b, int turn) {  // after read_ahead(b)
-            float *x = x2 + turn * a.K;
-            uint32_t *word = word2 + turn * a.K;
-            int *idk = id2 + turn * a.K;
+        const auto prepare = [&](int64_t b, int turn, int place) {  // after read_ahead(b)
+            float *x = x3 + place * a.K;
+            uint32_t *word = word3 + place * a.K;
+            int *idk = id3 + place * a.K;
             const T *row = a.z + b * a.ld;
             float m = -INFINITY;
             flags = 0;
@@ -332,91 +332,111 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             for (int k = lane; k < a.K; k += 32)
                 if (later_at[k] >= 0 && in_range(1604, lo + later_at[k], 1, a.V)) out[later_at[k]] = L::from(later[k]);
         };
-        if constexpr (GRAD)
-            for (int k = lane; k < a.K; k += 32) later_at[k] = -1;
+        // What a joined row leaves to do: its loss, and the gradient at the kept ids, which
+        // waits in `later`.
+        struct Row {
+            int flags;
+            float base, mass, w;
+        };
+        const auto finish = [&](int64_t b, int place, const Row &row, const float4 &sums) {
+            const float *x = x3 + place * a.K;
+            const uint32_t *word = word3 + place * a.K;
+            const int *idk = id3 + place * a.K;
+            const Peak rest = {sums.x, sums.y}, whole = {sums.z, sums.w};
+            const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - row.mass, 0.f) : 0.f;
+            const bool losses = rank == 0 && a.loss != nullptr;
+            const float ln_s = logf(whole.s), inv_s = 1.f / whole.s;
+            float part = 0.f;
+#pragma unroll 1
+            for (int k = lane; k < a.K; k += 32) {
+                const int at = idk[k] - lo;
+                const bool mine = idk[k] >= 0 && at >= 0 && at < count;
+                if constexpr (GRAD) later_at[k] = mine ? at : -1;
+                if (!mine && !(losses && idk[k] >= 0)) continue;
+                const float lp = x[k] - row.base, p = expf(lp), z = L::word(word[k], idk[k]);
+                if (losses && p != 0.f) part += p * (lp - ((z - whole.m) * a.inv_tau - ln_s));
+                if constexpr (GRAD) {
+                    if (!mine) continue;
+                    float all = p;
+                    if (row.flags & kTwice) {
+                        all = 0.f;
+#pragma unroll 1
+                        for (int i = 0; i < a.K; ++i)
+                            if (idk[i] == idk[k]) all += expf(x[i] - row.base);
+                    }
+                    const float q = exp2_fast((z - reference(whole.m)) * c) * inv_s;
+                    later[k] = row.w * ((row.mass + p_rest) * q - all);
+                }
+            }
+            if (losses) {
+                part = warp_sum(part);
+                if (lane == 0) {
+                    if (p_rest > 0.f)
+                        part += p_rest * (logf(p_rest) - ((rest.m - whole.m) * a.inv_tau + logf(rest.s) - ln_s));
+                    a.loss[b] = row.flags & kSome ? part : 0.f;
+                }
+            }
+            __syncwarp();
+        };
         read_ahead(first);
-        prepare(first, 0);
+        prepare(first, 0, 0);
         if (first + step < a.B) read_ahead(first + step);
         __syncthreads();  // the first row's marks are there
-        int turn = 0;
+        int turn = 0, place = 0, before = 2;  // places in threes: of this row, of the one before
+        Row last = {};
+        float4 sums = {};
         for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
-            const float *x = x2 + turn * a.K;
-            const uint32_t *word = word2 + turn * a.K;
-            const int *idk = id2 + turn * a.K;
-            const int row_flags = flags;
-            const float row_base = base, row_mass = mass, row_w = w;
+            const uint32_t *word = word3 + place * a.K;
+            const int *idk = id3 + place * a.K;
+            const Row row = {flags, base, mass, w};
             ptx::cp_async_wait_all();
             __syncwarp();
+            // the kept entries, each id once
             Peak kept = {-INFINITY, 0.f};
+#pragma unroll 1
+            for (int k = lane; k < a.K; k += 32) {
+                const int at = idk[k] - lo;
+                if (idk[k] >= 0 && at >= 0 && at < count) kept.m = fmaxf(kept.m, L::word(word[k], idk[k]));
+            }
+            kept.m = warp_max(kept.m);
 #pragma unroll 1
             for (int k = lane; k < a.K; k += 32) {
                 const int at = idk[k] - lo;
                 if (idk[k] < 0 || at < 0 || at >= count) continue;
                 bool once = true;
-                if (row_flags & kTwice)
+                if (row.flags & kTwice)
 #pragma unroll 1
                     for (int i = 0; i < k; ++i) once = once && idk[i] != idk[k];
-                const float z = L::word(word[k], idk[k]), one = z == -INFINITY ? 0.f : z != z ? z : 1.f;
-                if (once) kept = merge(kept, {z, one}, c);
+                if (once) kept.s += exp2_fast((L::word(word[k], idk[k]) - reference(kept.m)) * c);
             }
-            kept = warp_merge(kept, c);
-            if (b + step < a.B) prepare(b + step, turn ^ 1);
+            kept.s = warp_sum(kept.s);
+            const int next = place == 2 ? 0 : place + 1;
+            if (b + step < a.B) prepare(b + step, turn ^ 1, next);
             if (lane == 0) {
-                sh.entry = make_float4(kept.m, kept.s, row_mass, row_w);
-                sh.flags = row_flags;
+                sh.entry = make_float4(kept.m, kept.s, row.mass, row.w);
+                sh.flags = row.flags;
             }
             __syncwarp();
             block_arrive(kSummed, threads + 64);
             pass(b);
+            // what is left of the row before, while this one is summed up
             if (b + 2 * step < a.B) read_ahead(b + 2 * step);
+            if (b != first) finish(b - step, before, last, sums);
             block_sync(kAnswered, answered);
-
-            const Peak rest = {sh.whole.x, sh.whole.y}, whole = {sh.whole.z, sh.whole.w};
-            const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - row_mass, 0.f) : 0.f;
-            if constexpr (GRAD) {
-                // everyone's stores of the row before precede this row's sums
+            sums = sh.whole;
+            // everyone's stores of the row before precede this row's sums
+            if constexpr (GRAD)
                 if (b != first) write_later(b - step);
-#pragma unroll 1
-                for (int k = lane; k < a.K; k += 32) {
-                    const int at = idk[k] - lo;
-                    const bool mine = idk[k] >= 0 && at >= 0 && at < count;
-                    later_at[k] = mine ? at : -1;
-                    if (!mine) continue;
-                    float p = expf(x[k] - row_base);
-                    if (row_flags & kTwice) {
-                        p = 0.f;
-#pragma unroll 1
-                        for (int i = 0; i < a.K; ++i)
-                            if (idk[i] == idk[k]) p += expf(x[i] - row_base);
-                    }
-                    const float z = L::word(word[k], idk[k]);
-                    const float q = exp2_fast((z - reference(whole.m)) * c) / whole.s;
-                    later[k] = row_w * ((row_mass + p_rest) * q - p);
-                }
-            }
-            if (rank == 0 && a.loss != nullptr) {
-                const float ln_s = logf(whole.s);
-                float part = 0.f;
-#pragma unroll 1
-                for (int k = lane; k < a.K; k += 32) {
-                    if (idk[k] < 0) continue;
-                    const float lp = x[k] - row_base, p = expf(lp);
-                    const float z = L::word(word[k], idk[k]);
-                    if (p != 0.f) part += p * (lp - ((z - whole.m) * a.inv_tau - ln_s));
-                }
-                part = warp_sum(part);
-                if (lane == 0) {
-                    if (p_rest > 0.f)
-                        part += p_rest * (logf(p_rest) - ((rest.m - whole.m) * a.inv_tau + logf(rest.s) - ln_s));
-                    a.loss[b] = row_flags & kSome ? part : 0.f;
-                }
-            }
-            __syncwarp();
+            last = row;
+            before = place;
+            place = next;
         }
         if (S > 1) cluster_wait();
+        const int64_t end = first + (a.B - 1 - first) / step * step;
+        finish(end, before, last, sums);
         if constexpr (GRAD) {
             block_sync(kWritten, threads + 32);
-            write_later(first + (a.B - 1 - first) / step * step);
+            write_later(end);
         }
         return;
     }
@@ -606,7 +626,7 @@ cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, int num_sms, cu
     // Clusters that are resident at once: by device, log2 of the cluster, warps, and whether the
     // entries take much shared memory
     static std::atomic<int> resident[64][4][kMaxWarps + 1][2];
-    constexpr int most = kMaxThreads * ITEMS * 16 + kDistillMaxK * 32;
+    constexpr int most = kMaxThreads * ITEMS * 16 + kDistillMaxK * 44;
     constexpr int few = 128;
     int dev = 0, log_s = 0;
     const int many = a.K > few;
@@ -616,7 +636,7 @@ cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, int num_sms, cu
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(p.warps * 32 + 64);
     const size_t pieces = static_cast<size_t>(p.warps) * 32 * ITEMS * 16;
-    cfg.dynamicSmemBytes = pieces + (many ? kDistillMaxK : few) * 32;
+    cfg.dynamicSmemBytes = pieces + (many ? kDistillMaxK : few) * 44;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -640,7 +660,7 @@ cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, int num_sms, cu
     }
     const int64_t rows = a.B < clusters ? a.B : clusters;
     cfg.gridDim = dim3(static_cast<unsigned>(rows * p.S));
-    cfg.dynamicSmemBytes = pieces + static_cast<size_t>(a.K) * 32;
+    cfg.dynamicSmemBytes = pieces + static_cast<size_t>(a.K) * 44;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, distill_kernel<T, GRAD, ITEMS>, a, p.seg, p.S);
 }
