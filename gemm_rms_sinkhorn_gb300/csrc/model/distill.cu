@@ -73,14 +73,28 @@ __device__ __forceinline__ void block_arrive(int id, int count)
 {
     asm volatile("barrier.cta.arrive.aligned %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
-// 16 bytes to `p`'s place in the shared memory of block `rank` of the cluster.
-__device__ __forceinline__ void st_cluster(float4 *p, uint32_t rank, float4 v)
+// The same for one of the barriers `id` and `id` + 1: by numbers known to the compiler, which
+// otherwise sets all 16 barriers aside for the block.
+__device__ __forceinline__ void block_sync_turn(int id, int turn, int count)
+{
+    if (turn == 0)
+        block_sync(id, count);
+    else
+        block_sync(id + 1, count);
+}
+__device__ __forceinline__ void block_arrive_turn(int id, int turn, int count)
+{
+    if (turn == 0)
+        block_arrive(id, count);
+    else
+        block_arrive(id + 1, count);
+}
+// 8 bytes to `p`'s place in the shared memory of block `rank` of the cluster.
+__device__ __forceinline__ void st_cluster(float2 *p, uint32_t rank, float2 v)
 {
     uint32_t at;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(v.x), "f"(v.y),
-                 "f"(v.z), "f"(v.w)
-                 : "memory");
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
 }
 __device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {
@@ -158,12 +172,13 @@ __device__ __forceinline__ Peak merge(Peak a, Peak b, float c)
     const float m = fmaxf(a.m, b.m), r = reference(m);
     return {m, a.s * exp2_fast((a.m - r) * c) + b.s * exp2_fast((b.m - r) * c)};
 }
-// Over the lanes of a warp, the same in each of them.
+// Over the lanes of a warp, the same in each of them.  The largest value in one instruction,
+// as integers of the same order (v is no NaN).
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
+    int i = __float_as_int(v);
+    i = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
+    return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF));
 }
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -201,19 +216,24 @@ __device__ __noinline__ void store_some(T *p, uint4 v, int n)
 }
 
 struct Shared {
-    float4 row[2][kMaxCluster];   // (rest.m, rest.s, kept.m, kept.s) by block
-    float4 entry;                 // of the row's entries: kept.m, kept.s, Σ p, dloss·inv_tau
-    float4 whole;                 // the row's: rest.m, rest.s, and of both together
+    float2 rests[2][kMaxCluster][kMaxWarps], kepts[2][kMaxCluster];  // the cluster's peaks
+    float4 entry[2];              // of the row's entries: kept.m, kept.s, Σ p, dloss·inv_tau
+    float4 whole[2];              // the row's: rest.m, rest.s, and of both together
     float4 out;                   // the gradient: what to multiply by, the reference, whether there is one
     float2 rest[2][kMaxWarps];    // peaks by warp
-    uint2 marks[2][kMaxThreads];  // bit j·VEC + e: value e of the thread's piece j is kept
-    int flags;
+    uint2 marks[3][kMaxThreads];  // bit j·VEC + e: value e of the thread's piece j is kept
+    int flags[2];
 };
 constexpr int kSome = 1, kTwice = 2;  // entries are present; an id comes more than once here
-// The block's barriers.  A row's sums, entries and the next row's marks are there: the
-// joining warp waits for it, without a gradient the others, too.  The row is joined: those
-// that have to do with the answer wait.  The last row is written: the entries' warp waits.
-constexpr int kSummed = 1, kAnswered = 2, kWritten = 3;
+// The block's barriers, and who waits at them.  Pairs are taken by rows in turn: who only
+// arrives may come for the next row before all have come for this one, but not for the one
+// after that.
+//   kSummed    a row's sums, its entries and the next row's marks are there: the joining
+//              warp; without a gradient the row's threads, too
+//   kAnswered  the gradient's factor is there: the row's threads
+//   kJoined    the row's whole sums are there: the entries' warp
+//   kWritten   the last row's gradient is written: the entries' warp
+constexpr int kSummed = 1, kJoined = 3, kAnswered = 5, kWritten = 6;  // kSummed, kJoined: pairs
 
 template <typename T, bool GRAD, int ITEMS>
 __global__ void __launch_bounds__(kMaxThreads + 64, ITEMS > 8 ? 1 : 2)
@@ -229,7 +249,6 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
 
     const int threads = blockDim.x - 64, warps = threads >> 5;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int answered = GRAD ? threads + 64 : 64;  // threads at that barrier
     const uint32_t rank = S > 1 ? cluster_rank() : 0;
     const int lo = static_cast<int>(rank) * seg;
     const int count = max(min(a.V - lo, seg), 0);
@@ -245,7 +264,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
         }
     };
 
-    for (int i = tid; i < 2 * kMaxThreads; i += blockDim.x) (&sh.marks[0][0])[i] = make_uint2(0, 0);
+    for (int i = tid; i < 3 * kMaxThreads; i += blockDim.x) (&sh.marks[0][0])[i] = make_uint2(0, 0);
     // No early trigger: blocks of the next kernel that wait in the places of these cost more
     // (4096 rows of 131072, back to back: 592 us, 473 without) than their start would save.
     ptx::pdl_wait();
@@ -281,7 +300,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
         };
         int flags = 0;
         float base = 0.f, mass = 0.f, w = 0.f;
-        const auto prepare = [&](int64_t b, int turn, int place) {  // after read_ahead(b)
+        const auto prepare = [&](int64_t b, int place) {  // after read_ahead(b)
             float *x = x3 + place * a.K;
             uint32_t *word = word3 + place * a.K;
             int *idk = id3 + place * a.K;
@@ -306,7 +325,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
                     const bool mine = at >= 0 && at < count;
                     if (mine) {
                         const int p = at / VEC, bit = p / 32 % ITEMS * VEC + at % VEC;
-                        uint32_t *mark = &sh.marks[turn][p / kWarpPieces * 32 + p % 32].x + (bit >> 5);
+                        uint32_t *mark = &sh.marks[place][p / kWarpPieces * 32 + p % 32].x + (bit >> 5);
                         if (atomicOr(mark, 1u << (bit & 31)) >> (bit & 31) & 1u) flags |= kTwice;
                     }
                     if ((rank == 0 || mine) && in_range(1605, i, 1, a.V))
@@ -379,12 +398,11 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             __syncwarp();
         };
         read_ahead(first);
-        prepare(first, 0, 0);
+        prepare(first, 0);
         if (first + step < a.B) read_ahead(first + step);
         __syncthreads();  // the first row's marks are there
         int turn = 0, place = 0, before = 2;  // places in threes: of this row, of the one before
         Row last = {};
-        float4 sums = {};
         for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
             const uint32_t *word = word3 + place * a.K;
             const int *idk = id3 + place * a.K;
@@ -411,29 +429,33 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             }
             kept.s = warp_sum(kept.s);
             const int next = place == 2 ? 0 : place + 1;
-            if (b + step < a.B) prepare(b + step, turn ^ 1, next);
+            if (b + step < a.B) prepare(b + step, next);
             if (lane == 0) {
-                sh.entry = make_float4(kept.m, kept.s, row.mass, row.w);
-                sh.flags = row.flags;
+                sh.entry[turn] = make_float4(kept.m, kept.s, row.mass, row.w);
+                sh.flags[turn] = row.flags;
             }
             __syncwarp();
-            block_arrive(kSummed, threads + 64);
+            block_arrive_turn(kSummed, turn, threads + 64);
             pass(b);
-            // what is left of the row before, while this one is summed up
             if (b + 2 * step < a.B) read_ahead(b + 2 * step);
-            if (b != first) finish(b - step, before, last, sums);
-            block_sync(kAnswered, answered);
-            sums = sh.whole;
-            // everyone's stores of the row before precede this row's sums
-            if constexpr (GRAD)
-                if (b != first) write_later(b - step);
+            // what is left of the row before, while this one is summed up and joined
+            if (b != first) {
+                block_sync_turn(kJoined, turn ^ 1, 64);
+                // everyone's stores of the row before that precede the row's sums
+                if constexpr (GRAD)
+                    if (b - step != first) write_later(b - 2 * step);
+                finish(b - step, before, last, sh.whole[turn ^ 1]);
+            }
             last = row;
             before = place;
             place = next;
         }
         if (S > 1) cluster_wait();
         const int64_t end = first + (a.B - 1 - first) / step * step;
-        finish(end, before, last, sums);
+        block_sync_turn(kJoined, turn ^ 1, 64);
+        if constexpr (GRAD)
+            if (end != first) write_later(end - step);
+        finish(end, before, last, sh.whole[turn ^ 1]);
         if constexpr (GRAD) {
             block_sync(kWritten, threads + 32);
             write_later(end);
@@ -445,26 +467,36 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
         __syncthreads();
         int turn = 0;
         for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
-            block_sync(kSummed, threads + 64);
+            block_sync_turn(kSummed, turn, threads + 64);
             Peak rest = {-INFINITY, 0.f};
             if (lane < warps) rest = {sh.rest[turn][lane].x, sh.rest[turn][lane].y};
-            const float4 entry = sh.entry;
-            const int flags = sh.flags;
-            rest = warp_merge(rest, c);
+            const float4 entry = sh.entry[turn];
+            const int flags = sh.flags[turn];
             Peak kept = {entry.x, entry.y};
             if (S > 1) {
-                if (lane < S) st_cluster(&sh.row[turn][rank], lane, make_float4(rest.m, rest.s, kept.m, kept.s));
+                if (lane < warps)
+                    for (int r = 0; r < S; ++r) st_cluster(&sh.rests[turn][rank][lane], r, make_float2(rest.m, rest.s));
+                if (lane < S) st_cluster(&sh.kepts[turn][rank], lane, make_float2(kept.m, kept.s));
                 cluster_arrive_release();
                 cluster_wait();
-                const float4 v = sh.row[turn][lane & (S - 1)];
-                rest = {v.x, lane < S ? v.y : 0.f};
-                kept = {v.z, lane < S ? v.w : 0.f};
-                rest = warp_merge(rest, c);
+                rest = kept = {-INFINITY, 0.f};
+                if (lane < S) kept = {sh.kepts[turn][lane].x, sh.kepts[turn][lane].y};
+                float2 p[kMaxCluster / 2];
+#pragma unroll
+                for (int i = 0; i < kMaxCluster / 2; ++i) {  // two blocks' warps at once
+                    const int r = 2 * i + lane / kMaxWarps, w = lane % kMaxWarps;
+                    p[i] = r < S && w < warps ? sh.rests[turn][r][w] : make_float2(-INFINITY, 0.f);
+                    rest.m = fmaxf(rest.m, p[i].x);
+                }
+#pragma unroll
+                for (int i = 0; i < kMaxCluster / 2; ++i)
+                    rest.s += p[i].y * exp2_fast((p[i].x - reference(rest.m)) * c);
                 kept = warp_merge(kept, c);
             }
+            rest = warp_merge(rest, c);
             const Peak whole = merge(rest, kept, c);
             if (lane == 0) {
-                sh.whole = make_float4(rest.m, rest.s, whole.m, whole.s);
+                sh.whole[turn] = make_float4(rest.m, rest.s, whole.m, whole.s);
                 if constexpr (GRAD) {
                     const float mass = entry.z, w = entry.w;
                     const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - mass, 0.f) : 0.f;
@@ -476,7 +508,8 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
                 }
             }
             __syncwarp();
-            block_arrive(kAnswered, answered);
+            if constexpr (GRAD) block_arrive(kAnswered, threads + 32);
+            block_arrive_turn(kJoined, turn, 64);
         }
         return;
     }
@@ -516,10 +549,10 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             mine[j * 32] = make_uint4(L::kLowest, L::kLowest, L::kLowest, L::kLowest);
     fetch(first);
     __syncthreads();
-    int turn = 0;
-    for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
-        const uint2 marks = sh.marks[turn][tid];
-        if ((marks.x | marks.y) != 0) sh.marks[turn][tid] = make_uint2(0, 0);
+    int turn = 0, place = 0;
+    for (int64_t b = first; b < a.B; b += step, turn ^= 1, place = place == 2 ? 0 : place + 1) {
+        const uint2 marks = sh.marks[place][tid];
+        if ((marks.x | marks.y) != 0) sh.marks[place][tid] = make_uint2(0, 0);
         ptx::cp_async_wait_all();
         strike(marks.x | past.x, 0);
         strike(marks.y | past.y, 32);
@@ -553,12 +586,12 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
         if (lane == 0) sh.rest[turn][warp] = make_float2(rest.m, rest.s);
         __syncwarp();
         if constexpr (GRAD)
-            block_arrive(kSummed, threads + 64);
+            block_arrive_turn(kSummed, turn, threads + 64);
         else
-            block_sync(kSummed, threads + 64);  // the next row's marks are there
+            block_sync_turn(kSummed, turn, threads + 64);  // the next row's marks are there
         pass(b);
         if constexpr (GRAD) {
-            block_sync(kAnswered, answered);
+            block_sync(kAnswered, threads + 32);
             const float4 o = sh.out;
             const uint64_t minus_r = f2_pack(-o.y, -o.y), times = f2_pack(o.x, o.x);
             T *out = a.dz + b * a.ld + lo;
