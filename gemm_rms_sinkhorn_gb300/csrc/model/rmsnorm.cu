@@ -8,10 +8,14 @@
 // mixing to the scaling, so the inputs are read once and each output is rounded once.
 // Bound by memory.
 //
-// A group of G threads takes a token, a thread chunks of 8 channels g, g + G, ...; the
-// sum of squares is added in a fixed order, by lane, warp and then warps in order.
+// Blocks walk the tokens.  A group of G threads takes a token, a thread chunks of 8 channels
+// g, g + G, ... of it, the same ones in every token.  It copies the chunks of the next tokens
+// into shared memory itself and alone reads them: copies are in flight while the block adds
+// up its squares and writes, and nothing else waits for them.  The sum of squares is added
+// in a fixed order, by lane, warp and then over the warps.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "check.cuh"
@@ -40,111 +44,202 @@ Layout layout_of(int64_t C)
     return l;
 }
 
-// Sum of v over the threads of a group.  Every thread of the block calls it; `red` holds a
-// value a warp and is not written again before every thread has passed the next call's
-// barrier (callers alternate between two).
+constexpr int kMaxWarps = kMaxThreads / 32;
+
+// Sum of v over the threads of a group: a tree over lanes, then one over its warps.  Every
+// thread of the block calls it; `red` holds a value a warp and is not written again before
+// every thread has passed the next call's barrier (callers alternate between two).
 __device__ __forceinline__ float group_sum(float v, float *red, int first_warp, int warps)
 {
+    static_assert(kMaxWarps == 16, "four steps join the warps");
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    if (lane == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < warps; ++w) s += red[first_warp + w];
-    return s;
+    v = (lane & 15) < warps ? red[first_warp + (lane & 15)] : 0.f;
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
 }
 
-template <int n>  // streams, or 0: A + R
-__device__ __forceinline__ void load_mixed(const NormArgs &a, int64_t b, int64_t c8, float (&f)[8])
+// 1/sqrt(ms): the approximation's 2 units in the last place and a Newton step.  0 where ms is
+// 0 (a row of zeros with eps = 0) or infinite.
+__device__ __forceinline__ float inverse_root(float ms)
 {
-    float t[8];
-    if constexpr (n == 0) {
-        unpack8(ptx::ld_stream_v4(a.X + b * a.C + c8 * 8), f);
-        if (a.R != nullptr) {
-            unpack8(ptx::ld_stream_v4(a.R + b * a.C + c8 * 8), t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] += t[e];
-        }
-    } else {
-        uint4 xv[n];
-        float h[n];
-#pragma unroll
-        for (int i = 0; i < n; ++i) xv[i] = ptx::ld_stream_v4(a.X + (b * n + i) * a.C + c8 * 8);
-#pragma unroll
-        for (int i = 0; i < n; ++i) h[i] = ptx::ld_dep(a.H_pre + b * n + i);
-        unpack8(xv[0], t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = h[0] * t[e];
-#pragma unroll
-        for (int i = 1; i < n; ++i) {
-            unpack8(xv[i], t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = fmaf(h[i], t[e], f[e]);
-        }
-    }
+    if (ms == 0.f) return 0.f;
+    const float y = rsqrtf(ms);
+    return y == 0.f ? 0.f : fmaf(0.5f * y, fmaf(-(ms * y), y, 1.f), y);
 }
 
-__device__ __forceinline__ void load_gain(const float *gain, int64_t c8, float (&g)[8])
+__device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {
-    const uint4 u = ptx::ld_dep_v4(gain + c8 * 8), v = ptx::ld_dep_v4(gain + c8 * 8 + 4);
-    g[0] = __uint_as_float(u.x); g[1] = __uint_as_float(u.y);
-    g[2] = __uint_as_float(u.z); g[3] = __uint_as_float(u.w);
-    g[4] = __uint_as_float(v.x); g[5] = __uint_as_float(v.y);
-    g[6] = __uint_as_float(v.z); g[7] = __uint_as_float(v.w);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+template <int N>  // all copies of this thread have landed but those of its last N groups
+__device__ __forceinline__ void cp_async_wait_but()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int n, int ITEMS, bool Q8>
-__global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a, int G, int T)
+// Chunks that a thread has room for, of P pieces of 16 bytes each: what it has read of one
+// makes room for the one that many on.  About 128 bytes a thread in flight, or 128 KB an SM,
+// in whole tokens; half a token where that is over 256 bytes a thread.
+__host__ __device__ constexpr int slots_of(int P, int items)
 {
-    __shared__ float red[2][kMaxThreads / 32];
-    const int group = threadIdx.x / G, g = threadIdx.x % G, warps = G >> 5;
-    const int64_t C8 = a.C >> 3, nb = kept_blocks(a.C);
-    ptx::pdl_wait();
-    ptx::pdl_trigger();
-    int turn = 0;
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * T; first < a.B;
-         first += static_cast<int64_t>(gridDim.x) * T, turn ^= 1) {
-        const int64_t b = first + group;
-        const bool have = b < a.B && in_range(1501, b, 1, a.B);
-        float f[ITEMS][8], ss = 0.f;
+    return P * items > 16 ? items / 2 : P * items >= 8 ? items : 8 / (P * items) * items;
+}
+// The gain of a thread's channels stays in shared memory, but where those are many.
+__host__ __device__ constexpr bool gain_kept(int items) { return items <= 2; }
+template <int P, int ITEMS>  // P pieces a chunk
+__host__ __device__ constexpr int smem_pieces()  // a thread's
+{
+    return slots_of(P, ITEMS) * P + (gain_kept(ITEMS) ? 2 * ITEMS : 0);
+}
+
+__device__ __forceinline__ void load_gain(const float *gain, int64_t c8, uint4 &u, uint4 &v)
+{
+    u = ptx::ld_dep_v4(gain + c8 * 8);
+    v = ptx::ld_dep_v4(gain + c8 * 8 + 4);
+}
+__device__ __forceinline__ void f32_pairs(const uint4 &u, const uint4 &v, uint64_t (&t)[4])
+{
+    t[0] = f2_pack(__uint_as_float(u.x), __uint_as_float(u.y));
+    t[1] = f2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
+    t[2] = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
+    t[3] = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+
+template <int n, int ITEMS, bool Q8>  // n: streams, or 0: A + R
+__global__ void __launch_bounds__(kMaxThreads, 2) rmsnorm_kernel(const NormArgs a, int G, int T)
+{
+    constexpr int P = n == 0 ? 2 : n, kSlots = slots_of(P, ITEMS), kWeights = n == 0 ? 1 : n;
+    constexpr int kRooms = kSlots < ITEMS ? 1 : kSlots / ITEMS;  // whole tokens
+    __shared__ float red[2][kMaxWarps];
+    extern __shared__ __align__(16) uint4 dyn[];  // [smem_pieces][blockDim]
+    const int stride = blockDim.x, group = threadIdx.x / G, g = threadIdx.x % G, warps = G >> 5;
+    const int C = static_cast<int>(a.C), C8 = C >> 3, nb = static_cast<int>(kept_blocks(C));
+    const uint32_t B = static_cast<uint32_t>(a.B), step = gridDim.x * T;
+    const float inv_C = 1.0f / static_cast<float>(C);
+    uint4 *const mine = dyn + threadIdx.x, *const gain = mine + kSlots * P * stride;
+    bool live[ITEMS];  // whether the thread has such a chunk
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k) {
-            const int64_t c8 = k * G + g;
-            if (have && c8 < C8) {
-                load_mixed<n>(a, b, c8, f[k]);
-                if (a.H != nullptr) ptx::st_stream_v4(a.H + b * a.C + c8 * 8, pack8(f[k]));
+    for (int k = 0; k < ITEMS; ++k) live[k] = k * G + g < C8;
+    // chunk k of token b, whose streams begin at `row`
+    const int64_t in_step = static_cast<int64_t>(step) * (n == 0 ? 1 : n) * C;
+    const auto fetch = [&](uint4 *slot, uint32_t b, int64_t row, int k) {
+        if (b < B && live[k] && in_range(1501, b, 1, a.B)) {
+            const uint16_t *x = a.X + row + (k * G + g) * 8;
+            cp_async16(slot, x);
+            if constexpr (n == 0) {
+                if (a.R != nullptr) cp_async16(slot + stride, a.R + row + (k * G + g) * 8);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[k][e] = 0.f;
+                for (int i = 1; i < n; ++i) cp_async16(slot + i * stride, x += C);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(f[k][e], f[k][e], ss);
         }
-        const float ms = group_sum(ss, red[turn], group * warps, warps) / static_cast<float>(a.C) + a.eps;
-        const float rstd = ms != 0.f ? 1.0f / sqrtf(ms) : 0.f;
+        ptx::cp_async_commit();
+    };
+    uint32_t b = blockIdx.x * T + group;
+    const int64_t row0 = static_cast<int64_t>(b) * (n == 0 ? 1 : n) * C;
+    ptx::pdl_wait();
+    ptx::pdl_trigger();
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u)
+        fetch(mine + u * P * stride, b + u / ITEMS * step, row0 + u / ITEMS * in_step, u % ITEMS);
+    if constexpr (gain_kept(ITEMS)) {
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k)
+            if (live[k]) load_gain(a.gain, k * G + g, gain[2 * k * stride], gain[(2 * k + 1) * stride]);
+    }
+    float h_next[kWeights];
+    const auto weights = [&](uint32_t b) {
+        if constexpr (n > 0) {
+            const float *h = a.H_pre + static_cast<int64_t>(b) * n;
+#pragma unroll
+            for (int i = 0; i < n; ++i) h_next[i] = b < B ? ptx::ld_dep(h + i) : 0.f;
+        }
+    };
+    weights(b);
+    int turn = 0, room = 0;
+    int64_t in_row = row0;
+    for (uint32_t first = blockIdx.x * T; first < B; first += step, b += step, in_row += in_step, turn ^= 1) {
+        const bool have = b < B;
+        const int64_t row = static_cast<int64_t>(b) * C;
+        uint4 *const slots = mine + room * P * ITEMS * stride;
+        room = room + 1 == kRooms ? 0 : room + 1;
+        float h[kWeights];
+#pragma unroll
+        for (int i = 0; i < kWeights; ++i) h[i] = h_next[i];
+        weights(b + step);
+        uint64_t f[ITEMS][4], ss = 0;
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            uint4 *const x = slots + k % kSlots * P * stride;
+            cp_async_wait_but<kSlots - 1>();
+#pragma unroll
+            for (int p = 0; p < 4; ++p) f[k][p] = 0;
+            if (have && live[k]) {
+                uint64_t t[4];
+                if constexpr (n == 0) {
+                    unpack8_pairs(x[0], f[k]);
+                    if (a.R != nullptr) {
+                        unpack8_pairs(x[stride], t);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) f[k][p] = f2_add(f[k][p], t[p]);
+                    }
+                } else {  // as pre_mix8 does, to the bit
+                    unpack8_pairs(x[0], t);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) f[k][p] = f2_mul(f2_pack(h[0], h[0]), t[p]);
+#pragma unroll
+                    for (int i = 1; i < n; ++i) {
+                        unpack8_pairs(x[i * stride], t);
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) f[k][p] = f2_fma(f2_pack(h[i], h[i]), t[p], f[k][p]);
+                    }
+                }
+                if (a.H != nullptr) ptx::st_stream_v4(a.H + row + (k * G + g) * 8, pack8_pairs(f[k]));
+            }
+            // into the same place: its values have been read
+            fetch(x, b + (k + kSlots) / ITEMS * step, in_row + (k + kSlots) / ITEMS * in_step, (k + kSlots) % ITEMS);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) ss = f2_fma(f[k][p], f[k][p], ss);
+        }
+        float lo, hi;
+        f2_unpack(ss, lo, hi);
+        const float rstd = inverse_root(fmaf(group_sum(lo + hi, red[turn], group * warps, warps), inv_C, a.eps));
         if (a.rstd != nullptr && have && g == 0) a.rstd[b] = rstd;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int64_t c8 = k * G + g;
-            const bool live = have && c8 < C8;
-            float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (live) {
-                float w[8];
-                load_gain(a.gain, c8, w);
+            const bool ok = have && live[k];
+            uint64_t z[4] = {0, 0, 0, 0};
+            if (ok) {
+                uint4 u, v;
+                if constexpr (gain_kept(ITEMS))
+                    u = gain[2 * k * stride], v = gain[(2 * k + 1) * stride];
+                else
+                    load_gain(a.gain, k * G + g, u, v);
+                uint64_t w[4];
+                f32_pairs(u, v, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = f[k][e] * rstd * w[e];
+                for (int p = 0; p < 4; ++p) z[p] = f2_mul(f2_mul(f[k][p], f2_pack(rstd, rstd)), w[p]);
             }
             if constexpr (Q8) {
-                uint32_t m = kept::amax8(z);
+                float q[8];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) f2_unpack(z[p], q[2 * p], q[2 * p + 1]);
+                uint32_t m = kept::amax8(q);
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 const uint32_t E = kept::scale_code_f32(m);
-                if (live) {
-                    kept::st_stream_v2(a.Zq + b * a.C + c8 * 8, kept::encode8(z, E));
-                    if ((c8 & 3) == 0) a.Zs[b * nb + (c8 >> 2)] = static_cast<uint8_t>(E);
+                if (ok) {
+                    kept::st_stream_v2(a.Zq + row + (k * G + g) * 8, kept::encode8(q, E));
+                    if ((g & 3) == 0)  // G is a multiple of 32
+                        a.Zs[static_cast<int64_t>(b) * nb + ((k * G + g) >> 2)] = static_cast<uint8_t>(E);
                 }
-            } else if (live) {
-                ptx::st_stream_v4(a.Z + b * a.C + c8 * 8, pack8(z));
+            } else if (ok) {
+                ptx::st_stream_v4(a.Z + row + (k * G + g) * 8, pack8_pairs(z));
             }
         }
     }
@@ -157,94 +252,142 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormArgs a, 
 // workspace, and a second launch adds the rows in order.
 constexpr int kBackwardBlocks = 2;  // blocks an SM
 
-template <int ITEMS>
-__global__ void __launch_bounds__(kMaxThreads)
+template <int ITEMS, bool SKIP>
+__global__ void __launch_bounds__(kMaxThreads, ITEMS <= 2 ? 2 : 1)
 rmsnorm_backward_kernel(const NormBackwardArgs a, int G, int T, float *__restrict__ parts)
 {
-    __shared__ float red[2][kMaxThreads / 32];
+    constexpr int P = SKIP ? 3 : 2, kSlots = slots_of(P, ITEMS), kRooms = kSlots / ITEMS;
+    static_assert(kSlots % ITEMS == 0, "rooms for whole tokens");
+    __shared__ float red[2][kMaxWarps];
     __shared__ float4 join[ITEMS == 1 ? 2 * kMaxThreads : 1];
-    const int group = threadIdx.x / G, g = threadIdx.x % G, warps = G >> 5;
-    const int64_t C8 = a.C >> 3;
+    extern __shared__ __align__(16) uint4 dyn[];  // [smem_pieces][blockDim]
+    const int stride = blockDim.x, group = threadIdx.x / G, g = threadIdx.x % G, warps = G >> 5;
+    const int C = static_cast<int>(a.C), C8 = C >> 3;
+    const uint32_t B = static_cast<uint32_t>(a.B), step = gridDim.x * T;
+    const float inv_C = 1.0f / static_cast<float>(C);
+    uint4 *const mine = dyn + threadIdx.x, *const gain = mine + kSlots * P * stride;
+    bool live[ITEMS];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) live[k] = k * G + g < C8;
+    const int64_t row_step = static_cast<int64_t>(step) * C;
+    const auto fetch = [&](uint4 *slot, uint32_t b, int64_t row, int k) {
+        if (b < B && live[k] && in_range(1511, b, 1, a.B)) {
+            const int64_t at = row + (k * G + g) * 8;
+            cp_async16(slot, a.dZ + at);
+            cp_async16(slot + stride, a.H + at);
+            if constexpr (SKIP) cp_async16(slot + 2 * stride, a.dH_skip + at);
+        }
+        ptx::cp_async_commit();
+    };
+    uint32_t b = blockIdx.x * T + group;
+    int64_t row = static_cast<int64_t>(b) * C;
     ptx::pdl_wait();
     ptx::pdl_trigger();
-    float acc[ITEMS][8];
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u)
+        fetch(mine + u * P * stride, b + u / ITEMS * step, row + u / ITEMS * row_step, u % ITEMS);
+    if constexpr (gain_kept(ITEMS)) {
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k)
+            if (live[k]) load_gain(a.gain, k * G + g, gain[2 * k * stride], gain[(2 * k + 1) * stride]);
+    }
+    const auto the_gain = [&](int k, uint64_t (&w)[4]) {
+        uint4 u, v;
+        if constexpr (gain_kept(ITEMS))
+            u = gain[2 * k * stride], v = gain[(2 * k + 1) * stride];
+        else
+            load_gain(a.gain, k * G + g, u, v);
+        f32_pairs(u, v, w);
+    };
+    uint64_t acc[ITEMS][4];
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
-    int turn = 0;
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * T; first < a.B;
-         first += static_cast<int64_t>(gridDim.x) * T, turn ^= 1) {
-        const int64_t b = first + group;
-        const bool have = b < a.B && in_range(1511, b, 1, a.B);
-        const float rstd = have ? ptx::ld_dep(a.rstd + b) : 0.f;
+        for (int p = 0; p < 4; ++p) acc[k][p] = 0;
+    const auto the_rstd = [&](uint32_t b) { return b < B ? ptx::ld_dep(a.rstd + b) : 0.f; };
+    float rstd_next = the_rstd(b);
+    int turn = 0, room = 0;
+    for (uint32_t first = blockIdx.x * T; first < B; first += step, b += step, row += row_step, turn ^= 1) {
+        const bool have = b < B;
+        uint4 *const slots = mine + room * P * ITEMS * stride;
+        room = room + 1 == kRooms ? 0 : room + 1;
+        const float rstd = rstd_next;
+        rstd_next = the_rstd(b + step);
+        const uint64_t rr = f2_pack(rstd, rstd);
         uint4 dz[ITEMS], hv[ITEMS], sk[ITEMS];
+        uint64_t ss = 0;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int64_t c8 = k * G + g;
+            uint4 *const x = slots + k % kSlots * P * stride;
+            cp_async_wait_but<kSlots - 1>();
             dz[k] = hv[k] = sk[k] = make_uint4(0, 0, 0, 0);
-            if (have && c8 < C8) {
-                dz[k] = ptx::ld_stream_v4(a.dZ + b * a.C + c8 * 8);
-                hv[k] = ptx::ld_stream_v4(a.H + b * a.C + c8 * 8);
-                if (a.dH_skip != nullptr) sk[k] = ptx::ld_stream_v4(a.dH_skip + b * a.C + c8 * 8);
-            }
-        }
-        float s = 0.f;
+            if (have && live[k]) {
+                dz[k] = x[0];
+                hv[k] = x[stride];
+                if constexpr (SKIP) sk[k] = x[2 * stride];
+                uint64_t d[4], h[4], w[4];
+                unpack8_pairs(dz[k], d);
+                unpack8_pairs(hv[k], h);
+                the_gain(k, w);
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k) {
-            const int64_t c8 = k * G + g;
-            float d[8], h[8], w[8];
-            unpack8(dz[k], d);
-            unpack8(hv[k], h);
-            if (c8 < C8) {
-                load_gain(a.gain, c8, w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    s = fmaf(w[e] * d[e], h[e], s);
-                    acc[k][e] = fmaf(d[e] * rstd, h[e], acc[k][e]);
+                for (int p = 0; p < 4; ++p) {
+                    ss = f2_fma(f2_mul(w[p], d[p]), h[p], ss);
+                    acc[k][p] = f2_fma(f2_mul(d[p], rr), h[p], acc[k][p]);
                 }
             }
+            fetch(x, b + kRooms * step, row + kRooms * row_step, k);
         }
-        const float sum = group_sum(s, red[turn], group * warps, warps);
-        const float back = rstd * rstd * (sum / static_cast<float>(a.C));
+        float lo, hi;
+        f2_unpack(ss, lo, hi);
+        const float sum = group_sum(lo + hi, red[turn], group * warps, warps);
+        const float back = -(rstd * rstd * (sum * inv_C));
+        const uint64_t bb = f2_pack(back, back);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
-            const int64_t c8 = k * G + g;
-            if (!have || c8 >= C8) continue;
-            float d[8], h[8], w[8], o[8];
-            unpack8(dz[k], d);
-            unpack8(hv[k], h);
-            unpack8(sk[k], o);
-            load_gain(a.gain, c8, w);
+            if (!have || !live[k]) continue;
+            uint64_t d[4], h[4], w[4], o[4];
+            unpack8_pairs(dz[k], d);
+            unpack8_pairs(hv[k], h);
+            unpack8_pairs(sk[k], o);
+            the_gain(k, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = fmaf(rstd, fmaf(-h[e], back, w[e] * d[e]), o[e]);
-            ptx::st_stream_v4(a.dH + b * a.C + c8 * 8, pack8(o));
+            for (int p = 0; p < 4; ++p) o[p] = f2_fma(rr, f2_fma(h[p], bb, f2_mul(w[p], d[p])), o[p]);
+            ptx::st_stream_v4(a.dH + row + (k * G + g) * 8, pack8_pairs(o));
         }
     }
     // the sums of a block's tokens, group by group
+    float4 sum[ITEMS][2];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            f2_unpack(acc[k][2 * p], sum[k][p].x, sum[k][p].y);
+            f2_unpack(acc[k][2 * p + 1], sum[k][p].z, sum[k][p].w);
+        }
     if constexpr (ITEMS == 1) {
-        join[2 * threadIdx.x] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
-        join[2 * threadIdx.x + 1] = make_float4(acc[0][4], acc[0][5], acc[0][6], acc[0][7]);
+        join[2 * threadIdx.x] = sum[0][0];
+        join[2 * threadIdx.x + 1] = sum[0][1];
         __syncthreads();
         if (group != 0) return;
-        for (int k = 1; k < T; ++k) {
-            const float4 u = join[2 * (k * G + g)], v = join[2 * (k * G + g) + 1];
-            acc[0][0] += u.x; acc[0][1] += u.y; acc[0][2] += u.z; acc[0][3] += u.w;
-            acc[0][4] += v.x; acc[0][5] += v.y; acc[0][6] += v.z; acc[0][7] += v.w;
-        }
+        for (int k = 1; k < T; ++k)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float4 u = join[2 * (k * G + g) + p];
+                sum[0][p].x += u.x; sum[0][p].y += u.y; sum[0][p].z += u.z; sum[0][p].w += u.w;
+            }
     }
-    float *row = parts + static_cast<int64_t>(blockIdx.x) * a.C;
+    float *part = parts + static_cast<int64_t>(blockIdx.x) * C;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int64_t c8 = k * G + g;
-        if (c8 >= C8 || !in_range(1512, c8 * 8, 8, a.C)) continue;
-        *reinterpret_cast<float4 *>(row + c8 * 8) = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
-        *reinterpret_cast<float4 *>(row + c8 * 8 + 4) = make_float4(acc[k][4], acc[k][5], acc[k][6], acc[k][7]);
+        const int c8 = k * G + g;
+        if (!live[k] || !in_range(1512, c8 * 8, 8, a.C)) continue;
+        *reinterpret_cast<float4 *>(part + c8 * 8) = sum[k][0];
+        *reinterpret_cast<float4 *>(part + c8 * 8 + 4) = sum[k][1];
     }
 }
 
 // dgain (+)= the rows of `parts`, by slices of rows and then slices in order.
-constexpr int kJoinCols = 32, kJoinSlices = 8;
+constexpr int kJoinCols = 32, kJoinSlices = 16;
 __global__ void __launch_bounds__(kJoinCols * kJoinSlices)
 rmsnorm_join_kernel(const float *parts, int rows, int64_t C, int accumulate, float *dgain)
 {
@@ -255,8 +398,16 @@ rmsnorm_join_kernel(const float *parts, int rows, int64_t C, int accumulate, flo
     ptx::pdl_trigger();
     float s = 0.f;
     if (c < C)
-#pragma unroll 4
-        for (int r = slice; r < rows; r += kJoinSlices) s += ptx::ld_dep(parts + r * C + c);
+        for (int r0 = slice; r0 < rows; r0 += 8 * kJoinSlices) {  // eight loads in flight
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int r = r0 + u * kJoinSlices;
+                v[u] = r < rows ? ptx::ld_dep(parts + r * C + c) : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += v[u];
+        }
     part[slice][col] = s;
     __syncthreads();
     if (slice != 0 || c >= C) return;
@@ -272,16 +423,69 @@ int backward_blocks(int64_t B, int64_t C, int num_sms)
     return static_cast<int>(all < most ? all : most);
 }
 
+// Launches `kernel` with P pieces a chunk and `smem` bytes a thread; blocks: at most that many,
+// or 0: as many as are resident at once.
+template <typename Args, typename... More>
+cudaError_t launch_walking(void (*kernel)(const Args, int, int, More...), std::atomic<uint64_t> &done,
+                           std::atomic<int> *resident, int pieces, int64_t B, int64_t C, int blocks, int num_sms,
+                           cudaStream_t stream, const Args &a, More... more)
+{
+    const Layout l = layout_of(C);
+    const int threads = l.group * l.tokens;
+    const size_t smem = static_cast<size_t>(pieces) * threads * 16;
+    cudaError_t e = once_per_device(done, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pieces * kMaxThreads * 16);
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t all = (B + l.tokens - 1) / l.tokens;
+    if (blocks == 0) {
+        int each = resident[threads / 32].load(std::memory_order_relaxed);
+        if (each == 0) {
+            if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, threads, smem)) != cudaSuccess) return e;
+            if (each < 1) each = 1;
+            resident[threads / 32].store(each, std::memory_order_relaxed);
+        }
+        const int64_t most = static_cast<int64_t>(each) * num_sms;
+        blocks = static_cast<int>(all < most ? all : most);
+    }
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, stream, a, l.group, l.tokens,
+                      more...);
+}
+
+template <int n, int ITEMS, bool Q8>
+cudaError_t launch_forward_as(const NormArgs &a, int num_sms, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> done{0};
+    static std::atomic<int> resident[kMaxThreads / 32 + 1];
+    return launch_walking(rmsnorm_kernel<n, ITEMS, Q8>, done, resident, smem_pieces<n == 0 ? 2 : n, ITEMS>(), a.B, a.C, 0,
+                          num_sms, stream, a);
+}
+
 template <int n, bool Q8>
 cudaError_t launch_forward_n(const NormArgs &a, int num_sms, cudaStream_t stream)
 {
-    const Layout l = layout_of(a.C);
-    const int64_t all = (a.B + l.tokens - 1) / l.tokens, most = int64_t{1} << 30;
-    const dim3 grid(static_cast<unsigned>(all < most ? all : most)), block(l.group * l.tokens);
-    switch (l.items) {
-    case 1: return launch_pdl(rmsnorm_kernel<n, 1, Q8>, grid, block, 0, stream, a, l.group, l.tokens);
-    case 2: return launch_pdl(rmsnorm_kernel<n, 2, Q8>, grid, block, 0, stream, a, l.group, l.tokens);
-    default: return launch_pdl(rmsnorm_kernel<n, 4, Q8>, grid, block, 0, stream, a, l.group, l.tokens);
+    switch (layout_of(a.C).items) {
+    case 1: return launch_forward_as<n, 1, Q8>(a, num_sms, stream);
+    case 2: return launch_forward_as<n, 2, Q8>(a, num_sms, stream);
+    default: return launch_forward_as<n, 4, Q8>(a, num_sms, stream);
+    }
+}
+
+template <int ITEMS, bool SKIP>
+cudaError_t launch_backward_as(const NormBackwardArgs &a, int blocks, float *parts, int num_sms, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> done{0};
+    return launch_walking(rmsnorm_backward_kernel<ITEMS, SKIP>, done, nullptr, smem_pieces<SKIP ? 3 : 2, ITEMS>(), a.B,
+                          a.C, blocks, num_sms, stream, a, parts);
+}
+
+template <bool SKIP>
+cudaError_t launch_backward_skip(const NormBackwardArgs &a, int blocks, float *parts, int num_sms, cudaStream_t stream)
+{
+    switch (layout_of(a.C).items) {
+    case 1: return launch_backward_as<1, SKIP>(a, blocks, parts, num_sms, stream);
+    case 2: return launch_backward_as<2, SKIP>(a, blocks, parts, num_sms, stream);
+    default: return launch_backward_as<4, SKIP>(a, blocks, parts, num_sms, stream);
     }
 }
 
@@ -309,16 +513,10 @@ size_t rmsnorm_backward_workspace_bytes(int64_t B, int64_t C, int num_sms)
 cudaError_t launch_rmsnorm_backward(const NormBackwardArgs &a, void *workspace, int num_sms,
                                     cudaStream_t stream)
 {
-    const Layout l = layout_of(a.C);
     const int blocks = backward_blocks(a.B, a.C, num_sms);
-    const dim3 grid(blocks), block(l.group * l.tokens);
     float *parts = static_cast<float *>(workspace);
-    cudaError_t e;
-    switch (l.items) {
-    case 1: e = launch_pdl(rmsnorm_backward_kernel<1>, grid, block, 0, stream, a, l.group, l.tokens, parts); break;
-    case 2: e = launch_pdl(rmsnorm_backward_kernel<2>, grid, block, 0, stream, a, l.group, l.tokens, parts); break;
-    default: e = launch_pdl(rmsnorm_backward_kernel<4>, grid, block, 0, stream, a, l.group, l.tokens, parts); break;
-    }
+    const cudaError_t e = a.dH_skip != nullptr ? launch_backward_skip<true>(a, blocks, parts, num_sms, stream)
+                                               : launch_backward_skip<false>(a, blocks, parts, num_sms, stream);
     if (e != cudaSuccess) return e;
     return launch_pdl(rmsnorm_join_kernel, dim3(static_cast<unsigned>((a.C + kJoinCols - 1) / kJoinCols)),
                       dim3(kJoinCols * kJoinSlices), 0, stream, parts, blocks, a.C, a.accumulate, a.dgain);
