@@ -13,16 +13,17 @@
 //
 // A row is read once and its gradient written once: the blocks of a cluster of up to 8 hold
 // a segment each, a thread up to 64 values in registers, and walk the rows.  A thread's
-// pieces of the next row are copied into shared memory meanwhile; only it reads them, so
-// nothing else has to wait for them.
+// pieces of the next segment are copied into shared memory meanwhile; only it reads them, so
+// nothing else has to wait for them.  Without a gradient nothing has to be held, and a block
+// takes several segments of a row one after another; clusters are for few rows then.
 //
 // Two more warps keep all else away from those.  One takes the K entries, a row ahead: it
-// works out the teacher's sums, fetches the student's logits there and marks the kept ids in
-// a bit map, a word a thread; the thread overwrites its marked values with -inf before it
-// reads them.  The other joins a row's sums, over warps and then over the cluster through
-// distributed shared memory, and answers with the factor of the gradient.  What is due at
-// the kept ids is written a row later, behind what the row's threads wrote there.  dz may be
-// z: a row is written after all of the cluster has summed it up.
+// works out the teacher's sums, fetches the student's logits there and marks the kept ids of
+// the next segment in a bit map, a word a thread; the thread overwrites its marked values
+// with -inf before it reads them.  The other joins a row's sums, over warps and over the
+// cluster through distributed shared memory, and answers with the factor of the gradient.
+// What is due at the kept ids is written a row later, behind what the row's threads wrote
+// there.  dz may be z: a row is written after all of the cluster has summed it up.
 //
 // Exponentials are exp2((z - m)·c), c = inv_tau·log2 e, m the largest z seen, two values at
 // a time.  As one fused multiply-add z·c - m·c they would be off by what m·c rounds away:
@@ -221,23 +222,24 @@ struct Shared {
     float4 whole[2];              // the row's: rest.m, rest.s, and of both together
     float4 out;                   // the gradient: what to multiply by, the reference, whether there is one
     float2 rest[2][kMaxWarps];    // peaks by warp
-    uint2 marks[3][kMaxThreads];  // bit j·VEC + e: value e of the thread's piece j is kept
+    uint2 marks[2][kMaxThreads];  // bit j·VEC + e: value e of the thread's piece j is kept
     int flags[2];
 };
 constexpr int kSome = 1, kTwice = 2;  // entries are present; an id comes more than once here
-// The block's barriers, and who waits at them.  Pairs are taken by rows in turn: who only
-// arrives may come for the next row before all have come for this one, but not for the one
-// after that.
-//   kSummed    a row's sums, its entries and the next row's marks are there: the joining
-//              warp; without a gradient the row's threads, too
-//   kAnswered  the gradient's factor is there: the row's threads
-//   kJoined    the row's whole sums are there: the entries' warp
-//   kWritten   the last row's gradient is written: the entries' warp
-constexpr int kSummed = 1, kJoined = 3, kAnswered = 5, kWritten = 6;  // kSummed, kJoined: pairs
+// The block's barriers:
+//   kSegment   a segment's marks are there, and the one before is done with: the row's
+//              threads and the entries' warp meet
+//   kSummed    a row's sums and entries are there: the joining warp waits
+//   kAnswered  the gradient's factor is there: the row's threads wait
+//   kJoined    the row's whole sums are there: the entries' warp waits
+// kSummed and kJoined are pairs that rows take in turn: who only arrives there may come for
+// the next row before all have come for this one, but not for the one after that.
+constexpr int kSegment = 1, kSummed = 2, kJoined = 4, kAnswered = 6;
 
+// S blocks a row, Q segments of `seg` values a block.
 template <typename T, bool GRAD, int ITEMS>
 __global__ void __launch_bounds__(kMaxThreads + 64, ITEMS > 8 ? 1 : 2)
-distill_kernel(const DistillArgs<T> a, int seg, int S)
+distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
 {
     using L = Logit<T>;
     constexpr int VEC = L::kVec;
@@ -247,12 +249,11 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
     extern __shared__ __align__(16) uint4 dyn[];
     constexpr int kWarpPieces = ITEMS * 32;
 
+    const int Q = GRAD ? 1 : segments;
     const int threads = blockDim.x - 64, warps = threads >> 5;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = S > 1 ? cluster_rank() : 0;
-    const int lo = static_cast<int>(rank) * seg;
-    const int count = max(min(a.V - lo, seg), 0);
-    const int pieces = (count + VEC - 1) / VEC;
+    const int lo = static_cast<int>(rank) * Q * seg;
     const float c = a.inv_tau * kLog2e;
     const int64_t step = gridDim.x / S, first = blockIdx.x / S;
     // A row's barrier of the cluster, for the warps that do not wait for the others' sums:
@@ -264,7 +265,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
         }
     };
 
-    for (int i = tid; i < 3 * kMaxThreads; i += blockDim.x) (&sh.marks[0][0])[i] = make_uint2(0, 0);
+    for (int i = tid; i < 2 * kMaxThreads; i += blockDim.x) (&sh.marks[0][0])[i] = make_uint2(0, 0);
     // No early trigger: blocks of the next kernel that wait in the places of these cost more
     // (4096 rows of 131072, back to back: 592 us, 473 without) than their start would save.
     ptx::pdl_wait();
@@ -275,12 +276,11 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
     __syncthreads();
 
     if (warp == warps) {  // ---- the entries
-        // [3][K] x = t·inv_tau, the word that z lies in, id; [K] what follows later, and where
-        float *const x3 = reinterpret_cast<float *>(dyn + warps * kWarpPieces);
-        uint32_t *const word3 = reinterpret_cast<uint32_t *>(x3 + 3 * a.K);
-        int *const id3 = reinterpret_cast<int *>(word3 + 3 * a.K);
-        float *const later = reinterpret_cast<float *>(id3 + 3 * a.K);
-        int *const later_at = reinterpret_cast<int *>(later + a.K);  // -1: none
+        // [2][K] by row in turn: x = t·inv_tau, the word that z lies in, id (-1: absent)
+        float *const x2 = reinterpret_cast<float *>(dyn + warps * kWarpPieces);
+        uint32_t *const word2 = reinterpret_cast<uint32_t *>(x2 + 2 * a.K);
+        int *const id2 = reinterpret_cast<int *>(word2 + 2 * a.K);
+        const int mine = max(min(a.V - lo, Q * seg), 0);  // of the row's values
 
         constexpr int kAhead = 4;  // entries a lane that are read another row ahead
         int64_t id[kAhead];
@@ -298,15 +298,17 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             if (a.t_lse != nullptr) lse = ptx::ld_dep(a.t_lse + b);
             if constexpr (GRAD) dloss = ptx::ld_dep(a.dloss + b);
         };
-        int flags = 0;
-        float base = 0.f, mass = 0.f, w = 0.f;
-        const auto prepare = [&](int64_t b, int place) {  // after read_ahead(b)
-            float *x = x3 + place * a.K;
-            uint32_t *word = word3 + place * a.K;
-            int *idk = id3 + place * a.K;
+        struct Row {
+            int flags;
+            float base, mass, w;  // what x is taken relative to for log p, Σ p, dloss·inv_tau
+        };
+        const auto prepare = [&](int64_t b, int turn) -> Row {  // after read_ahead(b)
+            float *x = x2 + turn * a.K;
+            uint32_t *word = word2 + turn * a.K;
+            int *idk = id2 + turn * a.K;
             const T *row = a.z + b * a.ld;
+            Row r = {0, 0.f, 1.f, dloss * a.inv_tau};
             float m = -INFINITY;
-            flags = 0;
 #pragma unroll 1
             for (int k0 = lane; k0 < a.K; k0 += 32 * kAhead) {
                 if (k0 != lane) read(b, k0);
@@ -319,21 +321,15 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
                     idk[k] = i;
                     x[k] = t[u] * a.inv_tau;
                     if (!here) continue;
-                    flags |= kSome;
+                    r.flags = kSome;
                     m = fmaxf(m, x[k]);
-                    const int at = i - lo;
-                    const bool mine = at >= 0 && at < count;
-                    if (mine) {
-                        const int p = at / VEC, bit = p / 32 % ITEMS * VEC + at % VEC;
-                        uint32_t *mark = &sh.marks[place][p / kWarpPieces * 32 + p % 32].x + (bit >> 5);
-                        if (atomicOr(mark, 1u << (bit & 31)) >> (bit & 31) & 1u) flags |= kTwice;
-                    }
-                    if ((rank == 0 || mine) && in_range(1605, i, 1, a.V))
+                    if ((rank == 0 || static_cast<unsigned>(i - lo) < static_cast<unsigned>(mine)) &&
+                        in_range(1605, i, 1, a.V))
                         ptx::cp_async4(word + k, row + (i & -L::kWord));
                 }
             }
             ptx::cp_async_commit();
-            flags = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(flags)));
+            r.flags = __any_sync(0xffffffffu, r.flags) ? kSome : 0;
             __syncwarp();
             m = a.t_lse != nullptr ? lse : warp_max(m);
             float s = 0.f;
@@ -341,26 +337,30 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             for (int k = lane; k < a.K; k += 32)
                 if (idk[k] >= 0) s += expf(x[k] - m);
             s = warp_sum(s);
-            base = a.t_lse != nullptr ? m : m + logf(s);
-            mass = a.t_lse != nullptr ? s : 1.f;
-            w = dloss * a.inv_tau;
+            r.base = a.t_lse != nullptr ? m : m + logf(s);
+            if (a.t_lse != nullptr) r.mass = s;
+            return r;
         };
-        const auto write_later = [&](int64_t b) {
-            T *out = a.dz + b * a.ld + lo;
+        // Marks the kept ids of segment q; kTwice where one has been marked before.
+        const auto mark = [&](int turn, int q, int unit) {
+            const int *idk = id2 + turn * a.K;
+            const int from = lo + q * seg, count = max(min(a.V - from, seg), 0);
+            bool twice = false;
 #pragma unroll 1
-            for (int k = lane; k < a.K; k += 32)
-                if (later_at[k] >= 0 && in_range(1604, lo + later_at[k], 1, a.V)) out[later_at[k]] = L::from(later[k]);
+            for (int k = lane; k < a.K; k += 32) {
+                const int at = idk[k] - from;
+                if (idk[k] < 0 || at < 0 || at >= count) continue;
+                const int p = at / VEC, bit = p / 32 % ITEMS * VEC + at % VEC;
+                uint32_t *w = &sh.marks[unit][p / kWarpPieces * 32 + p % 32].x + (bit >> 5);
+                twice |= (atomicOr(w, 1u << (bit & 31)) >> (bit & 31) & 1u) != 0;
+            }
+            return __any_sync(0xffffffffu, twice) ? kTwice : 0;
         };
-        // What a joined row leaves to do: its loss, and the gradient at the kept ids, which
-        // waits in `later`.
-        struct Row {
-            int flags;
-            float base, mass, w;
-        };
-        const auto finish = [&](int64_t b, int place, const Row &row, const float4 &sums) {
-            const float *x = x3 + place * a.K;
-            const uint32_t *word = word3 + place * a.K;
-            const int *idk = id3 + place * a.K;
+        // What a joined row leaves to do: its loss, and the gradient at the kept ids.
+        const auto finish = [&](int64_t b, int turn, const Row &row, const float4 &sums) {
+            const float *x = x2 + turn * a.K;
+            const uint32_t *word = word2 + turn * a.K;
+            const int *idk = id2 + turn * a.K;
             const Peak rest = {sums.x, sums.y}, whole = {sums.z, sums.w};
             const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - row.mass, 0.f) : 0.f;
             const bool losses = rank == 0 && a.loss != nullptr;
@@ -368,23 +368,22 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             float part = 0.f;
 #pragma unroll 1
             for (int k = lane; k < a.K; k += 32) {
-                const int at = idk[k] - lo;
-                const bool mine = idk[k] >= 0 && at >= 0 && at < count;
-                if constexpr (GRAD) later_at[k] = mine ? at : -1;
-                if (!mine && !(losses && idk[k] >= 0)) continue;
-                const float lp = x[k] - row.base, p = expf(lp), z = L::word(word[k], idk[k]);
+                const int i = idk[k];
+                const bool here = i >= 0 && static_cast<unsigned>(i - lo) < static_cast<unsigned>(mine);
+                if (!here && !(losses && i >= 0)) continue;
+                const float lp = x[k] - row.base, p = expf(lp), z = L::word(word[k], i);
                 if (losses && p != 0.f) part += p * (lp - ((z - whole.m) * a.inv_tau - ln_s));
                 if constexpr (GRAD) {
-                    if (!mine) continue;
+                    if (!here || !in_range(1604, i, 1, a.V)) continue;
                     float all = p;
                     if (row.flags & kTwice) {
                         all = 0.f;
 #pragma unroll 1
-                        for (int i = 0; i < a.K; ++i)
-                            if (idk[i] == idk[k]) all += expf(x[i] - row.base);
+                        for (int l = 0; l < a.K; ++l)
+                            if (idk[l] == i) all += expf(x[l] - row.base);
                     }
                     const float q = exp2_fast((z - reference(whole.m)) * c) * inv_s;
-                    later[k] = row.w * ((row.mass + p_rest) * q - all);
+                    a.dz[b * a.ld + i] = L::from(row.w * ((row.mass + p_rest) * q - all));
                 }
             }
             if (losses) {
@@ -398,29 +397,31 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             __syncwarp();
         };
         read_ahead(first);
-        prepare(first, 0);
+        Row row = prepare(first, 0), last = {};
+        row.flags |= mark(0, 0, 0);
         if (first + step < a.B) read_ahead(first + step);
-        __syncthreads();  // the first row's marks are there
-        int turn = 0, place = 0, before = 2;  // places in threes: of this row, of the one before
-        Row last = {};
+        int turn = 0, unit = 0;
         for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
-            const uint32_t *word = word3 + place * a.K;
-            const int *idk = id3 + place * a.K;
-            const Row row = {flags, base, mass, w};
+            for (int q = 1; q < Q; ++q, unit ^= 1) {
+                block_sync(kSegment, threads + 32);
+                row.flags |= mark(turn, q, unit ^ 1);
+            }
+            block_sync(kSegment, threads + 32);
+            unit ^= 1;
+            const uint32_t *word = word2 + turn * a.K;
+            const int *idk = id2 + turn * a.K;
             ptx::cp_async_wait_all();
             __syncwarp();
             // the kept entries, each id once
             Peak kept = {-INFINITY, 0.f};
 #pragma unroll 1
-            for (int k = lane; k < a.K; k += 32) {
-                const int at = idk[k] - lo;
-                if (idk[k] >= 0 && at >= 0 && at < count) kept.m = fmaxf(kept.m, L::word(word[k], idk[k]));
-            }
+            for (int k = lane; k < a.K; k += 32)
+                if (idk[k] >= 0 && static_cast<unsigned>(idk[k] - lo) < static_cast<unsigned>(mine))
+                    kept.m = fmaxf(kept.m, L::word(word[k], idk[k]));
             kept.m = warp_max(kept.m);
 #pragma unroll 1
             for (int k = lane; k < a.K; k += 32) {
-                const int at = idk[k] - lo;
-                if (idk[k] < 0 || at < 0 || at >= count) continue;
+                if (idk[k] < 0 || static_cast<unsigned>(idk[k] - lo) >= static_cast<unsigned>(mine)) continue;
                 bool once = true;
                 if (row.flags & kTwice)
 #pragma unroll 1
@@ -428,8 +429,6 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
                 if (once) kept.s += exp2_fast((L::word(word[k], idk[k]) - reference(kept.m)) * c);
             }
             kept.s = warp_sum(kept.s);
-            const int next = place == 2 ? 0 : place + 1;
-            if (b + step < a.B) prepare(b + step, next);
             if (lane == 0) {
                 sh.entry[turn] = make_float4(kept.m, kept.s, row.mass, row.w);
                 sh.flags[turn] = row.flags;
@@ -437,34 +436,25 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             __syncwarp();
             block_arrive_turn(kSummed, turn, threads + 64);
             pass(b);
-            if (b + 2 * step < a.B) read_ahead(b + 2 * step);
-            // what is left of the row before, while this one is summed up and joined
             if (b != first) {
                 block_sync_turn(kJoined, turn ^ 1, 64);
-                // everyone's stores of the row before that precede the row's sums
-                if constexpr (GRAD)
-                    if (b - step != first) write_later(b - 2 * step);
-                finish(b - step, before, last, sh.whole[turn ^ 1]);
+                finish(b - step, turn ^ 1, last, sh.whole[turn ^ 1]);
             }
             last = row;
-            before = place;
-            place = next;
+            if (b + step < a.B) {  // in the place of the row before
+                row = prepare(b + step, turn ^ 1);
+                row.flags |= mark(turn ^ 1, 0, unit);
+                if (b + 2 * step < a.B) read_ahead(b + 2 * step);
+            }
         }
-        if (S > 1) cluster_wait();
-        const int64_t end = first + (a.B - 1 - first) / step * step;
+        block_sync(kSegment, threads + 32);  // the last row is written
         block_sync_turn(kJoined, turn ^ 1, 64);
-        if constexpr (GRAD)
-            if (end != first) write_later(end - step);
-        finish(end, before, last, sh.whole[turn ^ 1]);
-        if constexpr (GRAD) {
-            block_sync(kWritten, threads + 32);
-            write_later(end);
-        }
+        finish(first + (a.B - 1 - first) / step * step, turn ^ 1, last, sh.whole[turn ^ 1]);
+        if (S > 1) cluster_wait();
         return;
     }
 
     if (warp > warps) {  // ---- joining
-        __syncthreads();
         int turn = 0;
         for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
             block_sync_turn(kSummed, turn, threads + 64);
@@ -517,22 +507,16 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
     // ---- the row
     const uint64_t cc = f2_pack(c, c);
     const int at0 = warp * kWarpPieces + lane;  // this thread's first piece; the next ones 32 on
-    const int left = pieces - at0, full = count / VEC - at0;
-    // what lies past the segment's end in its last piece counts as kept, too
-    uint2 past = make_uint2(0, 0);
-    if (left > 0 && left != full && (left - 1) % 32 == 0 && left <= kWarpPieces) {
-        constexpr int per = 32 / VEC;
-        const int j = left / 32;
-        const uint32_t m = ((1u << VEC) - (1u << (count % VEC))) << (j % per * VEC);
-        (j < per ? past.x : past.y) = m;
-    }
-    const bool tail = (past.x | past.y) != 0;
     uint4 *const mine = dyn + at0;
-    const auto fetch = [&](int64_t b) {
-        const T *row = a.z + b * a.ld + lo + at0 * VEC;
+    // Segment q: how many values it has, how many pieces are left from at0 on, how many of
+    // those are whole.
+    const auto count_of = [&](int q) { return max(min(a.V - lo - q * seg, seg), 0); };
+    const auto fetch = [&](int64_t b, int q) {
+        const T *row = a.z + b * a.ld + lo + q * seg + at0 * VEC;
+        const int left = (count_of(q) + VEC - 1) / VEC - at0;
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j)
-            if (j * 32 < left && in_range(1602, lo + (at0 + j * 32) * VEC, VEC, a.ld))
+            if (j * 32 < left && in_range(1602, lo + q * seg + (at0 + j * 32) * VEC, VEC, a.ld))
                 cp_async16(mine + j * 32, row + j * 32 * VEC);
         ptx::cp_async_commit();
     };
@@ -543,28 +527,44 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             reinterpret_cast<T *>(mine + v / VEC * 32)[v % VEC] = L::lowest();
         }
     };
-#pragma unroll
-    for (int j = 0; j < ITEMS; ++j)  // pieces past the end stay -inf
-        if (j * 32 >= left)
-            mine[j * 32] = make_uint4(L::kLowest, L::kLowest, L::kLowest, L::kLowest);
-    fetch(first);
-    __syncthreads();
-    int turn = 0, place = 0;
-    for (int64_t b = first; b < a.B; b += step, turn ^= 1, place = place == 2 ? 0 : place + 1) {
-        const uint2 marks = sh.marks[place][tid];
-        if ((marks.x | marks.y) != 0) sh.marks[place][tid] = make_uint2(0, 0);
-        ptx::cp_async_wait_all();
-        strike(marks.x | past.x, 0);
-        strike(marks.y | past.y, 32);
+    if (in_range(1601, first, 1, a.B)) fetch(first, 0);
+    int turn = 0, unit = 0;
+    for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
+        Peak rest = {-INFINITY, 0.f};
         uint4 v[ITEMS];
+        int count = 0, left = 0;
+        bool tail = false;  // whether the row's last piece, one that is not whole, is this thread's
+        for (int q = 0; q < Q; ++q, unit ^= 1) {
+            count = count_of(q);
+            left = (count + VEC - 1) / VEC - at0;
+            block_sync(kSegment, threads + 32);
+            uint2 marks = sh.marks[unit][tid];
+            if ((marks.x | marks.y) != 0) sh.marks[unit][tid] = make_uint2(0, 0);
+            // what lies past the end in the last piece is struck out, too
+            tail = count % VEC != 0 && left > 0 && left <= kWarpPieces && left % 32 == 1;
+            if (tail) {
+                constexpr int per = 32 / VEC;
+                const int j = left / 32;
+                (j < per ? marks.x : marks.y) |= ((1u << VEC) - (1u << (count % VEC))) << (j % per * VEC);
+            }
+            ptx::cp_async_wait_all();
+            if (left <= (ITEMS - 1) * 32) {
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) v[j] = mine[j * 32];
-        if (b + step < a.B) fetch(b + step);
+                for (int j = 0; j < ITEMS; ++j)  // pieces past the end
+                    if (j * 32 >= left) mine[j * 32] = make_uint4(L::kLowest, L::kLowest, L::kLowest, L::kLowest);
+            }
+            strike(marks.x, 0);
+            strike(marks.y, 32);
+#pragma unroll
+            for (int j = 0; j < ITEMS; ++j) v[j] = mine[j * 32];
+            if (q + 1 < Q)
+                fetch(b, q + 1);
+            else if (b + step < a.B)
+                fetch(b + step, 0);
 
-        Peak rest;
-        rest.m = L::template largest<ITEMS>(v);
-        {
-            const float r = reference(rest.m);
+            Peak p;
+            p.m = L::template largest<ITEMS>(v);
+            const float r = reference(p.m);
             const uint64_t minus_r = f2_pack(-r, -r);
             uint64_t s = 0;
 #pragma unroll
@@ -580,15 +580,16 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             }
             float l, h;
             f2_unpack(s, l, h);
-            rest.s = l + h;
+            p.s = l + h;
+            if constexpr (GRAD)
+                rest = p;
+            else
+                rest = merge(rest, p, c);
         }
         rest = warp_merge(rest, c);
         if (lane == 0) sh.rest[turn][warp] = make_float2(rest.m, rest.s);
         __syncwarp();
-        if constexpr (GRAD)
-            block_arrive_turn(kSummed, turn, threads + 64);
-        else
-            block_sync_turn(kSummed, turn, threads + 64);  // the next row's marks are there
+        block_arrive_turn(kSummed, turn, threads + 64);
         pass(b);
         if constexpr (GRAD) {
             block_sync(kAnswered, threads + 32);
@@ -600,6 +601,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
                 continue;
             }
             out += at0 * VEC;
+            const int full = count / VEC - at0;
 #pragma unroll
             for (int j = 0; j < ITEMS; ++j) {
                 uint64_t f[VEC / 2];
@@ -622,29 +624,37 @@ distill_kernel(const DistillArgs<T> a, int seg, int S)
             }
         }
     }
+    block_sync(kSegment, threads + 32);
     if (S > 1) cluster_wait();
-    if constexpr (GRAD) block_arrive(kWritten, threads + 32);
 }
 
-// Blocks a row (a power of two up to 8), warps a block and pieces a thread.
+// Blocks a row (a power of two up to 8), segments a block, warps that hold a segment and
+// pieces a thread.
 struct Plan {
-    int S, seg, warps, items;
+    int S, Q, seg, warps, items;
 };
-constexpr int kPieces = 4096;    // a block's most, but where 8 blocks do not reach
+constexpr int kPieces = 4096;    // a segment's most, but where a gradient needs all and 8 blocks do not reach
 constexpr int kMinPieces = 256;  // rows are split further only down to this
 
 template <typename T>
-Plan plan_of(int64_t B, int V, int num_sms)
+Plan plan_of(int64_t B, int V, bool grad, int num_sms)
 {
     constexpr int VEC = Logit<T>::kVec;
-    const auto seg_of = [&](int s) { return ((V + s - 1) / s + 7) / 8 * 8; };
+    const auto seg_of = [&](int parts) { return ((V + parts - 1) / parts + 7) / 8 * 8; };
+    const auto segments = [&](int s) { return (seg_of(s) / VEC + kPieces - 1) / kPieces; };
     Plan p;
     p.S = 1;
-    while (p.S < kMaxCluster && seg_of(p.S) / VEC > kPieces) p.S *= 2;
-    // few rows: more blocks, and a piece a thread where that is enough
-    while (p.S < kMaxCluster && B * p.S * 2 <= num_sms && seg_of(p.S) / VEC > kMinPieces) p.S *= 2;
-    p.seg = seg_of(p.S);
-    const int pieces = p.seg / VEC, each = B * p.S <= num_sms ? 1 : kMaxItems;
+    if (grad)
+        while (p.S < kMaxCluster && segments(p.S) > 1) p.S *= 2;
+    // More blocks a row where that takes a fifth off the pieces that one after another go
+    // through a block (two an SM): where rows are few, or leave many places empty at the end.
+    const auto rounds = [&](int s) { return (B * s + 2 * num_sms - 1) / (2 * num_sms) * (seg_of(s) / VEC); };
+    for (int s = p.S * 2; s <= kMaxCluster && seg_of(s) / VEC >= kMinPieces; s *= 2)
+        if (rounds(s) * 5 <= rounds(p.S) * 4) p.S = s;
+    p.Q = grad ? 1 : segments(p.S);
+    p.seg = seg_of(p.S * p.Q);
+    // a piece a thread where a block has one segment of one row, for the shortest way through
+    const int pieces = p.seg / VEC, each = B * p.S <= num_sms && p.Q == 1 ? 1 : kMaxItems;
     const int most = (pieces + 32 * each - 1) / (32 * each);
     const int warps = most < kMaxWarps ? most : kMaxWarps;
     p.items = 1;
@@ -659,7 +669,7 @@ cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, int num_sms, cu
     // Clusters that are resident at once: by device, log2 of the cluster, warps, and whether the
     // entries take much shared memory
     static std::atomic<int> resident[64][4][kMaxWarps + 1][2];
-    constexpr int most = kMaxThreads * ITEMS * 16 + kDistillMaxK * 44;
+    constexpr int most = kMaxThreads * ITEMS * 16 + kDistillMaxK * 24;
     constexpr int few = 128;
     int dev = 0, log_s = 0;
     const int many = a.K > few;
@@ -669,7 +679,7 @@ cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, int num_sms, cu
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(p.warps * 32 + 64);
     const size_t pieces = static_cast<size_t>(p.warps) * 32 * ITEMS * 16;
-    cfg.dynamicSmemBytes = pieces + (many ? kDistillMaxK : few) * 44;
+    cfg.dynamicSmemBytes = pieces + (many ? kDistillMaxK : few) * 24;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -693,22 +703,22 @@ cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, int num_sms, cu
     }
     const int64_t rows = a.B < clusters ? a.B : clusters;
     cfg.gridDim = dim3(static_cast<unsigned>(rows * p.S));
-    cfg.dynamicSmemBytes = pieces + static_cast<size_t>(a.K) * 44;
+    cfg.dynamicSmemBytes = pieces + static_cast<size_t>(a.K) * 24;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, distill_kernel<T, GRAD, ITEMS>, a, p.seg, p.S);
+    return cudaLaunchKernelEx(&cfg, distill_kernel<T, GRAD, ITEMS>, a, p.seg, p.S, p.Q);
 }
 
 template <typename T, bool GRAD>
 cudaError_t launch_as(const DistillArgs<T> &a, int num_sms, cudaStream_t stream)
 {
-    const Plan p = plan_of<T>(a.B, a.V, num_sms);
+    const Plan p = plan_of<T>(a.B, a.V, GRAD, num_sms);
     switch (p.items) {
     case 1: return launch_items<T, GRAD, 1>(a, p, num_sms, stream);
     case 2: return launch_items<T, GRAD, 2>(a, p, num_sms, stream);
     case 4: return launch_items<T, GRAD, 4>(a, p, num_sms, stream);
     case 8: return launch_items<T, GRAD, 8>(a, p, num_sms, stream);
     default:
-        if constexpr (Logit<T>::kVec * 16 <= kMaxBits) return launch_items<T, GRAD, 16>(a, p, num_sms, stream);
+        if constexpr (GRAD && Logit<T>::kVec * 16 <= kMaxBits) return launch_items<T, GRAD, 16>(a, p, num_sms, stream);
         return cudaErrorInvalidValue;
     }
 }

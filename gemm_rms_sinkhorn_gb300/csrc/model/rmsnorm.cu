@@ -250,7 +250,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rmsnorm_kernel(const NormArgs 
 // The blocks walk the tokens; a thread meets the same channels in each of them, so it
 // holds their share of dgain in fp32 registers.  A block's sums go to its row of the
 // workspace, and a second launch adds the rows in order.
-constexpr int kBackwardBlocks = 2;  // blocks an SM
+// Blocks an SM: as many as are resident at 64 registers a thread, or 128 with 4 chunks.  (Four
+// of the narrow ones are: 16384 tokens of 256 take 10.7 us then, 9.5 with two, for each block
+// ends with its row of the workspace.)
+int blocks_per_sm(int items) { return items <= 2 ? 2 : 1; }
 
 template <int ITEMS, bool SKIP>
 __global__ void __launch_bounds__(kMaxThreads, ITEMS <= 2 ? 2 : 1)
@@ -386,7 +389,9 @@ rmsnorm_backward_kernel(const NormBackwardArgs a, int G, int T, float *__restric
     }
 }
 
-// dgain (+)= the rows of `parts`, by slices of rows and then slices in order.
+// dgain (+)= the rows of `parts`, by slices of rows and then slices in order.  304 rows of
+// 7168 are 9 MB, in L2: what counts is how many loads are in flight.  128 rows take 3.5 us
+// (4.5 with 8 columns a block and 32 slices, 5.0 with 32 columns and 32 slices).
 constexpr int kJoinCols = 32, kJoinSlices = 16;
 __global__ void __launch_bounds__(kJoinCols * kJoinSlices)
 rmsnorm_join_kernel(const float *parts, int rows, int64_t C, int accumulate, float *dgain)
@@ -398,7 +403,7 @@ rmsnorm_join_kernel(const float *parts, int rows, int64_t C, int accumulate, flo
     ptx::pdl_trigger();
     float s = 0.f;
     if (c < C)
-        for (int r0 = slice; r0 < rows; r0 += 8 * kJoinSlices) {  // eight loads in flight
+        for (int r0 = slice; r0 < rows; r0 += 8 * kJoinSlices) {
             float v[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -410,7 +415,7 @@ rmsnorm_join_kernel(const float *parts, int rows, int64_t C, int accumulate, flo
         }
     part[slice][col] = s;
     __syncthreads();
-    if (slice != 0 || c >= C) return;
+    if (slice != 0 || c >= C || !in_range(1521, c, 1, C)) return;
 #pragma unroll
     for (int k = 1; k < kJoinSlices; ++k) s += part[k][col];
     dgain[c] = accumulate ? ptx::ld_dep(dgain + c) + s : s;
@@ -419,7 +424,7 @@ rmsnorm_join_kernel(const float *parts, int rows, int64_t C, int accumulate, flo
 int backward_blocks(int64_t B, int64_t C, int num_sms)
 {
     const Layout l = layout_of(C);
-    const int64_t all = (B + l.tokens - 1) / l.tokens, most = static_cast<int64_t>(kBackwardBlocks) * num_sms;
+    const int64_t all = (B + l.tokens - 1) / l.tokens, most = static_cast<int64_t>(blocks_per_sm(l.items)) * num_sms;
     return static_cast<int>(all < most ? all : most);
 }
 

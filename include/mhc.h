@@ -535,7 +535,8 @@ int mhc_rmsnorm_backward(const mhc_bf16 *dZ, const mhc_bf16 *H, const float *gai
  * The backward works from z alone, in one pass: a training step that knows dloss [B] fp32
  * (1/rows, times tau² where that is wanted) needs no forward call.  Its loss may be NULL.
  * dz [B][ld] has z's type and may be exactly z; columns from V on are neither read for
- * their value nor written.  Results are bitwise reproducible.
+ * their value nor written.  Results are bitwise reproducible; the losses of the two calls
+ * may differ in their last bits.
  *
  * Rules as for the calls above, and: V >= 1, K >= 1, ld >= V, inv_tau finite and > 0
  * (MHC_ERR_INVALID); B < 2^31, V <= 2^18, K <= 1024, ld % 8 == 0 and ld <= 2^24
