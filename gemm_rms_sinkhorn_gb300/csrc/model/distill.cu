@@ -17,13 +17,14 @@
 // nothing else has to wait for them.  Without a gradient nothing has to be held, and a block
 // takes several segments of a row one after another; clusters are for few rows then.
 //
-// Two more warps keep all else away from those.  One takes the K entries, a row ahead: it
-// works out the teacher's sums, fetches the student's logits there and marks the kept ids of
-// the next segment in a bit map, a word a thread; the thread overwrites its marked values
-// with -inf before it reads them.  The other joins a row's sums, over warps and over the
-// cluster through distributed shared memory, and answers with the factor of the gradient.
-// What is due at the kept ids is written a row later, behind what the row's threads wrote
-// there.  dz may be z: a row is written after all of the cluster has summed it up.
+// Two more warps keep all else away from those.  One takes the K entries, one or two rows
+// ahead: it works out the teacher's sums, fetches the student's logits there and marks the
+// kept ids of a segment in a bit map, a word a thread; the thread overwrites its marked
+// values with -inf before it reads them.  The other joins a row's sums, over warps and over
+// the cluster through distributed shared memory, answers with the factor of the gradient,
+// and then has the row before to finish: its loss, and what is due at the kept ids, behind
+// what the row's threads wrote there.  dz may be z: a row is written after all of the cluster
+// has summed it up.
 //
 // Exponentials are exp2((z - m)·c), c = inv_tau·log2 e, m the largest z seen, two values at
 // a time.  As one fused multiply-add z·c - m·c they would be off by what m·c rounds away:
@@ -97,6 +98,8 @@ __device__ __forceinline__ void st_cluster(float2 *p, uint32_t rank, float2 v)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
 }
+// All copies of this thread have landed but those of its last group.
+__device__ __forceinline__ void cp_async_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 __device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
@@ -216,25 +219,32 @@ __device__ __noinline__ void store_some(T *p, uint4 v, int n)
         }
 }
 
+constexpr int kPlaces = 4;  // rows whose entries are held: one to finish, one summed up, two ahead
+struct Info {               // of a row's entries
+    float kept_m, kept_s;   // the student's peak there, of this block's segments
+    float base, unit;       // log p = x - base, p = e·unit
+    float mass, w;          // Σ p, dloss·inv_tau
+    int flags;
+};
 struct Shared {
     float2 rests[2][kMaxCluster][kMaxWarps], kepts[2][kMaxCluster];  // the cluster's peaks
-    float4 entry[2];              // of the row's entries: kept.m, kept.s, Σ p, dloss·inv_tau
-    float4 whole[2];              // the row's: rest.m, rest.s, and of both together
     float4 out;                   // the gradient: what to multiply by, the reference, whether there is one
     float2 rest[2][kMaxWarps];    // peaks by warp
-    uint2 marks[2][kMaxThreads];  // bit j·VEC + e: value e of the thread's piece j is kept
-    int flags[2];
+    uint2 marks[3][kMaxThreads];  // bit j·VEC + e: value e of the thread's piece j is kept
+    Info info[kPlaces];
 };
 constexpr int kSome = 1, kTwice = 2;  // entries are present; an id comes more than once here
 // The block's barriers:
-//   kSegment   a segment's marks are there, and the one before is done with: the row's
-//              threads and the entries' warp meet
-//   kSummed    a row's sums and entries are there: the joining warp waits
+//   kSegment   (without a gradient) a segment's marks are there, and the one before is done
+//              with: the row's threads and the entries' warp meet
+//   kSummed    a row's sums and entries, and the next row's marks, are there: the joining warp
+//              waits
 //   kAnswered  the gradient's factor is there: the row's threads wait
-//   kJoined    the row's whole sums are there: the entries' warp waits
+//   kJoined    the row is joined and the one before finished: the entries' warp waits
+//   kWritten   the last row's gradient is written: the joining warp waits
 // kSummed and kJoined are pairs that rows take in turn: who only arrives there may come for
 // the next row before all have come for this one, but not for the one after that.
-constexpr int kSegment = 1, kSummed = 2, kJoined = 4, kAnswered = 6;
+constexpr int kSegment = 1, kSummed = 2, kJoined = 4, kAnswered = 6, kWritten = 7;
 
 // S blocks a row, Q segments of `seg` values a block.
 template <typename T, bool GRAD, int ITEMS>
@@ -254,8 +264,13 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = S > 1 ? cluster_rank() : 0;
     const int lo = static_cast<int>(rank) * Q * seg;
+    const unsigned mine_values = max(min(a.V - lo, Q * seg), 0);  // of the row
     const float c = a.inv_tau * kLog2e;
     const int64_t step = gridDim.x / S, first = blockIdx.x / S;
+    // [kPlaces][K] each: x = t·inv_tau, e^(x - largest x), the word that z lies in, id (-1: absent)
+    float *const xs = reinterpret_cast<float *>(dyn + warps * kWarpPieces), *const es = xs + kPlaces * a.K;
+    uint32_t *const words = reinterpret_cast<uint32_t *>(es + kPlaces * a.K);
+    int *const ids = reinterpret_cast<int *>(words + kPlaces * a.K);
     // A row's barrier of the cluster, for the warps that do not wait for the others' sums:
     // they take part a row behind.
     const auto pass = [&](int64_t b) {
@@ -265,7 +280,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         }
     };
 
-    for (int i = tid; i < 2 * kMaxThreads; i += blockDim.x) (&sh.marks[0][0])[i] = make_uint2(0, 0);
+    for (int i = tid; i < 3 * kMaxThreads; i += blockDim.x) (&sh.marks[0][0])[i] = make_uint2(0, 0);
     // No early trigger: blocks of the next kernel that wait in the places of these cost more
     // (4096 rows of 131072, back to back: 592 us, 473 without) than their start would save.
     ptx::pdl_wait();
@@ -276,13 +291,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
     __syncthreads();
 
     if (warp == warps) {  // ---- the entries
-        // [2][K] by row in turn: x = t·inv_tau, the word that z lies in, id (-1: absent)
-        float *const x2 = reinterpret_cast<float *>(dyn + warps * kWarpPieces);
-        uint32_t *const word2 = reinterpret_cast<uint32_t *>(x2 + 2 * a.K);
-        int *const id2 = reinterpret_cast<int *>(word2 + 2 * a.K);
-        const int mine = max(min(a.V - lo, Q * seg), 0);  // of the row's values
-
-        constexpr int kAhead = 4;  // entries a lane that are read another row ahead
+        constexpr int kAhead = 4;  // entries a lane taken at once, the first ones read another row ahead
         int64_t id[kAhead];
         float t[kAhead], lse = 0.f, dloss = 0.f;
         const auto read = [&](int64_t b, int k0) {
@@ -294,21 +303,30 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             }
         };
         const auto read_ahead = [&](int64_t b) {
+            if (b >= a.B) return;
             read(b, lane);
             if (a.t_lse != nullptr) lse = ptx::ld_dep(a.t_lse + b);
             if constexpr (GRAD) dloss = ptx::ld_dep(a.dloss + b);
         };
-        struct Row {
-            int flags;
-            float base, mass, w;  // what x is taken relative to for log p, Σ p, dloss·inv_tau
+        // Marks value `at` of a segment; whether it has been marked before.
+        const auto mark = [&](uint2 *marks, int at) {
+            const int p = at / VEC, bit = p / 32 % ITEMS * VEC + at % VEC;
+            uint32_t *w = &marks[p / kWarpPieces * 32 + p % 32].x + (bit >> 5);
+            return (atomicOr(w, 1u << (bit & 31)) >> (bit & 31) & 1u) != 0;
         };
-        const auto prepare = [&](int64_t b, int turn) -> Row {  // after read_ahead(b)
-            float *x = x2 + turn * a.K;
-            uint32_t *word = word2 + turn * a.K;
-            int *idk = id2 + turn * a.K;
+        // Row b into its place, its first segment's kept ids into `marks`; after read_ahead(b).
+        const auto prepare = [&](int64_t b, int place, uint2 *marks) {
+            if (b >= a.B) {
+                ptx::cp_async_commit();
+                return;
+            }
+            float *x = xs + place * a.K, *e = es + place * a.K;
+            uint32_t *word = words + place * a.K;
+            int *idk = ids + place * a.K;
             const T *row = a.z + b * a.ld;
-            Row r = {0, 0.f, 1.f, dloss * a.inv_tau};
+            const int count = max(min(a.V - lo, seg), 0);
             float m = -INFINITY;
+            bool some = false, twice = false;
 #pragma unroll 1
             for (int k0 = lane; k0 < a.K; k0 += 32 * kAhead) {
                 if (k0 != lane) read(b, k0);
@@ -321,69 +339,147 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                     idk[k] = i;
                     x[k] = t[u] * a.inv_tau;
                     if (!here) continue;
-                    r.flags = kSome;
+                    some = true;
                     m = fmaxf(m, x[k]);
-                    if ((rank == 0 || static_cast<unsigned>(i - lo) < static_cast<unsigned>(mine)) &&
-                        in_range(1605, i, 1, a.V))
+                    if ((rank == 0 || static_cast<unsigned>(i - lo) < mine_values) && in_range(1605, i, 1, a.V))
                         ptx::cp_async4(word + k, row + (i & -L::kWord));
+                    if (i >= lo && i - lo < count) twice |= mark(marks, i - lo);
                 }
             }
             ptx::cp_async_commit();
-            r.flags = __any_sync(0xffffffffu, r.flags) ? kSome : 0;
-            __syncwarp();
+            some = __any_sync(0xffffffffu, some);
+            twice = __any_sync(0xffffffffu, twice);
             m = a.t_lse != nullptr ? lse : warp_max(m);
             float s = 0.f;
-#pragma unroll 1
-            for (int k = lane; k < a.K; k += 32)
-                if (idk[k] >= 0) s += expf(x[k] - m);
-            s = warp_sum(s);
-            r.base = a.t_lse != nullptr ? m : m + logf(s);
-            if (a.t_lse != nullptr) r.mass = s;
-            return r;
-        };
-        // Marks the kept ids of segment q; kTwice where one has been marked before.
-        const auto mark = [&](int turn, int q, int unit) {
-            const int *idk = id2 + turn * a.K;
-            const int from = lo + q * seg, count = max(min(a.V - from, seg), 0);
-            bool twice = false;
-#pragma unroll 1
+#pragma unroll 4
             for (int k = lane; k < a.K; k += 32) {
-                const int at = idk[k] - from;
-                if (idk[k] < 0 || at < 0 || at >= count) continue;
-                const int p = at / VEC, bit = p / 32 % ITEMS * VEC + at % VEC;
-                uint32_t *w = &sh.marks[unit][p / kWarpPieces * 32 + p % 32].x + (bit >> 5);
-                twice |= (atomicOr(w, 1u << (bit & 31)) >> (bit & 31) & 1u) != 0;
+                const float v = idk[k] >= 0 ? expf(x[k] - m) : 0.f;
+                e[k] = v;
+                s += v;
             }
-            return __any_sync(0xffffffffu, twice) ? kTwice : 0;
+            s = warp_sum(s);
+            if (lane == 0) {
+                Info &r = sh.info[place];
+                r.base = a.t_lse != nullptr ? m : m + logf(s);
+                r.unit = a.t_lse != nullptr ? 1.f : 1.f / s;
+                r.mass = a.t_lse != nullptr ? s : 1.f;
+                r.w = dloss * a.inv_tau;
+                r.flags = (some ? kSome : 0) | (twice ? kTwice : 0);
+            }
+            __syncwarp();
         };
-        // What a joined row leaves to do: its loss, and the gradient at the kept ids.
-        const auto finish = [&](int64_t b, int turn, const Row &row, const float4 &sums) {
-            const float *x = x2 + turn * a.K;
-            const uint32_t *word = word2 + turn * a.K;
-            const int *idk = id2 + turn * a.K;
-            const Peak rest = {sums.x, sums.y}, whole = {sums.z, sums.w};
-            const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - row.mass, 0.f) : 0.f;
-            const bool losses = rank == 0 && a.loss != nullptr;
-            const float ln_s = logf(whole.s), inv_s = 1.f / whole.s;
-            float part = 0.f;
+        // The peak at the kept ids of this block, each once.
+        const auto peak = [&](int place) {
+            const uint32_t *word = words + place * a.K;
+            const int *idk = ids + place * a.K;
+            const int flags = sh.info[place].flags;
+            Peak kept = {-INFINITY, 0.f};
+#pragma unroll 4
+            for (int k = lane; k < a.K; k += 32)
+                if (idk[k] >= 0 && static_cast<unsigned>(idk[k] - lo) < mine_values)
+                    kept.m = fmaxf(kept.m, L::word(word[k], idk[k]));
+            kept.m = warp_max(kept.m);
+            const float r = reference(kept.m);
+            if (flags & kTwice) {
 #pragma unroll 1
+                for (int k = lane; k < a.K; k += 32) {
+                    if (idk[k] < 0 || static_cast<unsigned>(idk[k] - lo) >= mine_values) continue;
+                    bool once = true;
+#pragma unroll 1
+                    for (int i = 0; i < k; ++i) once = once && idk[i] != idk[k];
+                    if (once) kept.s += exp2_fast((L::word(word[k], idk[k]) - r) * c);
+                }
+            } else {
+#pragma unroll 4
+                for (int k = lane; k < a.K; k += 32)
+                    if (idk[k] >= 0 && static_cast<unsigned>(idk[k] - lo) < mine_values)
+                        kept.s += exp2_fast((L::word(word[k], idk[k]) - r) * c);
+            }
+            kept.s = warp_sum(kept.s);
+            if (lane == 0) {
+                sh.info[place].kept_m = kept.m;
+                sh.info[place].kept_s = kept.s;
+            }
+            __syncwarp();
+        };
+        constexpr int kLead = GRAD ? 2 : 1;  // rows prepared ahead
+        read_ahead(first);
+        prepare(first, 0, sh.marks[0]);
+        read_ahead(first + step);
+        if constexpr (GRAD) {
+            prepare(first + step, 1, sh.marks[1]);
+            read_ahead(first + 2 * step);
+        }
+        __syncthreads();  // the first marks are there
+        int turn = 0, place = 0, third = kLead;  // third: of the marks, where the row after the lead has them
+        int unit = 0;
+        for (int64_t b = first; b < a.B; b += step, turn ^= 1, place = (place + 1) % kPlaces) {
+            if constexpr (!GRAD) {
+                const int *idk = ids + place * a.K;
+                for (int q = 1; q <= Q; ++q) {
+                    block_sync(kSegment, threads + 32);
+                    unit ^= 1;
+                    if (q == Q) break;
+                    const int from = lo + q * seg, count = max(min(a.V - from, seg), 0);
+                    bool twice = false;
+#pragma unroll 4
+                    for (int k = lane; k < a.K; k += 32)
+                        if (idk[k] >= from && idk[k] - from < count) twice |= mark(sh.marks[unit], idk[k] - from);
+                    if (__any_sync(0xffffffffu, twice) && lane == 0) sh.info[place].flags |= kTwice;
+                    __syncwarp();
+                }
+            }
+            if constexpr (GRAD)
+                cp_async_wait_but_one();
+            else
+                ptx::cp_async_wait_all();
+            __syncwarp();
+            peak(place);
+            block_arrive_turn(kSummed, turn, threads + 64);
+            pass(b);
+            // A row on: its place is that of a row that has been finished, and its marks that of
+            // one that has been summed up, once the row before this one is joined.
+            if (b != first) block_sync_turn(kJoined, turn ^ 1, 64);
+            prepare(b + kLead * step, (place + kLead) % kPlaces, sh.marks[GRAD ? third : unit]);
+            read_ahead(b + (kLead + 1) * step);
+            third = third == 2 ? 0 : third + 1;
+        }
+        if constexpr (!GRAD) block_sync(kSegment, threads + 32);
+        block_sync_turn(kJoined, turn ^ 1, 64);
+        if (S > 1) cluster_wait();
+        return;
+    }
+
+    if (warp > warps) {  // ---- joining
+        // What a joined row leaves to do: its loss, and the gradient at the kept ids.
+        const auto finish = [&](int64_t b, int place, Peak rest, Peak whole) {
+            const float *x = xs + place * a.K, *e = es + place * a.K;
+            const uint32_t *word = words + place * a.K;
+            const int *idk = ids + place * a.K;
+            const Info &r = sh.info[place];
+            const float base = r.base, unit = r.unit, mass = r.mass, w = r.w;
+            const int flags = r.flags;
+            const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - mass, 0.f) : 0.f;
+            const bool losses = rank == 0 && a.loss != nullptr;
+            const float ln_s = logf(whole.s), factor = w * (mass + p_rest) / whole.s, ref = reference(whole.m);
+            float part = 0.f;
+#pragma unroll 2
             for (int k = lane; k < a.K; k += 32) {
                 const int i = idk[k];
-                const bool here = i >= 0 && static_cast<unsigned>(i - lo) < static_cast<unsigned>(mine);
+                const bool here = i >= 0 && static_cast<unsigned>(i - lo) < mine_values;
                 if (!here && !(losses && i >= 0)) continue;
-                const float lp = x[k] - row.base, p = expf(lp), z = L::word(word[k], i);
-                if (losses && p != 0.f) part += p * (lp - ((z - whole.m) * a.inv_tau - ln_s));
+                const float p = e[k] * unit, z = L::word(word[k], i);
+                if (losses && p != 0.f) part += p * (x[k] - base - ((z - whole.m) * a.inv_tau - ln_s));
                 if constexpr (GRAD) {
                     if (!here || !in_range(1604, i, 1, a.V)) continue;
                     float all = p;
-                    if (row.flags & kTwice) {
+                    if (flags & kTwice) {
                         all = 0.f;
 #pragma unroll 1
                         for (int l = 0; l < a.K; ++l)
-                            if (idk[l] == i) all += expf(x[l] - row.base);
+                            if (idk[l] == i) all += e[l] * unit;
                     }
-                    const float q = exp2_fast((z - reference(whole.m)) * c) * inv_s;
-                    a.dz[b * a.ld + i] = L::from(row.w * ((row.mass + p_rest) * q - all));
+                    a.dz[b * a.ld + i] = L::from(fmaf(exp2_fast((z - ref) * c), factor, -(w * all)));
                 }
             }
             if (losses) {
@@ -391,81 +487,23 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 if (lane == 0) {
                     if (p_rest > 0.f)
                         part += p_rest * (logf(p_rest) - ((rest.m - whole.m) * a.inv_tau + logf(rest.s) - ln_s));
-                    a.loss[b] = row.flags & kSome ? part : 0.f;
+                    a.loss[b] = flags & kSome ? part : 0.f;
                 }
             }
             __syncwarp();
         };
-        read_ahead(first);
-        Row row = prepare(first, 0), last = {};
-        row.flags |= mark(0, 0, 0);
-        if (first + step < a.B) read_ahead(first + step);
-        int turn = 0, unit = 0;
-        for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
-            for (int q = 1; q < Q; ++q, unit ^= 1) {
-                block_sync(kSegment, threads + 32);
-                row.flags |= mark(turn, q, unit ^ 1);
-            }
-            block_sync(kSegment, threads + 32);
-            unit ^= 1;
-            const uint32_t *word = word2 + turn * a.K;
-            const int *idk = id2 + turn * a.K;
-            ptx::cp_async_wait_all();
-            __syncwarp();
-            // the kept entries, each id once
-            Peak kept = {-INFINITY, 0.f};
-#pragma unroll 1
-            for (int k = lane; k < a.K; k += 32)
-                if (idk[k] >= 0 && static_cast<unsigned>(idk[k] - lo) < static_cast<unsigned>(mine))
-                    kept.m = fmaxf(kept.m, L::word(word[k], idk[k]));
-            kept.m = warp_max(kept.m);
-#pragma unroll 1
-            for (int k = lane; k < a.K; k += 32) {
-                if (idk[k] < 0 || static_cast<unsigned>(idk[k] - lo) >= static_cast<unsigned>(mine)) continue;
-                bool once = true;
-                if (row.flags & kTwice)
-#pragma unroll 1
-                    for (int i = 0; i < k; ++i) once = once && idk[i] != idk[k];
-                if (once) kept.s += exp2_fast((L::word(word[k], idk[k]) - reference(kept.m)) * c);
-            }
-            kept.s = warp_sum(kept.s);
-            if (lane == 0) {
-                sh.entry[turn] = make_float4(kept.m, kept.s, row.mass, row.w);
-                sh.flags[turn] = row.flags;
-            }
-            __syncwarp();
-            block_arrive_turn(kSummed, turn, threads + 64);
-            pass(b);
-            if (b != first) {
-                block_sync_turn(kJoined, turn ^ 1, 64);
-                finish(b - step, turn ^ 1, last, sh.whole[turn ^ 1]);
-            }
-            last = row;
-            if (b + step < a.B) {  // in the place of the row before
-                row = prepare(b + step, turn ^ 1);
-                row.flags |= mark(turn ^ 1, 0, unit);
-                if (b + 2 * step < a.B) read_ahead(b + 2 * step);
-            }
-        }
-        block_sync(kSegment, threads + 32);  // the last row is written
-        block_sync_turn(kJoined, turn ^ 1, 64);
-        finish(first + (a.B - 1 - first) / step * step, turn ^ 1, last, sh.whole[turn ^ 1]);
-        if (S > 1) cluster_wait();
-        return;
-    }
-
-    if (warp > warps) {  // ---- joining
-        int turn = 0;
-        for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
+        __syncthreads();
+        Peak last_rest = {}, last_whole = {};
+        int turn = 0, place = 0;
+        for (int64_t b = first; b < a.B; b += step, turn ^= 1, place = (place + 1) % kPlaces) {
             block_sync_turn(kSummed, turn, threads + 64);
             Peak rest = {-INFINITY, 0.f};
             if (lane < warps) rest = {sh.rest[turn][lane].x, sh.rest[turn][lane].y};
-            const float4 entry = sh.entry[turn];
-            const int flags = sh.flags[turn];
-            Peak kept = {entry.x, entry.y};
+            const Info &r = sh.info[place];
+            Peak kept = {r.kept_m, r.kept_s};
             if (S > 1) {
                 if (lane < warps)
-                    for (int r = 0; r < S; ++r) st_cluster(&sh.rests[turn][rank][lane], r, make_float2(rest.m, rest.s));
+                    for (int i = 0; i < S; ++i) st_cluster(&sh.rests[turn][rank][lane], i, make_float2(rest.m, rest.s));
                 if (lane < S) st_cluster(&sh.kepts[turn][rank], lane, make_float2(kept.m, kept.s));
                 cluster_arrive_release();
                 cluster_wait();
@@ -474,8 +512,8 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 float2 p[kMaxCluster / 2];
 #pragma unroll
                 for (int i = 0; i < kMaxCluster / 2; ++i) {  // two blocks' warps at once
-                    const int r = 2 * i + lane / kMaxWarps, w = lane % kMaxWarps;
-                    p[i] = r < S && w < warps ? sh.rests[turn][r][w] : make_float2(-INFINITY, 0.f);
+                    const int from = 2 * i + lane / kMaxWarps, w = lane % kMaxWarps;
+                    p[i] = from < S && w < warps ? sh.rests[turn][from][w] : make_float2(-INFINITY, 0.f);
                     rest.m = fmaxf(rest.m, p[i].x);
                 }
 #pragma unroll
@@ -485,22 +523,26 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             }
             rest = warp_merge(rest, c);
             const Peak whole = merge(rest, kept, c);
-            if (lane == 0) {
-                sh.whole[turn] = make_float4(rest.m, rest.s, whole.m, whole.s);
-                if constexpr (GRAD) {
-                    const float mass = entry.z, w = entry.w;
-                    const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - mass, 0.f) : 0.f;
+            if constexpr (GRAD) {
+                if (lane == 0) {
+                    const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - r.mass, 0.f) : 0.f;
                     // q_rest·(M - p_rest/q_rest) = M·q_rest - p_rest, shared out by exp2 over the rest's sum
                     const float q_rest = rest.s == 0.f ? 0.f : rest.s * exp2_fast((rest.m - whole.m) * c) / whole.s;
-                    const float scale = rest.s != 0.f ? w * ((mass + p_rest) * q_rest - p_rest) / rest.s
+                    const float scale = rest.s != 0.f ? r.w * ((r.mass + p_rest) * q_rest - p_rest) / rest.s
                                                       : whole.s != 0.f ? 0.f : NAN;
-                    sh.out = make_float4(scale, reference(rest.m), flags & kSome ? 1.f : 0.f, 0.f);
+                    sh.out = make_float4(scale, reference(rest.m), r.flags & kSome ? 1.f : 0.f, 0.f);
                 }
+                __syncwarp();
+                block_arrive(kAnswered, threads + 32);
             }
-            __syncwarp();
-            if constexpr (GRAD) block_arrive(kAnswered, threads + 32);
+            // everyone's stores of the row before precede this row's sums
+            if (b != first) finish(b - step, (place + kPlaces - 1) % kPlaces, last_rest, last_whole);
             block_arrive_turn(kJoined, turn, 64);
+            last_rest = rest;
+            last_whole = whole;
         }
+        if constexpr (GRAD) block_sync(kWritten, threads + 32);
+        finish(first + (a.B - 1 - first) / step * step, (place + kPlaces - 1) % kPlaces, last_rest, last_whole);
         return;
     }
 
@@ -528,18 +570,20 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         }
     };
     if (in_range(1601, first, 1, a.B)) fetch(first, 0);
-    int turn = 0, unit = 0;
+    __syncthreads();
+    int turn = 0, place = 0;  // place: of the marks, by rows in threes or by segments in turn
     for (int64_t b = first; b < a.B; b += step, turn ^= 1) {
         Peak rest = {-INFINITY, 0.f};
         uint4 v[ITEMS];
         int count = 0, left = 0;
         bool tail = false;  // whether the row's last piece, one that is not whole, is this thread's
-        for (int q = 0; q < Q; ++q, unit ^= 1) {
+        for (int q = 0; q < Q; ++q) {
             count = count_of(q);
             left = (count + VEC - 1) / VEC - at0;
-            block_sync(kSegment, threads + 32);
-            uint2 marks = sh.marks[unit][tid];
-            if ((marks.x | marks.y) != 0) sh.marks[unit][tid] = make_uint2(0, 0);
+            if constexpr (!GRAD) block_sync(kSegment, threads + 32);
+            uint2 marks = sh.marks[place][tid];
+            if ((marks.x | marks.y) != 0) sh.marks[place][tid] = make_uint2(0, 0);
+            place = place == (GRAD ? 2 : 1) ? 0 : place + 1;
             // what lies past the end in the last piece is struck out, too
             tail = count % VEC != 0 && left > 0 && left <= kWarpPieces && left % 32 == 1;
             if (tail) {
@@ -595,13 +639,17 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             block_sync(kAnswered, threads + 32);
             const float4 o = sh.out;
             const uint64_t minus_r = f2_pack(-o.y, -o.y), times = f2_pack(o.x, o.x);
-            T *out = a.dz + b * a.ld + lo;
+            T *out = a.dz + b * a.ld + lo + at0 * VEC;
+            const int full = count / VEC - at0;
             if (o.z == 0.f) {  // no entries: zeros, whatever z holds
-                for (int i = tid; i < count; i += threads) out[i] = L::from(0.f);
+                for (int j = 0; j < ITEMS; ++j) {
+                    if (j * 32 < full)
+                        ptx::st_stream_v4(out + j * 32 * VEC, make_uint4(0, 0, 0, 0));
+                    else if (tail && j == left / 32)
+                        store_some(out + j * 32 * VEC, make_uint4(0, 0, 0, 0), count % VEC);
+                }
                 continue;
             }
-            out += at0 * VEC;
-            const int full = count / VEC - at0;
 #pragma unroll
             for (int j = 0; j < ITEMS; ++j) {
                 uint64_t f[VEC / 2];
@@ -624,7 +672,10 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             }
         }
     }
-    block_sync(kSegment, threads + 32);
+    if constexpr (GRAD)
+        block_arrive(kWritten, threads + 32);
+    else
+        block_sync(kSegment, threads + 32);
     if (S > 1) cluster_wait();
 }
 
@@ -634,6 +685,7 @@ struct Plan {
     int S, Q, seg, warps, items;
 };
 constexpr int kPieces = 4096;    // a segment's most, but where a gradient needs all and 8 blocks do not reach
+constexpr int kEntryBytes = kPlaces * 16;
 constexpr int kMinPieces = 256;  // rows are split further only down to this
 
 template <typename T>
@@ -666,20 +718,20 @@ Plan plan_of(int64_t B, int V, bool grad, int num_sms)
 template <typename T, bool GRAD, int ITEMS>
 cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, int num_sms, cudaStream_t stream)
 {
-    // Clusters that are resident at once: by device, log2 of the cluster, warps, and whether the
-    // entries take much shared memory
-    static std::atomic<int> resident[64][4][kMaxWarps + 1][2];
-    constexpr int most = kMaxThreads * ITEMS * 16 + kDistillMaxK * 24;
-    constexpr int few = 128;
+    // Clusters that are resident at once: by device, log2 of the cluster, warps, and how much
+    // shared memory the entries take (up to 512 two blocks of 16 warps are resident)
+    static std::atomic<int> resident[64][4][kMaxWarps + 1][3];
+    constexpr int most = kMaxThreads * ITEMS * 16 + kDistillMaxK * kEntryBytes;
+    constexpr int some[3] = {128, 512, kDistillMaxK};
     int dev = 0, log_s = 0;
-    const int many = a.K > few;
+    const int many = a.K > some[1] ? 2 : a.K > some[0] ? 1 : 0;
     while (1 << log_s < p.S) ++log_s;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(p.warps * 32 + 64);
     const size_t pieces = static_cast<size_t>(p.warps) * 32 * ITEMS * 16;
-    cfg.dynamicSmemBytes = pieces + (many ? kDistillMaxK : few) * 24;
+    cfg.dynamicSmemBytes = pieces + some[many] * kEntryBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -703,7 +755,7 @@ cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, int num_sms, cu
     }
     const int64_t rows = a.B < clusters ? a.B : clusters;
     cfg.gridDim = dim3(static_cast<unsigned>(rows * p.S));
-    cfg.dynamicSmemBytes = pieces + static_cast<size_t>(a.K) * 24;
+    cfg.dynamicSmemBytes = pieces + static_cast<size_t>(a.K) * kEntryBytes;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, distill_kernel<T, GRAD, ITEMS>, a, p.seg, p.S, p.Q);
 }
