@@ -69,7 +69,8 @@ int distill_checked(const DistillArgs<T> &a, int64_t V, bool grad, mhc_stream_t 
 {
     const int64_t B = a.B, ld = a.ld;
     if (B < 0 || V < 1 || a.K < 1 || ld < V) return MHC_ERR_INVALID;
-    if (!std::isfinite(a.inv_tau) || !(a.inv_tau > 0.f)) return MHC_ERR_INVALID;
+    // up to 2^64, so that differences of logits times it are numbers
+    if (!(a.inv_tau > 0.f) || !(a.inv_tau <= 0x1p64f)) return MHC_ERR_INVALID;
     if (B >= (int64_t{1} << 31) || V > kDistillMaxV || a.K > kDistillMaxK) return MHC_ERR_UNSUPPORTED;
     if (ld % 8 != 0 || ld > (int64_t{1} << 24)) return MHC_ERR_UNSUPPORTED;
     if (B == 0) return MHC_OK;

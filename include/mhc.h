@@ -529,8 +529,8 @@ int mhc_rmsnorm_backward(const mhc_bf16 *dZ, const mhc_bf16 *H, const float *gai
  * An id that comes more than once has its p added up.  K = 1 without t_lse is cross
  * entropy.  A row without entries has loss 0 and dz 0, whatever its z (padding).  z may hold
  * -inf (a masked vocabulary); where a kept id with p > 0 has it, the loss is +inf.  Any
- * other row with a NaN or +inf in z, or with z = -inf throughout, has loss and dz NaN; one
- * with a NaN or +inf in t or t_lse has loss NaN.
+ * other row with a NaN or +inf in z, or with z = -inf throughout, has loss and dz NaN.  A NaN
+ * or +inf in t makes the row's loss NaN; so may a t_lse that is not finite.
  *
  * The backward works from z alone, in one pass: a training step that knows dloss [B] fp32
  * (1/rows, times tau² where that is wanted) needs no forward call.  Its loss may be NULL.
@@ -538,7 +538,7 @@ int mhc_rmsnorm_backward(const mhc_bf16 *dZ, const mhc_bf16 *H, const float *gai
  * their value nor written.  Results are bitwise reproducible; the losses of the two calls
  * may differ in their last bits.
  *
- * Rules as for the calls above, and: V >= 1, K >= 1, ld >= V, inv_tau finite and > 0
+ * Rules as for the calls above, and: V >= 1, K >= 1, ld >= V, 0 < inv_tau <= 2^64
  * (MHC_ERR_INVALID); B < 2^31, V <= 2^18, K <= 1024, ld % 8 == 0 and ld <= 2^24
  * (MHC_ERR_UNSUPPORTED).
  */

@@ -85,11 +85,12 @@ def test_eps(call):
 def test_loss_rules(call):
     assert call() == NO_DEVICE
     for kw in (dict(B=-1), dict(V=0), dict(K=0), dict(K=-3), dict(ld=992), dict(it=0.0), dict(it=-1.0),
-               dict(it=math.nan), dict(it=math.inf)):
+               dict(it=math.nan), dict(it=math.inf), dict(it=2.0 ** 65)):
         assert call(**kw) == mhc.MHC_ERR_INVALID, kw
     for kw in (dict(B=1 << 31), dict(V=(1 << 18) + 8, ld=(1 << 18) + 8), dict(K=1025), dict(ld=1004),
                dict(ld=(1 << 24) + 8)):
         assert call(**kw) == mhc.MHC_ERR_UNSUPPORTED, kw
+    assert call(it=2.0 ** 64) == NO_DEVICE
     assert call(V=993) == NO_DEVICE and call(K=1024) == NO_DEVICE  # K may be over V
 
 
