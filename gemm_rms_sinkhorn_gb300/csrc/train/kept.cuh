@@ -64,14 +64,19 @@ __device__ __forceinline__ uint2 encode8(const uint4 &v, uint32_t E)
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// The same from fp32: E of a block from its largest magnitude's bits, and eight
-// values to codes under it.
-__device__ __forceinline__ uint32_t amax8(const float (&f)[8])
+// The same from fp32, in pairs: the largest magnitude of eight values as its bit pattern (a
+// NaN is larger than all), E of a block from that, and the codes under it.
+__device__ __forceinline__ uint32_t amax8(const uint64_t (&v)[4])
 {
-    uint32_t a = 0;
+    float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-    return a;
+    for (int p = 0; p < 4; ++p) {
+        float lo, hi;
+        f2_unpack(v[p], lo, hi);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(lo)));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(hi)));
+    }
+    return __float_as_uint(m);
 }
 __device__ __forceinline__ uint32_t scale_code_f32(uint32_t amax)
 {
@@ -79,20 +84,22 @@ __device__ __forceinline__ uint32_t scale_code_f32(uint32_t amax)
     const int e = static_cast<int>((amax + 0x1FFFFFu) >> 23) - 8;
     return e < static_cast<int>(kScaleMin) ? kScaleMin : static_cast<uint32_t>(e);
 }
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], uint32_t E)
+__device__ __forceinline__ uint2 encode8(const uint64_t (&v)[4], uint32_t E)
 {
     if (E == kScaleNan) return make_uint2(kCodesNan, kCodesNan);
     const float inv = __uint_as_float((254u - E) << 23);  // 2^(127 - E), exact
-    float f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = v[e];
-    if (E == kScaleMax) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = fminf(fmaxf(f[e], -0x1.ep127f), 0x1.ep127f);
-    }
     uint32_t h[4];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) h[p] = f32x2_to_e4m3(f[2 * p] * inv, f[2 * p + 1] * inv);
+    for (int p = 0; p < 4; ++p) {
+        float lo, hi;
+        uint64_t f = v[p];
+        if (E == kScaleMax) {
+            f2_unpack(f, lo, hi);
+            f = f2_pack(fminf(fmaxf(lo, -0x1.ep127f), 0x1.ep127f), fminf(fmaxf(hi, -0x1.ep127f), 0x1.ep127f));
+        }
+        f2_unpack(f2_mul(f, f2_pack(inv, inv)), lo, hi);
+        h[p] = f32x2_to_e4m3(lo, hi);
+    }
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
