@@ -569,6 +569,11 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             reinterpret_cast<T *>(mine + v / VEC * 32)[v % VEC] = L::lowest();
         }
     };
+    // Clusters fetch the next row behind the answer, which keeps less in flight while they wait
+    // for one another: 4096 rows of 131072 353 us, 377 where a row is fetched as its place is
+    // free; 2000 of fp32 321, 335.  A block alone does not (4095 rows of 32000 94, 93), nor do
+    // clusters that have few rows (500 rows of fp32, 50001, seven a cluster: 39, 37).
+    const bool late = GRAD && S > 1 && a.B > 8 * step;
     if (in_range(1601, first, 1, a.B)) fetch(first, 0);
     __syncthreads();
     int turn = 0, place = 0;  // place: of the marks, by rows in threes or by segments in turn
@@ -603,7 +608,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             for (int j = 0; j < ITEMS; ++j) v[j] = mine[j * 32];
             if (q + 1 < Q)
                 fetch(b, q + 1);
-            else if (b + step < a.B)
+            else if (!late && b + step < a.B)
                 fetch(b + step, 0);
 
             Peak p;
@@ -637,6 +642,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         pass(b);
         if constexpr (GRAD) {
             block_sync(kAnswered, threads + 32);
+            if (late && b + step < a.B) fetch(b + step, 0);
             const float4 o = sh.out;
             const uint64_t minus_r = f2_pack(-o.y, -o.y), times = f2_pack(o.x, o.x);
             T *out = a.dz + b * a.ld + lo + at0 * VEC;

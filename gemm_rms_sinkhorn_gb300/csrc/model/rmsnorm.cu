@@ -30,17 +30,20 @@ namespace {
 constexpr int kMaxThreads = 512;
 
 // How a token of C channels is laid over threads: `items` chunks of 8 channels a thread,
-// `group` threads a token, `tokens` tokens a block.
+// `group` threads a token, `tokens` tokens a block of `most` threads.  The backward, where a
+// block ends with its row of the workspace, takes blocks of 512: 16384 tokens of 2048 47 us,
+// 59 with 256.
 struct Layout {
     int items, group, tokens;
 };
-Layout layout_of(int64_t C)
+constexpr int kForwardThreads = 256, kBackwardThreads = kMaxThreads;
+Layout layout_of(int64_t C, int most)
 {
     const int c8 = static_cast<int>(C / 8);
     Layout l;
     l.items = c8 <= 256 ? 1 : c8 <= 1024 ? 2 : 4;
     l.group = (((c8 + l.items - 1) / l.items) + 31) / 32 * 32;
-    l.tokens = l.group >= 256 ? 1 : 256 / l.group;
+    l.tokens = l.group >= most ? 1 : most / l.group;  // one with 4 chunks a thread
     return l;
 }
 
@@ -89,18 +92,23 @@ __device__ __forceinline__ void cp_async_wait_but()
 }
 
 // Chunks that a thread has room for, of P pieces of 16 bytes each: what it has read of one
-// makes room for the one that many on.  About 128 bytes a thread in flight, or 128 KB an SM,
-// in whole tokens; half a token where that is over 256 bytes a thread.
+// makes room for the one that many on.  More in flight is not better (us, with one / two /
+// four): 4 streams, 16384 tokens of 2048 60 / 63 / 62, 4096 of 16384 121 / 127 / 128; 5
+// streams, 8191 tokens of 4096 68 / 69 / 70; a residual, 16384 tokens of 2048 43 / 46 / 47.
+// Two are where a chunk is small (one stream, 16384 tokens of 4096 68 / 65 / 67; a residual,
+// 16384 of 7168 151 / 148 / 152) and where blocks are few (8 streams, 4096 tokens of 7168
+// 86 / 85).  The backward with a gradient past the norm, 16384 of 7168: 159 / 148.
 __host__ __device__ constexpr int slots_of(int P, int items)
 {
-    return P * items > 16 ? items / 2 : P * items >= 8 ? items : 8 / (P * items) * items;
+    return P == 1 || P == 8 || (P == 2 && items > 1) ? 2 : 1;
 }
+constexpr int kBackwardSlots = 2;
 // The gain of a thread's channels stays in shared memory, but where those are many.
 __host__ __device__ constexpr bool gain_kept(int items) { return items <= 2; }
-template <int P, int ITEMS>  // P pieces a chunk
-__host__ __device__ constexpr int smem_pieces()  // a thread's
+// A thread's pieces of shared memory, with room for `slots` chunks of P.
+__host__ __device__ constexpr int smem_pieces(int P, int items, int slots)
 {
-    return slots_of(P, ITEMS) * P + (gain_kept(ITEMS) ? 2 * ITEMS : 0);
+    return slots * P + (gain_kept(items) ? 2 * items : 0);
 }
 
 __device__ __forceinline__ void load_gain(const float *gain, int64_t c8, uint4 &u, uint4 &v)
@@ -264,19 +272,16 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rmsnorm_kernel(const NormArgs 
 // The blocks walk the tokens; a thread meets the same channels in each of them, so it
 // holds their share of dgain in fp32 registers.  A block's sums go to its row of the
 // workspace, and a second launch adds the rows in order.
-// Blocks an SM: as many as are resident at 64 registers a thread, or 128 with 4 chunks.  (Four
-// of the narrow ones are: 16384 tokens of 256 take 10.7 us then, 9.5 with two, for each block
-// ends with its row of the workspace.)
+// Blocks an SM: as many as are resident at 64 registers a thread, or 128 with 4 chunks.
 int blocks_per_sm(int items) { return items <= 2 ? 2 : 1; }
 
 template <int ITEMS, bool SKIP>
 __global__ void __launch_bounds__(kMaxThreads, ITEMS <= 2 ? 2 : 1)
 rmsnorm_backward_kernel(const NormBackwardArgs a, int G, int T, float *__restrict__ parts)
 {
-    constexpr int P = SKIP ? 3 : 2, kSlots = slots_of(P, ITEMS), kRooms = kSlots / ITEMS;
-    static_assert(kSlots % ITEMS == 0, "rooms for whole tokens");
+    constexpr int P = SKIP ? 3 : 2, kSlots = kBackwardSlots;
+    constexpr int kRooms = kSlots < ITEMS ? 1 : kSlots / ITEMS;
     __shared__ float red[2][kMaxWarps];
-    __shared__ float4 join[ITEMS == 1 ? 2 * kMaxThreads : 1];
     extern __shared__ __align__(16) uint4 dyn[];  // [smem_pieces][blockDim]
     const int stride = blockDim.x, group = threadIdx.x / G, g = threadIdx.x % G, warps = G >> 5;
     const int C = static_cast<int>(a.C), C8 = C >> 3;
@@ -352,7 +357,7 @@ rmsnorm_backward_kernel(const NormBackwardArgs a, int G, int T, float *__restric
                     acc[k][p] = f2_fma(f2_mul(d[p], rr), h[p], acc[k][p]);
                 }
             }
-            fetch(x, b + kRooms * step, row + kRooms * row_step, k);
+            fetch(x, b + (k + kSlots) / ITEMS * step, row + (k + kSlots) / ITEMS * row_step, (k + kSlots) % ITEMS);
         }
         float lo, hi;
         f2_unpack(ss, lo, hi);
@@ -381,17 +386,23 @@ rmsnorm_backward_kernel(const NormBackwardArgs a, int G, int T, float *__restric
             f2_unpack(acc[k][2 * p], sum[k][p].x, sum[k][p].y);
             f2_unpack(acc[k][2 * p + 1], sum[k][p].z, sum[k][p].w);
         }
-    if constexpr (ITEMS == 1) {
-        join[2 * threadIdx.x] = sum[0][0];
-        join[2 * threadIdx.x + 1] = sum[0][1];
-        __syncthreads();
-        if (group != 0) return;
-        for (int k = 1; k < T; ++k)
+    if constexpr (gain_kept(ITEMS)) {
+        if (T > 1) {  // through the places of the gain
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const float4 u = join[2 * (k * G + g) + p];
-                sum[0][p].x += u.x; sum[0][p].y += u.y; sum[0][p].z += u.z; sum[0][p].w += u.w;
-            }
+            for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) reinterpret_cast<float4 *>(gain)[(2 * k + p) * stride] = sum[k][p];
+            __syncthreads();
+            if (group != 0) return;
+            for (int t = 1; t < T; ++t)
+#pragma unroll
+                for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const float4 u = reinterpret_cast<const float4 *>(gain)[(2 * k + p) * stride + t * G];
+                        sum[k][p].x += u.x; sum[k][p].y += u.y; sum[k][p].z += u.z; sum[k][p].w += u.w;
+                    }
+        }
     }
     float *part = parts + static_cast<int64_t>(blockIdx.x) * C;
 #pragma unroll
@@ -437,19 +448,18 @@ rmsnorm_join_kernel(const float *parts, int rows, int64_t C, int accumulate, flo
 
 int backward_blocks(int64_t B, int64_t C, int num_sms)
 {
-    const Layout l = layout_of(C);
+    const Layout l = layout_of(C, kBackwardThreads);
     const int64_t all = (B + l.tokens - 1) / l.tokens, most = static_cast<int64_t>(blocks_per_sm(l.items)) * num_sms;
     return static_cast<int>(all < most ? all : most);
 }
 
-// Launches `kernel` with P pieces a chunk and `smem` bytes a thread; blocks: at most that many,
-// or 0: as many as are resident at once.
+// Launches `kernel` with so many pieces of shared memory a thread; blocks: how many, or 0: as
+// many as are resident at once.
 template <typename Args, typename... More>
 cudaError_t launch_walking(void (*kernel)(const Args, int, int, More...), std::atomic<uint64_t> &done,
-                           std::atomic<int> *resident, int pieces, int64_t B, int64_t C, int blocks, int num_sms,
+                           std::atomic<int> *resident, int pieces, const Layout &l, int64_t B, int blocks, int num_sms,
                            cudaStream_t stream, const Args &a, More... more)
 {
-    const Layout l = layout_of(C);
     const int threads = l.group * l.tokens;
     const size_t smem = static_cast<size_t>(pieces) * threads * 16;
     cudaError_t e = once_per_device(done, [&] {
@@ -474,16 +484,17 @@ cudaError_t launch_walking(void (*kernel)(const Args, int, int, More...), std::a
 template <int n, int ITEMS, bool Q8>
 cudaError_t launch_forward_as(const NormArgs &a, int num_sms, cudaStream_t stream)
 {
+    constexpr int P = n == 0 ? 2 : n, pieces = smem_pieces(P, ITEMS, slots_of(P, ITEMS));
     static std::atomic<uint64_t> done{0};
     static std::atomic<int> resident[kMaxThreads / 32 + 1];
-    return launch_walking(rmsnorm_kernel<n, ITEMS, Q8>, done, resident, smem_pieces<n == 0 ? 2 : n, ITEMS>(), a.B, a.C, 0,
+    return launch_walking(rmsnorm_kernel<n, ITEMS, Q8>, done, resident, pieces, layout_of(a.C, kForwardThreads), a.B, 0,
                           num_sms, stream, a);
 }
 
 template <int n, bool Q8>
 cudaError_t launch_forward_n(const NormArgs &a, int num_sms, cudaStream_t stream)
 {
-    switch (layout_of(a.C).items) {
+    switch (layout_of(a.C, kForwardThreads).items) {
     case 1: return launch_forward_as<n, 1, Q8>(a, num_sms, stream);
     case 2: return launch_forward_as<n, 2, Q8>(a, num_sms, stream);
     default: return launch_forward_as<n, 4, Q8>(a, num_sms, stream);
@@ -494,14 +505,14 @@ template <int ITEMS, bool SKIP>
 cudaError_t launch_backward_as(const NormBackwardArgs &a, int blocks, float *parts, int num_sms, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
-    return launch_walking(rmsnorm_backward_kernel<ITEMS, SKIP>, done, nullptr, smem_pieces<SKIP ? 3 : 2, ITEMS>(), a.B,
-                          a.C, blocks, num_sms, stream, a, parts);
+    return launch_walking(rmsnorm_backward_kernel<ITEMS, SKIP>, done, nullptr, smem_pieces(SKIP ? 3 : 2, ITEMS, kBackwardSlots),
+                          layout_of(a.C, kBackwardThreads), a.B, blocks, num_sms, stream, a, parts);
 }
 
 template <bool SKIP>
 cudaError_t launch_backward_skip(const NormBackwardArgs &a, int blocks, float *parts, int num_sms, cudaStream_t stream)
 {
-    switch (layout_of(a.C).items) {
+    switch (layout_of(a.C, kBackwardThreads).items) {
     case 1: return launch_backward_as<1, SKIP>(a, blocks, parts, num_sms, stream);
     case 2: return launch_backward_as<2, SKIP>(a, blocks, parts, num_sms, stream);
     default: return launch_backward_as<4, SKIP>(a, blocks, parts, num_sms, stream);
