@@ -267,7 +267,8 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
     const unsigned mine_values = max(min(a.V - lo, Q * seg), 0);  // of the row
     const float c = a.inv_tau * kLog2e;
     const int64_t step = gridDim.x / S, first = blockIdx.x / S;
-    // [kPlaces][K] each: x = t·inv_tau, e^(x - largest x), the word that z lies in, id (-1: absent)
+    // [kPlaces][K] each: x = t·inv_tau less the row's largest (t_lse: not less), e = e^x (e^(x -
+    // t_lse)), the word that z lies in, id (-1: absent)
     float *const xs = reinterpret_cast<float *>(dyn + warps * kWarpPieces), *const es = xs + kPlaces * a.K;
     uint32_t *const words = reinterpret_cast<uint32_t *>(es + kPlaces * a.K);
     int *const ids = reinterpret_cast<int *>(words + kPlaces * a.K);
@@ -337,10 +338,10 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                     const bool here = id[u] >= 0 && id[u] < a.V && t[u] != -INFINITY;
                     const int i = here ? static_cast<int>(id[u]) : -1;
                     idk[k] = i;
-                    x[k] = t[u] * a.inv_tau;
+                    x[k] = t[u];
                     if (!here) continue;
                     some = true;
-                    m = fmaxf(m, x[k]);
+                    m = fmaxf(m, t[u]);
                     if ((rank == 0 || static_cast<unsigned>(i - lo) < mine_values) && in_range(1605, i, 1, a.V))
                         ptx::cp_async4(word + k, row + (i & -L::kWord));
                     if (i >= lo && i - lo < count) twice |= mark(marks, i - lo);
@@ -349,18 +350,20 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             ptx::cp_async_commit();
             some = __any_sync(0xffffffffu, some);
             twice = __any_sync(0xffffffffu, twice);
-            m = a.t_lse != nullptr ? lse : warp_max(m);
+            // the difference first: t times inv_tau may overflow where t is the type's lowest value
+            m = a.t_lse != nullptr ? 0.f : warp_max(m);
             float s = 0.f;
 #pragma unroll 4
             for (int k = lane; k < a.K; k += 32) {
-                const float v = idk[k] >= 0 ? expf(x[k] - m) : 0.f;
+                x[k] = (x[k] - m) * a.inv_tau;
+                const float v = idk[k] >= 0 ? expf(x[k] - lse) : 0.f;
                 e[k] = v;
                 s += v;
             }
             s = warp_sum(s);
             if (lane == 0) {
                 Info &r = sh.info[place];
-                r.base = a.t_lse != nullptr ? m : m + logf(s);
+                r.base = a.t_lse != nullptr ? lse : logf(s);
                 r.unit = a.t_lse != nullptr ? 1.f : 1.f / s;
                 r.mass = a.t_lse != nullptr ? s : 1.f;
                 r.w = dloss * a.inv_tau;
@@ -722,7 +725,7 @@ Plan plan_of(int64_t B, int V, bool grad, int num_sms)
 }
 
 template <typename T, bool GRAD, int ITEMS>
-cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, int num_sms, cudaStream_t stream)
+cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, cudaStream_t stream)
 {
     // Clusters that are resident at once: by device, log2 of the cluster, warps, and how much
     // shared memory the entries take (up to 512 two blocks of 16 warps are resident)
@@ -771,12 +774,12 @@ cudaError_t launch_as(const DistillArgs<T> &a, int num_sms, cudaStream_t stream)
 {
     const Plan p = plan_of<T>(a.B, a.V, GRAD, num_sms);
     switch (p.items) {
-    case 1: return launch_items<T, GRAD, 1>(a, p, num_sms, stream);
-    case 2: return launch_items<T, GRAD, 2>(a, p, num_sms, stream);
-    case 4: return launch_items<T, GRAD, 4>(a, p, num_sms, stream);
-    case 8: return launch_items<T, GRAD, 8>(a, p, num_sms, stream);
+    case 1: return launch_items<T, GRAD, 1>(a, p, stream);
+    case 2: return launch_items<T, GRAD, 2>(a, p, stream);
+    case 4: return launch_items<T, GRAD, 4>(a, p, stream);
+    case 8: return launch_items<T, GRAD, 8>(a, p, stream);
     default:
-        if constexpr (GRAD && Logit<T>::kVec * 16 <= kMaxBits) return launch_items<T, GRAD, 16>(a, p, num_sms, stream);
+        if constexpr (GRAD && Logit<T>::kVec * 16 <= kMaxBits) return launch_items<T, GRAD, 16>(a, p, stream);
         return cudaErrorInvalidValue;
     }
 }

@@ -4,8 +4,10 @@ Roundings of the kernels, u = U32 = 2^-24 each (relative to the value):
   - exp((z - m)·c), c = inv_tau·log2 e: the difference, c twice, the product, each off by u of the
     exponent, so e^(4u·|x|) at |x| = |z - m|·inv_tau; the exponential itself 2^-22 = 4u.
   - a sum over V values: a thread adds at most 64 of them in two chains, then 5 levels of a tree over
-    lanes, at most 8 in turn and 5 levels over warps and blocks, and 2 peaks; three times the sums are
-    shifted to another largest value by an exponential.  Teacher: 32 lanes add K / 32 each, 5 levels.
+    lanes, at most 8 in turn and 5 levels over warps and blocks, and 2 peaks: 20 more, and 16 where a block
+    takes segments one after another.  Sums are shifted to another largest value by an exponential (where
+    that stays the same it is 1): from a thread's to a warp's, a row's, and where a segment has a larger one.
+    Teacher: 32 lanes add K / 32 each, 5 levels.
 """
 import torch
 

@@ -234,6 +234,29 @@ def test_a_vocabulary_masked_by_the_lowest_value(dt):
         check(d, out, dz, 0.5)
 
 
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_a_teacher_masked_by_the_lowest_value(dt, rest):
+    """Times 1/temperature the lowest value is -inf: where it stands for all entries, they are all alike."""
+    B, V, K, it = 3, 900, 40, 4.0
+    d = make(31, B, V, K, dt, rest, it)
+    d["t"][1, 5:] = d["t"][2, 0] = -2e4  # e^(t·inv_tau) is 0
+    low = dict(d, t=d["t"].clone())
+    low["t"][1, 5:] = low["t"][2, 0] = torch.finfo(F32).min
+    if rest:
+        d["t_lse"] = low["t_lse"] = torch.logsumexp(d["t"] * it, 1) + 0.2
+    else:
+        d["t"][0], low["t"][0] = 0.0, torch.finfo(F32).min
+    g = Guarded()
+    out, dz, _ = call(low, up8(V), it, g)
+    check(d, out, dz, it)
+    same, same_dz, _ = call(d, up8(V), it, g)
+    assert torch.equal(out, same) and torch.equal(dz[:, :V], same_dz[:, :V])
+    fwd, _, _ = call(low, up8(V), it, g, grad=False)
+    check(d, fwd, None, it)
+    g.check()
+
+
 def test_one_entry_is_cross_entropy():
     B, V = 37, 513
     d = make(12, B, V, 1, F32, False)
