@@ -219,12 +219,36 @@ __device__ __noinline__ void store_some(T *p, uint4 v, int n)
         }
 }
 
+// The sum of e at the entries that are `again`, of the chunks of 32 that have a bit in `repeats`.
+__device__ __forceinline__ float repeated(const int *idk, const float *e, int again, uint32_t repeats, int Kp)
+{
+    float sum = 0.f;
+#pragma unroll 1
+    for (; repeats != 0; repeats &= repeats - 1) {
+        const int from = (__ffs(static_cast<int>(repeats)) - 1) * 32;
+#pragma unroll 1
+        for (int l = from; l < from + 32 && l < Kp; l += 16) {
+            const int4 *v = reinterpret_cast<const int4 *>(idk + l);
+            bool any = false;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                any |= v[q].x == again | v[q].y == again | v[q].z == again | v[q].w == again;
+            if (!any) continue;
+#pragma unroll 1
+            for (int q = l; q < l + 16; ++q)
+                if (idk[q] == again) sum += e[q];
+        }
+    }
+    return sum;
+}
+
 constexpr int kPlaces = 4;  // rows whose entries are held: one to finish, one summed up, two ahead
 struct Info {               // of a row's entries
     float kept_m, kept_s;   // the student's peak there, of this block's segments
     float base, unit;       // log p = x - base, p = e·unit
     float mass, w;          // Σ p, dloss·inv_tau
-    int flags;
+    int some;               // whether entries are present
+    uint32_t repeats;       // bit j: one of entries 32·j.. is a repeat (kRepeat)
 };
 struct Shared {
     float2 rests[2][kMaxCluster][kMaxWarps], kepts[2][kMaxCluster];  // the cluster's peaks
@@ -233,7 +257,9 @@ struct Shared {
     uint2 marks[3][kMaxThreads];  // bit j·VEC + e: value e of the thread's piece j is kept
     Info info[kPlaces];
 };
-constexpr int kSome = 1, kTwice = 2;  // entries are present; an id comes more than once here
+// Marks an entry whose id an entry before it has, in the block that holds the id.
+constexpr int kRepeat = 1 << 30;
+__host__ __device__ constexpr int room_of(int K) { return (K + 15) & ~15; }  // entries
 // The block's barriers:
 //   kSegment   (without a gradient) a segment's marks are there, and the one before is done
 //              with: the row's threads and the entries' warp meet
@@ -255,8 +281,9 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
     constexpr int VEC = L::kVec;
     static_assert(ITEMS * VEC <= kMaxBits, "a thread's values have a bit each");
     __shared__ Shared sh;
-    // pieces [warps][ITEMS][32], a warp's one after another; then the entries
-    extern __shared__ __align__(16) uint4 dyn[];
+    // pieces [warps][ITEMS][32], a warp's one after another; then the entries.  Lines of 128
+    // bytes: 16 bytes past that the loss of 2048 rows of 131072 takes 99 us, not 83.
+    extern __shared__ __align__(128) uint4 dyn[];
     constexpr int kWarpPieces = ITEMS * 32;
 
     const int Q = GRAD ? 1 : segments;
@@ -267,11 +294,12 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
     const unsigned mine_values = max(min(a.V - lo, Q * seg), 0);  // of the row
     const float c = a.inv_tau * kLog2e;
     const int64_t step = gridDim.x / S, first = blockIdx.x / S;
-    // [kPlaces][K] each: x = t·inv_tau less the row's largest (t_lse: not less), e = e^x (e^(x -
-    // t_lse)), the word that z lies in, id (-1: absent)
-    float *const xs = reinterpret_cast<float *>(dyn + warps * kWarpPieces), *const es = xs + kPlaces * a.K;
-    uint32_t *const words = reinterpret_cast<uint32_t *>(es + kPlaces * a.K);
-    int *const ids = reinterpret_cast<int *>(words + kPlaces * a.K);
+    // [kPlaces][K, to a multiple of 16] each: x = t·inv_tau less the row's largest (t_lse: not
+    // less), e = e^x (e^(x - t_lse)), the word that z lies in, the id (-1: absent)
+    const int Kp = room_of(a.K);
+    float *const xs = reinterpret_cast<float *>(dyn + warps * kWarpPieces), *const es = xs + kPlaces * Kp;
+    uint32_t *const words = reinterpret_cast<uint32_t *>(es + kPlaces * Kp);
+    int *const ids = reinterpret_cast<int *>(words + kPlaces * Kp);
     // A row's barrier of the cluster, for the warps that do not wait for the others' sums:
     // they take part a row behind.
     const auto pass = [&](int64_t b) {
@@ -295,17 +323,17 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         constexpr int kAhead = 4;  // entries a lane taken at once, the first ones read another row ahead
         int64_t id[kAhead];
         float t[kAhead], lse = 0.f, dloss = 0.f;
-        const auto read = [&](int64_t b, int k0) {
+        const auto read = [&](int64_t b, int base) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const int k = k0 + 32 * u;
+                const int k = base + 32 * u + lane;
                 id[u] = k < a.K ? ptx::ld_dep(a.ids + b * a.K + k) : -1;
                 t[u] = k < a.K ? ptx::ld_dep(a.t + b * a.K + k) : 0.f;
             }
         };
         const auto read_ahead = [&](int64_t b) {
             if (b >= a.B) return;
-            read(b, lane);
+            read(b, 0);
             if (a.t_lse != nullptr) lse = ptx::ld_dep(a.t_lse + b);
             if constexpr (GRAD) dloss = ptx::ld_dep(a.dloss + b);
         };
@@ -315,41 +343,51 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             uint32_t *w = &marks[p / kWarpPieces * 32 + p % 32].x + (bit >> 5);
             return (atomicOr(w, 1u << (bit & 31)) >> (bit & 31) & 1u) != 0;
         };
+        // Whether an entry's id i has come before; `marked`: whether its mark was there.  Of
+        // lanes with the same id, which came to mark it in any order, the first one is new.
+        const auto repeats = [&](bool in, int i, bool marked) {
+            if (!__any_sync(0xffffffffu, marked)) return false;
+            const uint32_t same = __match_any_sync(0xffffffffu, in ? i : -1 - lane);
+            const uint32_t fresh = __ballot_sync(0xffffffffu, in && !marked);
+            return in && ((same & fresh) == 0 || lane != __ffs(static_cast<int>(same)) - 1);
+        };
         // Row b into its place, its first segment's kept ids into `marks`; after read_ahead(b).
         const auto prepare = [&](int64_t b, int place, uint2 *marks) {
             if (b >= a.B) {
                 ptx::cp_async_commit();
                 return;
             }
-            float *x = xs + place * a.K, *e = es + place * a.K;
-            uint32_t *word = words + place * a.K;
-            int *idk = ids + place * a.K;
+            float *x = xs + place * Kp, *e = es + place * Kp;
+            uint32_t *word = words + place * Kp;
+            int *idk = ids + place * Kp;
             const T *row = a.z + b * a.ld;
             const int count = max(min(a.V - lo, seg), 0);
             float m = -INFINITY;
-            bool some = false, twice = false;
+            bool some = false;
+            uint32_t chunks = 0;
 #pragma unroll 1
-            for (int k0 = lane; k0 < a.K; k0 += 32 * kAhead) {
-                if (k0 != lane) read(b, k0);
+            for (int base = 0; base < Kp; base += 32 * kAhead) {
+                if (base != 0) read(b, base);
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    const int k = k0 + 32 * u;
-                    if (k >= a.K) continue;
+                    const int k = base + 32 * u + lane;
                     const bool here = id[u] >= 0 && id[u] < a.V && t[u] != -INFINITY;
                     const int i = here ? static_cast<int>(id[u]) : -1;
-                    idk[k] = i;
-                    x[k] = t[u];
-                    if (!here) continue;
-                    some = true;
-                    m = fmaxf(m, t[u]);
-                    if ((rank == 0 || static_cast<unsigned>(i - lo) < mine_values) && in_range(1605, i, 1, a.V))
-                        ptx::cp_async4(word + k, row + (i & -L::kWord));
-                    if (i >= lo && i - lo < count) twice |= mark(marks, i - lo);
+                    if (k < Kp) x[k] = t[u];
+                    if (here) {
+                        some = true;
+                        m = fmaxf(m, t[u]);
+                        if ((rank == 0 || static_cast<unsigned>(i - lo) < mine_values) && in_range(1605, i, 1, a.V))
+                            ptx::cp_async4(word + k, row + (i & -L::kWord));
+                    }
+                    const bool in = i >= lo && i - lo < count, again = repeats(in, i, in && mark(marks, i - lo));
+                    if (again) chunks |= 1u << (k >> 5);
+                    if (k < Kp) idk[k] = again ? i | kRepeat : i;
                 }
             }
             ptx::cp_async_commit();
             some = __any_sync(0xffffffffu, some);
-            twice = __any_sync(0xffffffffu, twice);
+            chunks = __reduce_or_sync(0xffffffffu, chunks);
             // the difference first: t times inv_tau may overflow where t is the type's lowest value
             m = a.t_lse != nullptr ? 0.f : warp_max(m);
             float s = 0.f;
@@ -367,37 +405,26 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 r.unit = a.t_lse != nullptr ? 1.f : 1.f / s;
                 r.mass = a.t_lse != nullptr ? s : 1.f;
                 r.w = dloss * a.inv_tau;
-                r.flags = (some ? kSome : 0) | (twice ? kTwice : 0);
+                r.some = some;
+                r.repeats = chunks;
             }
             __syncwarp();
         };
-        // The peak at the kept ids of this block, each once.
+        // The peak at the kept ids of this block, each once (absent and repeated ones lie outside).
         const auto peak = [&](int place) {
-            const uint32_t *word = words + place * a.K;
-            const int *idk = ids + place * a.K;
-            const int flags = sh.info[place].flags;
+            const uint32_t *word = words + place * Kp;
+            const int *idk = ids + place * Kp;
             Peak kept = {-INFINITY, 0.f};
 #pragma unroll 4
             for (int k = lane; k < a.K; k += 32)
-                if (idk[k] >= 0 && static_cast<unsigned>(idk[k] - lo) < mine_values)
+                if (static_cast<unsigned>(idk[k] - lo) < mine_values)
                     kept.m = fmaxf(kept.m, L::word(word[k], idk[k]));
             kept.m = warp_max(kept.m);
             const float r = reference(kept.m);
-            if (flags & kTwice) {
-#pragma unroll 1
-                for (int k = lane; k < a.K; k += 32) {
-                    if (idk[k] < 0 || static_cast<unsigned>(idk[k] - lo) >= mine_values) continue;
-                    bool once = true;
-#pragma unroll 1
-                    for (int i = 0; i < k; ++i) once = once && idk[i] != idk[k];
-                    if (once) kept.s += exp2_fast((L::word(word[k], idk[k]) - r) * c);
-                }
-            } else {
 #pragma unroll 4
-                for (int k = lane; k < a.K; k += 32)
-                    if (idk[k] >= 0 && static_cast<unsigned>(idk[k] - lo) < mine_values)
-                        kept.s += exp2_fast((L::word(word[k], idk[k]) - r) * c);
-            }
+            for (int k = lane; k < a.K; k += 32)
+                if (static_cast<unsigned>(idk[k] - lo) < mine_values)
+                    kept.s += exp2_fast((L::word(word[k], idk[k]) - r) * c);
             kept.s = warp_sum(kept.s);
             if (lane == 0) {
                 sh.info[place].kept_m = kept.m;
@@ -418,17 +445,18 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         int unit = 0;
         for (int64_t b = first; b < a.B; b += step, turn ^= 1, place = (place + 1) % kPlaces) {
             if constexpr (!GRAD) {
-                const int *idk = ids + place * a.K;
+                int *idk = ids + place * Kp;
                 for (int q = 1; q <= Q; ++q) {
                     block_sync(kSegment, threads + 32);
                     unit ^= 1;
                     if (q == Q) break;
                     const int from = lo + q * seg, count = max(min(a.V - from, seg), 0);
-                    bool twice = false;
-#pragma unroll 4
-                    for (int k = lane; k < a.K; k += 32)
-                        if (idk[k] >= from && idk[k] - from < count) twice |= mark(sh.marks[unit], idk[k] - from);
-                    if (__any_sync(0xffffffffu, twice) && lane == 0) sh.info[place].flags |= kTwice;
+#pragma unroll 2
+                    for (int base = 0; base < Kp; base += 32) {
+                        const int k = base + lane, i = k < Kp ? idk[k] : -1;
+                        const bool in = i >= from && i - from < count;
+                        if (repeats(in, i, in && mark(sh.marks[unit], i - from))) idk[k] = i | kRepeat;
+                    }
                     __syncwarp();
                 }
             }
@@ -456,12 +484,13 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
     if (warp > warps) {  // ---- joining
         // What a joined row leaves to do: its loss, and the gradient at the kept ids.
         const auto finish = [&](int64_t b, int place, Peak rest, Peak whole) {
-            const float *x = xs + place * a.K, *e = es + place * a.K;
-            const uint32_t *word = words + place * a.K;
-            const int *idk = ids + place * a.K;
+            const float *x = xs + place * Kp, *e = es + place * Kp;
+            const uint32_t *word = words + place * Kp;
+            const int *idk = ids + place * Kp;
             const Info &r = sh.info[place];
             const float base = r.base, unit = r.unit, mass = r.mass, w = r.w;
-            const int flags = r.flags;
+            const uint32_t repeats = r.repeats;
+            const bool some = r.some;
             const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - mass, 0.f) : 0.f;
             const bool losses = rank == 0 && a.loss != nullptr;
             const float ln_s = logf(whole.s), factor = w * (mass + p_rest) / whole.s, ref = reference(whole.m);
@@ -469,20 +498,22 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
 #pragma unroll 2
             for (int k = lane; k < a.K; k += 32) {
                 const int i = idk[k];
-                const bool here = i >= 0 && static_cast<unsigned>(i - lo) < mine_values;
+                const bool here = static_cast<unsigned>(i - lo) < mine_values;  // and no repeat
                 if (!here && !(losses && i >= 0)) continue;
                 const float p = e[k] * unit, z = L::word(word[k], i);
                 if (losses && p != 0.f) part += p * (x[k] - base - ((z - whole.m) * a.inv_tau - ln_s));
                 if constexpr (GRAD) {
-                    if (!here || !in_range(1604, i, 1, a.V)) continue;
-                    float all = p;
-                    if (flags & kTwice) {
-                        all = 0.f;
+                    if (here && repeats == 0 && in_range(1604, i, 1, a.V))
+                        a.dz[b * a.ld + i] = L::from(fmaf(exp2_fast((z - ref) * c), factor, -(w * p)));
+                }
+            }
+            if (GRAD && repeats != 0) {
 #pragma unroll 1
-                        for (int l = 0; l < a.K; ++l)
-                            if (idk[l] == i) all += e[l] * unit;
-                    }
-                    a.dz[b * a.ld + i] = L::from(fmaf(exp2_fast((z - ref) * c), factor, -(w * all)));
+                for (int k = lane; k < a.K; k += 32) {
+                    const int i = idk[k];
+                    if (static_cast<unsigned>(i - lo) >= mine_values || !in_range(1604, i, 1, a.V)) continue;
+                    const float all = unit * (e[k] + repeated(idk, e, i | kRepeat, repeats, Kp));
+                    a.dz[b * a.ld + i] = L::from(fmaf(exp2_fast((L::word(word[k], i) - ref) * c), factor, -(w * all)));
                 }
             }
             if (losses) {
@@ -490,7 +521,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 if (lane == 0) {
                     if (p_rest > 0.f)
                         part += p_rest * (logf(p_rest) - ((rest.m - whole.m) * a.inv_tau + logf(rest.s) - ln_s));
-                    a.loss[b] = flags & kSome ? part : 0.f;
+                    a.loss[b] = some ? part : 0.f;
                 }
             }
             __syncwarp();
@@ -533,7 +564,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                     const float q_rest = rest.s == 0.f ? 0.f : rest.s * exp2_fast((rest.m - whole.m) * c) / whole.s;
                     const float scale = rest.s != 0.f ? r.w * ((r.mass + p_rest) * q_rest - p_rest) / rest.s
                                                       : whole.s != 0.f ? 0.f : NAN;
-                    sh.out = make_float4(scale, reference(rest.m), r.flags & kSome ? 1.f : 0.f, 0.f);
+                    sh.out = make_float4(scale, reference(rest.m), r.some ? 1.f : 0.f, 0.f);
                 }
                 __syncwarp();
                 block_arrive(kAnswered, threads + 32);
@@ -730,7 +761,7 @@ cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, cudaStream_t st
     // Clusters that are resident at once: by device, log2 of the cluster, warps, and how much
     // shared memory the entries take (up to 512 two blocks of 16 warps are resident)
     static std::atomic<int> resident[64][4][kMaxWarps + 1][3];
-    constexpr int most = kMaxThreads * ITEMS * 16 + kDistillMaxK * kEntryBytes;
+    constexpr int most = kMaxThreads * ITEMS * 16 + room_of(kDistillMaxK) * kEntryBytes;
     constexpr int some[3] = {128, 512, kDistillMaxK};
     int dev = 0, log_s = 0;
     const int many = a.K > some[1] ? 2 : a.K > some[0] ? 1 : 0;
@@ -764,7 +795,7 @@ cudaError_t launch_items(const DistillArgs<T> &a, const Plan &p, cudaStream_t st
     }
     const int64_t rows = a.B < clusters ? a.B : clusters;
     cfg.gridDim = dim3(static_cast<unsigned>(rows * p.S));
-    cfg.dynamicSmemBytes = pieces + static_cast<size_t>(a.K) * kEntryBytes;
+    cfg.dynamicSmemBytes = pieces + static_cast<size_t>(room_of(a.K)) * kEntryBytes;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, distill_kernel<T, GRAD, ITEMS>, a, p.seg, p.S, p.Q);
 }

@@ -133,6 +133,31 @@ def test_an_id_that_comes_more_than_once(B, V, K, dt, rest):
     assert torch.equal(out, again) and torch.equal(dz[:, :V], dz2[:, :V])
 
 
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("V,K,of", [(1000, 64, 20), (32000, 1024, 600), (131072, 1001, 3), (262144, 130, 64)])
+def test_ids_drawn_with_repetition(V, K, of, rest):
+    """As a teacher that samples what it keeps draws them: repeats side by side and far apart, of every part
+    of a row; and the same bits each time."""
+    B, it = 3, 1.0
+    d = make(V + of, B, V, K, F32, rest, it)
+    g = torch.Generator().manual_seed(K)
+    d["ids"] = torch.randperm(V, generator=g)[:of][torch.randint(0, of, (B, K), generator=g)]
+    d["ids"][2, 1::2] = -1
+    d["ids"][1, :40] = d["ids"][1, 0]
+    if rest:  # a sum that leaves something over
+        d["t_lse"] = torch.logsumexp(d["t"] * it, 1) + 0.1
+    mem = Guarded()
+    out, dz, _ = call(d, up8(V), it, mem)
+    check(d, out, dz, it)
+    fwd, _, _ = call(d, up8(V), it, mem, grad=False)
+    check(d, fwd, None, it)
+    for _ in range(3):
+        again, dz2, _ = call(d, up8(V), it, mem)
+        assert torch.equal(out, again) and torch.equal(dz[:, :V], dz2[:, :V])
+        assert torch.equal(call(d, up8(V), it, mem, grad=False)[0], fwd)
+    mem.check()
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_a_masked_vocabulary(dt):
     """-inf in z: no share, no gradient; a kept id there makes the loss infinite."""
