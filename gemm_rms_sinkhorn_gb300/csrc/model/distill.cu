@@ -29,6 +29,14 @@
 // Exponentials are exp2((z - m)·c), c = inv_tau·log2 e, m the largest z seen, two values at
 // a time.  As one fused multiply-add z·c - m·c they would be off by what m·c rounds away:
 // with a vocabulary masked by the type's lowest value m may be that.
+//
+// Bound by memory, all else is kept behind it: 3.6 instructions a value for the sum and 4.4 for
+// the gradient, two exponentials at 32 a clock and SM.  Of the copy rate of 6.78 TB/s: loss of
+// 2048 rows of 131072 bf16, K = 64, 83 us, 0.96; with the gradient 4095 rows of 32000, K = 32,
+// 92.6 us, 0.84 (14 rounds of rows for 13.5); 4096 of 131072, K = 128, 357 us, 0.89 (blocks of a
+// cluster wait for one another); 500 rows of 50001 fp32 37 us, 0.79 (7 rounds for 6.6).  Few
+// rows: 5.6 us, the call.  Above K = 256 the entries' warp sets the pace: 4096 rows of 32000
+// with the gradient 91 us at K = 128, 98 at 256, 138 at 512, 330 at 1024.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -98,8 +106,15 @@ __device__ __forceinline__ void st_cluster(float2 *p, uint32_t rank, float2 v)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
 }
-// All copies of this thread have landed but those of its last group.
-__device__ __forceinline__ void cp_async_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+template <int N>  // all copies of this thread have landed but those of its last N groups
+__device__ __forceinline__ void cp_async_wait_but()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async8(void *dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
@@ -219,8 +234,8 @@ __device__ __noinline__ void store_some(T *p, uint4 v, int n)
         }
 }
 
-// The sum of e at the entries that are `again`, of the chunks of 32 that have a bit in `repeats`.
-__device__ __forceinline__ float repeated(const int *idk, const float *e, int again, uint32_t repeats, int Kp)
+// The sum of e^(x - shift) at the entries that are `again`, of the chunks of 32 that have a bit in `repeats`.
+__device__ __forceinline__ float repeated(const int *idk, const float *x, float shift, int again, uint32_t repeats, int Kp)
 {
     float sum = 0.f;
 #pragma unroll 1
@@ -236,7 +251,7 @@ __device__ __forceinline__ float repeated(const int *idk, const float *e, int ag
             if (!any) continue;
 #pragma unroll 1
             for (int q = l; q < l + 16; ++q)
-                if (idk[q] == again) sum += e[q];
+                if (idk[q] == again) sum += expf(x[q] - shift);
         }
     }
     return sum;
@@ -245,7 +260,7 @@ __device__ __forceinline__ float repeated(const int *idk, const float *e, int ag
 constexpr int kPlaces = 4;  // rows whose entries are held: one to finish, one summed up, two ahead
 struct Info {               // of a row's entries
     float kept_m, kept_s;   // the student's peak there, of this block's segments
-    float base, unit;       // log p = x - base, p = e·unit
+    float base, unit;       // log p = x - base, p = e^x·unit (t_lse: e^(x - base))
     float mass, w;          // Σ p, dloss·inv_tau
     int some;               // whether entries are present
     uint32_t repeats;       // bit j: one of entries 32·j.. is a repeat (kRepeat)
@@ -295,11 +310,13 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
     const float c = a.inv_tau * kLog2e;
     const int64_t step = gridDim.x / S, first = blockIdx.x / S;
     // [kPlaces][K, to a multiple of 16] each: x = t·inv_tau less the row's largest (t_lse: not
-    // less), e = e^x (e^(x - t_lse)), the word that z lies in, the id (-1: absent)
+    // less), the word that z lies in, the id (-1: absent); then a row's entries as they come
     const int Kp = room_of(a.K);
-    float *const xs = reinterpret_cast<float *>(dyn + warps * kWarpPieces), *const es = xs + kPlaces * Kp;
-    uint32_t *const words = reinterpret_cast<uint32_t *>(es + kPlaces * Kp);
+    float *const xs = reinterpret_cast<float *>(dyn + warps * kWarpPieces);
+    uint32_t *const words = reinterpret_cast<uint32_t *>(xs + kPlaces * Kp);
     int *const ids = reinterpret_cast<int *>(words + kPlaces * Kp);
+    int64_t *const came_ids = reinterpret_cast<int64_t *>(ids + kPlaces * Kp);
+    float *const came_ts = reinterpret_cast<float *>(came_ids + Kp);
     // A row's barrier of the cluster, for the warps that do not wait for the others' sums:
     // they take part a row behind.
     const auto pass = [&](int64_t b) {
@@ -320,22 +337,21 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
     __syncthreads();
 
     if (warp == warps) {  // ---- the entries
-        constexpr int kAhead = 4;  // entries a lane taken at once, the first ones read another row ahead
-        int64_t id[kAhead];
-        float t[kAhead], lse = 0.f, dloss = 0.f;
-        const auto read = [&](int64_t b, int base) {
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int k = base + 32 * u + lane;
-                id[u] = k < a.K ? ptx::ld_dep(a.ids + b * a.K + k) : -1;
-                t[u] = k < a.K ? ptx::ld_dep(a.t + b * a.K + k) : 0.f;
-            }
-        };
+        float lse = 0.f, dloss = 0.f;
+        // What is given for row b, on its way; a lane reads what it has copied itself.
         const auto read_ahead = [&](int64_t b) {
-            if (b >= a.B) return;
-            read(b, 0);
-            if (a.t_lse != nullptr) lse = ptx::ld_dep(a.t_lse + b);
-            if constexpr (GRAD) dloss = ptx::ld_dep(a.dloss + b);
+            if (b < a.B) {
+                const int64_t *id = a.ids + b * a.K;
+                const float *t = a.t + b * a.K;
+#pragma unroll 4
+                for (int k = lane; k < a.K; k += 32) {
+                    cp_async8(came_ids + k, id + k);
+                    ptx::cp_async4(came_ts + k, t + k);
+                }
+                if (a.t_lse != nullptr) lse = ptx::ld_dep(a.t_lse + b);
+                if constexpr (GRAD) dloss = ptx::ld_dep(a.dloss + b);
+            }
+            ptx::cp_async_commit();
         };
         // Marks value `at` of a segment; whether it has been marked before.
         const auto mark = [&](uint2 *marks, int at) {
@@ -357,33 +373,32 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 ptx::cp_async_commit();
                 return;
             }
-            float *x = xs + place * Kp, *e = es + place * Kp;
+            float *x = xs + place * Kp;
             uint32_t *word = words + place * Kp;
             int *idk = ids + place * Kp;
             const T *row = a.z + b * a.ld;
             const int count = max(min(a.V - lo, seg), 0);
             float m = -INFINITY;
             bool some = false;
+            ptx::cp_async_wait_all();  // read_ahead's
             uint32_t chunks = 0;
-#pragma unroll 1
-            for (int base = 0; base < Kp; base += 32 * kAhead) {
-                if (base != 0) read(b, base);
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int k = base + 32 * u + lane;
-                    const bool here = id[u] >= 0 && id[u] < a.V && t[u] != -INFINITY;
-                    const int i = here ? static_cast<int>(id[u]) : -1;
-                    if (k < Kp) x[k] = t[u];
-                    if (here) {
-                        some = true;
-                        m = fmaxf(m, t[u]);
-                        if ((rank == 0 || static_cast<unsigned>(i - lo) < mine_values) && in_range(1605, i, 1, a.V))
-                            ptx::cp_async4(word + k, row + (i & -L::kWord));
-                    }
-                    const bool in = i >= lo && i - lo < count, again = repeats(in, i, in && mark(marks, i - lo));
-                    if (again) chunks |= 1u << (k >> 5);
-                    if (k < Kp) idk[k] = again ? i | kRepeat : i;
+#pragma unroll 4
+            for (int base = 0; base < Kp; base += 32) {
+                const int k = base + lane;
+                const int64_t id = k < a.K ? came_ids[k] : -1;
+                const float t = k < a.K ? came_ts[k] : 0.f;
+                const bool here = id >= 0 && id < a.V && t != -INFINITY;
+                const int i = here ? static_cast<int>(id) : -1;
+                if (k < Kp) x[k] = t;
+                if (here) {
+                    some = true;
+                    m = fmaxf(m, t);
+                    if ((rank == 0 || static_cast<unsigned>(i - lo) < mine_values) && in_range(1605, i, 1, a.V))
+                        ptx::cp_async4(word + k, row + (i & -L::kWord));
                 }
+                const bool in = i >= lo && i - lo < count, again = repeats(in, i, in && mark(marks, i - lo));
+                if (again) chunks |= 1u << (k >> 5);
+                if (k < Kp) idk[k] = again ? i | kRepeat : i;
             }
             ptx::cp_async_commit();
             some = __any_sync(0xffffffffu, some);
@@ -394,9 +409,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
 #pragma unroll 4
             for (int k = lane; k < a.K; k += 32) {
                 x[k] = (x[k] - m) * a.inv_tau;
-                const float v = idk[k] >= 0 ? expf(x[k] - lse) : 0.f;
-                e[k] = v;
-                s += v;
+                if (idk[k] >= 0) s += expf(x[k] - lse);
             }
             s = warp_sum(s);
             if (lane == 0) {
@@ -434,13 +447,14 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         };
         constexpr int kLead = GRAD ? 2 : 1;  // rows prepared ahead
         read_ahead(first);
-        prepare(first, 0, sh.marks[0]);
-        read_ahead(first + step);
-        if constexpr (GRAD) {
-            prepare(first + step, 1, sh.marks[1]);
-            read_ahead(first + 2 * step);
+        // the first row's marks are all that the others need to begin (500 rows of fp32 38.0 us
+        // behind both rows, 37.2 behind one)
+#pragma unroll 1
+        for (int r = 0; r < kLead; ++r) {
+            prepare(first + r * step, r, sh.marks[r]);
+            read_ahead(first + (r + 1) * step);
+            if (r == 0) __syncthreads();  // the first marks are there
         }
-        __syncthreads();  // the first marks are there
         int turn = 0, place = 0, third = kLead;  // third: of the marks, where the row after the lead has them
         int unit = 0;
         for (int64_t b = first; b < a.B; b += step, turn ^= 1, place = (place + 1) % kPlaces) {
@@ -461,9 +475,9 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 }
             }
             if constexpr (GRAD)
-                cp_async_wait_but_one();
+                cp_async_wait_but<2>();
             else
-                ptx::cp_async_wait_all();
+                cp_async_wait_but<1>();
             __syncwarp();
             peak(place);
             block_arrive_turn(kSummed, turn, threads + 64);
@@ -484,11 +498,11 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
     if (warp > warps) {  // ---- joining
         // What a joined row leaves to do: its loss, and the gradient at the kept ids.
         const auto finish = [&](int64_t b, int place, Peak rest, Peak whole) {
-            const float *x = xs + place * Kp, *e = es + place * Kp;
+            const float *x = xs + place * Kp;
             const uint32_t *word = words + place * Kp;
             const int *idk = ids + place * Kp;
             const Info &r = sh.info[place];
-            const float base = r.base, unit = r.unit, mass = r.mass, w = r.w;
+            const float base = r.base, unit = r.unit, mass = r.mass, w = r.w, shift = a.t_lse != nullptr ? base : 0.f;
             const uint32_t repeats = r.repeats;
             const bool some = r.some;
             const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - mass, 0.f) : 0.f;
@@ -500,7 +514,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 const int i = idk[k];
                 const bool here = static_cast<unsigned>(i - lo) < mine_values;  // and no repeat
                 if (!here && !(losses && i >= 0)) continue;
-                const float p = e[k] * unit, z = L::word(word[k], i);
+                const float p = expf(x[k] - shift) * unit, z = L::word(word[k], i);
                 if (losses && p != 0.f) part += p * (x[k] - base - ((z - whole.m) * a.inv_tau - ln_s));
                 if constexpr (GRAD) {
                     if (here && repeats == 0 && in_range(1604, i, 1, a.V))
@@ -512,7 +526,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 for (int k = lane; k < a.K; k += 32) {
                     const int i = idk[k];
                     if (static_cast<unsigned>(i - lo) >= mine_values || !in_range(1604, i, 1, a.V)) continue;
-                    const float all = unit * (e[k] + repeated(idk, e, i | kRepeat, repeats, Kp));
+                    const float all = unit * (expf(x[k] - shift) + repeated(idk, x, shift, i | kRepeat, repeats, Kp));
                     a.dz[b * a.ld + i] = L::from(fmaf(exp2_fast((L::word(word[k], i) - ref) * c), factor, -(w * all)));
                 }
             }
@@ -604,7 +618,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         }
     };
     // Clusters fetch the next row behind the answer, which keeps less in flight while they wait
-    // for one another: 4096 rows of 131072 353 us, 377 where a row is fetched as its place is
+    // for one another: 4096 rows of 131072 359 us, 377 where a row is fetched as its place is
     // free; 2000 of fp32 321, 335.  A block alone does not (4095 rows of 32000 94, 93), nor do
     // clusters that have few rows (500 rows of fp32, 50001, seven a cluster: 39, 37).
     const bool late = GRAD && S > 1 && a.B > 8 * step;
@@ -725,7 +739,7 @@ struct Plan {
     int S, Q, seg, warps, items;
 };
 constexpr int kPieces = 4096;    // a segment's most, but where a gradient needs all and 8 blocks do not reach
-constexpr int kEntryBytes = kPlaces * 16;
+constexpr int kEntryBytes = kPlaces * 12 + 12;
 constexpr int kMinPieces = 256;  // rows are split further only down to this
 
 template <typename T>

