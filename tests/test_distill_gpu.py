@@ -241,6 +241,18 @@ def test_large_logits_and_temperatures():
         check(d, out, dz, inv_tau)
 
 
+@pytest.mark.parametrize("inv_tau", [1e-30, 1e4])
+@pytest.mark.parametrize("rest", [False, True])
+def test_temperatures_far_out(rest, inv_tau):
+    """All alike, and one that takes all."""
+    B, V, K = 4, 3001, 8
+    d = make(12, B, V, K, F32, rest, inv_tau)
+    g = Guarded()
+    out, dz, _ = call(d, 3008, inv_tau, g)
+    g.check()
+    check(d, out, dz, inv_tau)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_a_vocabulary_masked_by_the_lowest_value(dt):
     """The type's lowest value in place of -inf: the rest's largest logit may be that."""

@@ -93,6 +93,32 @@ def test_pre_apply_rmsnorm(B, n, C, q8, keep):
         assert torch.equal(F, H)
 
 
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("B,n,C", [(33, 4, 264), (3, 8, 8200), (40, 0, 2056)])
+def test_either_of_what_the_backward_needs_alone(B, n, C, q8):
+    """n = 0: a residual's sum.  What is written does not depend on what else is."""
+    g = Guarded()
+    X, R = g.put(streams(B + C, B, max(n, 1), C)), g.put(streams(C, B, 1, C)[:, 0])
+    gain, h = g.put(1 + normal(1, C, std=0.2, dtype=F32)), g.put(torch.sigmoid(normal(2, B, max(n, 1))).float())
+
+    def run(H, rstd, Z):
+        tail = "_q8" if q8 else ""
+        if n:
+            getattr(mhc, "mhc_pre_apply_rmsnorm" + tail)(X, h, gain, EPS, B, n, C, H, rstd, *Z)
+        else:
+            getattr(mhc, "mhc_add_rmsnorm" + tail)(X[:, 0], R, gain, EPS, B, C, H, rstd, *Z)
+
+    all_H, all_rstd, all_Z = outputs(g, B, C, q8, True)
+    run(all_H, all_rstd, all_Z)
+    for only_H in (False, True):
+        H, rstd, Z = outputs(g, B, C, q8, True)
+        run(H if only_H else None, None if only_H else rstd, Z)
+        torch.cuda.synchronize()
+        g.check()
+        assert all(torch.equal(a, b) for a, b in zip(Z, all_Z))
+        assert torch.equal(H, all_H) if only_H else torch.equal(rstd, all_rstd)
+
+
 @pytest.mark.parametrize("into", ["new", "A", "R", "none", "alone"])
 @pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("B,C", ADD)
