@@ -32,11 +32,11 @@
 //
 // Bound by memory, all else is kept behind it: 3.6 instructions a value for the sum and 4.4 for
 // the gradient, two exponentials at 32 a clock and SM.  Of the copy rate of 6.78 TB/s: loss of
-// 2048 rows of 131072 bf16, K = 64, 83 us, 0.96; with the gradient 4095 rows of 32000, K = 32,
-// 92.6 us, 0.84 (14 rounds of rows for 13.5); 4096 of 131072, K = 128, 357 us, 0.89 (blocks of a
-// cluster wait for one another); 500 rows of 50001 fp32 37 us, 0.79 (7 rounds for 6.6).  Few
+// 2048 rows of 131072 bf16, K = 64, 84 us, 0.95; with the gradient 4095 rows of 32000, K = 32,
+// 93.2 us, 0.83 (14 rounds of rows for 13.5); 4096 of 131072, K = 128, 350 us, 0.91 (blocks of a
+// cluster wait for one another); 500 rows of 50001 fp32 35.8 us, 0.82 (7 rounds for 6.6).  Few
 // rows: 5.6 us, the call.  Above K = 256 the entries' warp sets the pace: 4096 rows of 32000
-// with the gradient 91 us at K = 128, 98 at 256, 138 at 512, 330 at 1024.
+// with the gradient 91 us at K = 128, 96 at 256, 137 at 512, 339 at 1024.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -617,11 +617,6 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             reinterpret_cast<T *>(mine + v / VEC * 32)[v % VEC] = L::lowest();
         }
     };
-    // Clusters fetch the next row behind the answer, which keeps less in flight while they wait
-    // for one another: 4096 rows of 131072 359 us, 377 where a row is fetched as its place is
-    // free; 2000 of fp32 321, 335.  A block alone does not (4095 rows of 32000 94, 93), nor do
-    // clusters that have few rows (500 rows of fp32, 50001, seven a cluster: 39, 37).
-    const bool late = GRAD && S > 1 && a.B > 8 * step;
     if (in_range(1601, first, 1, a.B)) fetch(first, 0);
     __syncthreads();
     int turn = 0, place = 0;  // place: of the marks, by rows in threes or by segments in turn
@@ -656,7 +651,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             for (int j = 0; j < ITEMS; ++j) v[j] = mine[j * 32];
             if (q + 1 < Q)
                 fetch(b, q + 1);
-            else if (!late && b + step < a.B)
+            else if (!GRAD && b + step < a.B)
                 fetch(b + step, 0);
 
             Peak p;
@@ -689,8 +684,12 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         block_arrive_turn(kSummed, turn, threads + 64);
         pass(b);
         if constexpr (GRAD) {
+            // The next row here, not as soon as its place is free: less is in flight while other
+            // blocks sum up.  4096 rows of 131072 350 us, 378 as soon as may be, 358 behind the
+            // answer; 4096 of 50304 138, 145; 500 of 50001 in fp32 35.8, 37.2; but 4096 of
+            // 32000 in fp32 174, 169.
+            if (b + step < a.B) fetch(b + step, 0);
             block_sync(kAnswered, threads + 32);
-            if (late && b + step < a.B) fetch(b + step, 0);
             const float4 o = sh.out;
             const uint64_t minus_r = f2_pack(-o.y, -o.y), times = f2_pack(o.x, o.x);
             T *out = a.dz + b * a.ld + lo + at0 * VEC;
