@@ -32,7 +32,7 @@
 //
 // Bound by memory, all else is kept behind it: 3.6 instructions a value for the sum and 4.4 for
 // the gradient, two exponentials at 32 a clock and SM.  Of the copy rate of 6.78 TB/s: loss of
-// 2048 rows of 131072 bf16, K = 64, 84 us, 0.95; with the gradient 4095 rows of 32000, K = 32,
+// 2048 rows of 131072 bf16, K = 64, 82 us, 0.97; with the gradient 4095 rows of 32000, K = 32,
 // 93.2 us, 0.83 (14 rounds of rows for 13.5); 4096 of 131072, K = 128, 350 us, 0.91 (blocks of a
 // cluster wait for one another); 500 rows of 50001 fp32 35.8 us, 0.82 (7 rounds for 6.6).  Few
 // rows: 5.6 us, the call.  Above K = 256 the entries' warp sets the pace: 4096 rows of 32000
@@ -649,11 +649,6 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             strike(marks.y, 32);
 #pragma unroll
             for (int j = 0; j < ITEMS; ++j) v[j] = mine[j * 32];
-            if (q + 1 < Q)
-                fetch(b, q + 1);
-            else if (!GRAD && b + step < a.B)
-                fetch(b + step, 0);
-
             Peak p;
             p.m = L::template largest<ITEMS>(v);
             const float r = reference(p.m);
@@ -677,6 +672,12 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 rest = p;
             else
                 rest = merge(rest, p, c);
+            // The next segment (with a gradient: below) behind the sum, not as soon as its place is
+            // free: 2048 rows of 131072 82 us, 84; 16384 of 8192 68, 70.
+            if (q + 1 < Q)
+                fetch(b, q + 1);
+            else if (!GRAD && b + step < a.B)
+                fetch(b + step, 0);
         }
         rest = warp_merge(rest, c);
         if (lane == 0) sh.rest[turn][warp] = make_float2(rest.m, rest.s);
