@@ -18,12 +18,15 @@
 // takes several segments of a row one after another; clusters are for few rows then.
 //
 // Two more warps keep all else away from those.  One takes the K entries, one or two rows
-// ahead: it works out the teacher's sums, fetches the student's logits there and marks the
-// kept ids of a segment in a bit map, a word a thread; the thread overwrites its marked
-// values with -inf before it reads them.  The other joins a row's sums, over warps and over
-// the cluster through distributed shared memory, answers with the factor of the gradient,
+// ahead: it works out the teacher's sums, fetches the student's logits at those of its own
+// segments and marks the kept ids of a segment in a bit map, a word a thread; the thread
+// overwrites its marked values with -inf before it reads them.  A mark that is there already is
+// an id that came before.  The other warp joins a row's sums, over warps and
+// over the cluster through distributed shared memory, answers with the factor of the gradient,
 // and then has the row before to finish: its loss, and what is due at the kept ids, behind
-// what the row's threads wrote there.  dz may be z: a row is written after all of the cluster
+// what the row's threads wrote there.  Where ids repeat it makes one entry of all of an id
+// first (merge_repeats): p_k is their sum.  Each block of a cluster has its own ids' part of the loss;
+// rank 0 adds them up, by rank.  dz may be z: a row is written after all of the cluster
 // has summed it up.
 //
 // Exponentials are exp2((z - m)·c), c = inv_tau·log2 e, m the largest z seen, two values at
@@ -234,27 +237,100 @@ __device__ __noinline__ void store_some(T *p, uint4 v, int n)
         }
 }
 
-// The sum of e^(x - shift) at the entries that are `again`, of the chunks of 32 that have a bit in `repeats`.
-__device__ __forceinline__ float repeated(const int *idk, const float *x, float shift, int again, uint32_t repeats, int Kp)
+// An entry's id, where it is not just that: kRepeat, an entry before has it, too (in the block that
+// holds the id); kFirst, others have it, too, and its x is being added up.
+constexpr int kRepeat = 1 << 30, kFirst = 1 << 29;
+
+// The entries of an id made one: the first gets the x of their sum, log Σ e^(x - shift) + shift, the
+// others are absent from here on.  For one warp; `chunks` has bit j where one of entries 32·j.. is a
+// repeat.  Sums are added in the order of the entries, by chunks.
+//
+// A repeat looks for its first among all entries before it, 128 at once.  Where that would be many, two
+// tables of Kp places each are laid first, one behind the other: an id's entry is at its place in the
+// first unless another has overwritten it, and in that case in the second unless, again, overwritten;
+// so few are left to look.
+constexpr int kFewRepeats = 6;
+__device__ __noinline__ void merge_repeats(float *x, int *ids, uint16_t *table, int Kp, float shift, uint32_t chunks)
 {
-    float sum = 0.f;
+    const int lane = threadIdx.x & 31;
+    const auto repeat = [](int i) { return i >= 0 && (i & kRepeat) != 0; };
+    const auto place1 = [&](int id) { return table + __umulhi(static_cast<uint32_t>(id) * 0x9E3779B1u, Kp); };
+    const auto place2 = [&](int id) { return table + Kp + __umulhi(static_cast<uint32_t>(id) * 0x85EBCA6Bu, Kp); };
+    int repeats = 0;
 #pragma unroll 1
-    for (; repeats != 0; repeats &= repeats - 1) {
-        const int from = (__ffs(static_cast<int>(repeats)) - 1) * 32;
-#pragma unroll 1
-        for (int l = from; l < from + 32 && l < Kp; l += 16) {
-            const int4 *v = reinterpret_cast<const int4 *>(idk + l);
-            bool any = false;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                any |= v[q].x == again | v[q].y == again | v[q].z == again | v[q].w == again;
-            if (!any) continue;
-#pragma unroll 1
-            for (int q = l; q < l + 16; ++q)
-                if (idk[q] == again) sum += expf(x[q] - shift);
-        }
+    for (uint32_t m = chunks; m != 0; m &= m - 1) {
+        const int k = (__ffs(static_cast<int>(m)) - 1) * 32 + lane;
+        repeats += __popc(__ballot_sync(0xffffffffu, k < Kp && repeat(ids[k])));
     }
-    return sum;
+    const bool laid = repeats > kFewRepeats;
+    if (laid) {
+#pragma unroll 4
+        for (int k = lane; k < Kp; k += 32)
+            if (ids[k] >= 0 && !repeat(ids[k])) *place1(ids[k]) = static_cast<uint16_t>(k);
+        __syncwarp();
+#pragma unroll 4
+        for (int k = lane; k < Kp; k += 32)
+            if (ids[k] >= 0 && !repeat(ids[k]) && *place1(ids[k]) != k) *place2(ids[k]) = static_cast<uint16_t>(k);
+        __syncwarp();
+    }
+    uint32_t firsts = 0;  // as `chunks`
+#pragma unroll 1
+    for (uint32_t m = chunks; m != 0; m &= m - 1) {
+        const int base = (__ffs(static_cast<int>(m)) - 1) * 32, k = base + lane, i = k < Kp ? ids[k] : -1;
+        const bool again = repeat(i);
+        const int id = i ^ kRepeat;
+        int first = -1;
+        if (laid && again) {  // a place that nothing was written to holds anything
+            const auto right = [&](int f) { return f < Kp && (ids[f] & ~kFirst) == id; };
+            first = *place1(id);
+            if (!right(first)) first = *place2(id);
+            if (!right(first)) first = -1;
+        }
+        const int end = min(base + 32, Kp);
+#pragma unroll 1
+        for (uint32_t left = __ballot_sync(0xffffffffu, again && first < 0); left != 0; left &= left - 1) {
+            const int from = __ffs(static_cast<int>(left)) - 1, look = __shfl_sync(0xffffffffu, id, from);
+            int f = -1;
+#pragma unroll 4
+            for (int at = lane * 4; at < end; at += 128) {
+                const int4 v = *reinterpret_cast<const int4 *>(ids + at);
+                if ((v.x & ~kFirst) == look) f = at;
+                if ((v.y & ~kFirst) == look) f = at + 1;
+                if ((v.z & ~kFirst) == look) f = at + 2;
+                if ((v.w & ~kFirst) == look) f = at + 3;
+            }
+            f = __reduce_max_sync(0xffffffffu, f);
+            if (lane == from) first = f;
+        }
+        const float e = again ? expf(x[k] - shift) : 0.f;
+        if (again) ids[k] = -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, first >= 0 ? first : -1 - lane);
+        float sum = e;
+        if (__any_sync(0xffffffffu, (same & (same - 1)) != 0)) {
+            sum = 0.f;
+#pragma unroll 8
+            for (int l = 0; l < 32; ++l) {
+                const float more = __shfl_sync(0xffffffffu, e, l);
+                if ((same >> l & 1) != 0) sum += more;
+            }
+        }
+        if (first >= 0 && lane == __ffs(static_cast<int>(same)) - 1) {
+            const bool added = (ids[first] & kFirst) != 0;
+            x[first] = (added ? x[first] : expf(x[first] - shift)) + sum;
+            ids[first] |= kFirst;
+            firsts |= 1u << (first >> 5);
+        }
+        __syncwarp();
+    }
+    firsts = __reduce_or_sync(0xffffffffu, firsts);
+#pragma unroll 1
+    for (; firsts != 0; firsts &= firsts - 1) {
+        const int k = (__ffs(static_cast<int>(firsts)) - 1) * 32 + lane;
+        if (k >= Kp || ids[k] < 0 || (ids[k] & kFirst) == 0) continue;
+        ids[k] ^= kFirst;
+        x[k] = logf(x[k]) + shift;
+    }
+    __syncwarp();
 }
 
 constexpr int kPlaces = 4;  // rows whose entries are held: one to finish, one summed up, two ahead
@@ -267,13 +343,12 @@ struct Info {               // of a row's entries
 };
 struct Shared {
     float2 rests[2][kMaxCluster][kMaxWarps], kepts[2][kMaxCluster];  // the cluster's peaks
+    float2 parts[2][kMaxCluster];  // rank 0: the blocks' parts of a loss, at the end of the last two
     float4 out;                   // the gradient: what to multiply by, the reference, whether there is one
     float2 rest[2][kMaxWarps];    // peaks by warp
     uint2 marks[3][kMaxThreads];  // bit j·VEC + e: value e of the thread's piece j is kept
     Info info[kPlaces];
 };
-// Marks an entry whose id an entry before it has, in the block that holds the id.
-constexpr int kRepeat = 1 << 30;
 __host__ __device__ constexpr int room_of(int K) { return (K + 15) & ~15; }  // entries
 // The block's barriers:
 //   kSegment   (without a gradient) a segment's marks are there, and the one before is done
@@ -310,19 +385,31 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
     const float c = a.inv_tau * kLog2e;
     const int64_t step = gridDim.x / S, first = blockIdx.x / S;
     // [kPlaces][K, to a multiple of 16] each: x = t·inv_tau less the row's largest (t_lse: not
-    // less), the word that z lies in, the id (-1: absent); then a row's entries as they come
+    // less), the word that z lies in, the id (-1: absent, or kRepeat); then a row's entries as they come
     const int Kp = room_of(a.K);
     float *const xs = reinterpret_cast<float *>(dyn + warps * kWarpPieces);
     uint32_t *const words = reinterpret_cast<uint32_t *>(xs + kPlaces * Kp);
     int *const ids = reinterpret_cast<int *>(words + kPlaces * Kp);
     int64_t *const came_ids = reinterpret_cast<int64_t *>(ids + kPlaces * Kp);
     float *const came_ts = reinterpret_cast<float *>(came_ids + Kp);
+    uint16_t *const table = reinterpret_cast<uint16_t *>(came_ts + Kp);  // [2][K, to a multiple of 16]: merge_repeats'
     // A row's barrier of the cluster, for the warps that do not wait for the others' sums:
     // they take part a row behind.
     const auto pass = [&](int64_t b) {
         if (S > 1) {
             if (b != first) cluster_wait();
             cluster_arrive_relaxed();
+        }
+    };
+    // Their last part is in the last row's barrier and in the one of the last losses.
+    const bool losses = !GRAD || a.loss != nullptr;
+    const auto leave = [&] {
+        if (S > 1) {
+            cluster_wait();
+            if (losses) {
+                cluster_arrive_relaxed();
+                cluster_wait();
+            }
         }
     };
 
@@ -367,6 +454,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             const uint32_t fresh = __ballot_sync(0xffffffffu, in && !marked);
             return in && ((same & fresh) == 0 || lane != __ffs(static_cast<int>(same)) - 1);
         };
+        uint32_t chunks = 0;  // bit j: this lane has found a repeat in entries 32·j.. of the row prepared last
         // Row b into its place, its first segment's kept ids into `marks`; after read_ahead(b).
         const auto prepare = [&](int64_t b, int place, uint2 *marks) {
             if (b >= a.B) {
@@ -381,7 +469,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             float m = -INFINITY;
             bool some = false;
             ptx::cp_async_wait_all();  // read_ahead's
-            uint32_t chunks = 0;
+            chunks = 0;
 #pragma unroll 4
             for (int base = 0; base < Kp; base += 32) {
                 const int k = base + lane;
@@ -393,16 +481,17 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 if (here) {
                     some = true;
                     m = fmaxf(m, t);
-                    if ((rank == 0 || static_cast<unsigned>(i - lo) < mine_values) && in_range(1605, i, 1, a.V))
+                    if (static_cast<unsigned>(i - lo) < mine_values && in_range(1605, i, 1, a.V))
                         ptx::cp_async4(word + k, row + (i & -L::kWord));
                 }
                 const bool in = i >= lo && i - lo < count, again = repeats(in, i, in && mark(marks, i - lo));
-                if (again) chunks |= 1u << (k >> 5);
+                if (again) chunks |= 1u << (base >> 5);
                 if (k < Kp) idk[k] = again ? i | kRepeat : i;
             }
             ptx::cp_async_commit();
             some = __any_sync(0xffffffffu, some);
-            chunks = __reduce_or_sync(0xffffffffu, chunks);
+            uint32_t repeats_of_all = 0;
+            if constexpr (GRAD) repeats_of_all = __reduce_or_sync(0xffffffffu, chunks);
             // the difference first: t times inv_tau may overflow where t is the type's lowest value
             m = a.t_lse != nullptr ? 0.f : warp_max(m);
             float s = 0.f;
@@ -419,11 +508,11 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 r.mass = a.t_lse != nullptr ? s : 1.f;
                 r.w = dloss * a.inv_tau;
                 r.some = some;
-                r.repeats = chunks;
+                if constexpr (GRAD) r.repeats = repeats_of_all;
             }
             __syncwarp();
         };
-        // The peak at the kept ids of this block, each once (absent and repeated ones lie outside).
+        // The peak at the kept ids of this block, each once.
         const auto peak = [&](int place) {
             const uint32_t *word = words + place * Kp;
             const int *idk = ids + place * Kp;
@@ -469,10 +558,15 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                     for (int base = 0; base < Kp; base += 32) {
                         const int k = base + lane, i = k < Kp ? idk[k] : -1;
                         const bool in = i >= from && i - from < count;
-                        if (repeats(in, i, in && mark(sh.marks[unit], i - from))) idk[k] = i | kRepeat;
+                        if (repeats(in, i, in && mark(sh.marks[unit], i - from))) {
+                            idk[k] = i | kRepeat;
+                            chunks |= 1u << (base >> 5);
+                        }
                     }
                     __syncwarp();
                 }
+                const uint32_t all = __reduce_or_sync(0xffffffffu, chunks);
+                if (lane == 0) sh.info[place].repeats = all;
             }
             if constexpr (GRAD)
                 cp_async_wait_but<2>();
@@ -491,55 +585,51 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         }
         if constexpr (!GRAD) block_sync(kSegment, threads + 32);
         block_sync_turn(kJoined, turn ^ 1, 64);
-        if (S > 1) cluster_wait();
+        leave();
         return;
     }
 
     if (warp > warps) {  // ---- joining
-        // What a joined row leaves to do: its loss, and the gradient at the kept ids.
+        // What a joined row leaves to do at this block's kept ids: their part of the loss, and the gradient.
         const auto finish = [&](int64_t b, int place, Peak rest, Peak whole) {
+            const Info &r = sh.info[place];
+            if (r.repeats != 0)
+                merge_repeats(xs + place * Kp, ids + place * Kp, table, Kp, a.t_lse != nullptr ? r.base : 0.f, r.repeats);
             const float *x = xs + place * Kp;
             const uint32_t *word = words + place * Kp;
             const int *idk = ids + place * Kp;
-            const Info &r = sh.info[place];
             const float base = r.base, unit = r.unit, mass = r.mass, w = r.w, shift = a.t_lse != nullptr ? base : 0.f;
-            const uint32_t repeats = r.repeats;
             const bool some = r.some;
             const float p_rest = a.t_lse != nullptr && rest.s != 0.f ? fmaxf(1.f - mass, 0.f) : 0.f;
-            const bool losses = rank == 0 && a.loss != nullptr;
             const float ln_s = logf(whole.s), factor = w * (mass + p_rest) / whole.s, ref = reference(whole.m);
             float part = 0.f;
 #pragma unroll 2
             for (int k = lane; k < a.K; k += 32) {
                 const int i = idk[k];
-                const bool here = static_cast<unsigned>(i - lo) < mine_values;  // and no repeat
-                if (!here && !(losses && i >= 0)) continue;
+                if (static_cast<unsigned>(i - lo) >= mine_values) continue;
                 const float p = expf(x[k] - shift) * unit, z = L::word(word[k], i);
                 if (losses && p != 0.f) part += p * (x[k] - base - ((z - whole.m) * a.inv_tau - ln_s));
                 if constexpr (GRAD) {
-                    if (here && repeats == 0 && in_range(1604, i, 1, a.V))
+                    if (in_range(1604, i, 1, a.V))
                         a.dz[b * a.ld + i] = L::from(fmaf(exp2_fast((z - ref) * c), factor, -(w * p)));
-                }
-            }
-            if (GRAD && repeats != 0) {
-#pragma unroll 1
-                for (int k = lane; k < a.K; k += 32) {
-                    const int i = idk[k];
-                    if (static_cast<unsigned>(i - lo) >= mine_values || !in_range(1604, i, 1, a.V)) continue;
-                    const float all = unit * (expf(x[k] - shift) + repeated(idk, x, shift, i | kRepeat, repeats, Kp));
-                    a.dz[b * a.ld + i] = L::from(fmaf(exp2_fast((L::word(word[k], i) - ref) * c), factor, -(w * all)));
                 }
             }
             if (losses) {
                 part = warp_sum(part);
-                if (lane == 0) {
-                    if (p_rest > 0.f)
-                        part += p_rest * (logf(p_rest) - ((rest.m - whole.m) * a.inv_tau + logf(rest.s) - ln_s));
-                    a.loss[b] = some ? part : 0.f;
-                }
+                if (rank == 0 && p_rest > 0.f)
+                    part += p_rest * (logf(p_rest) - ((rest.m - whole.m) * a.inv_tau + logf(rest.s) - ln_s));
+                if (!some) part = 0.f;
+                if (S == 1 && lane == 0) a.loss[b] = part;
             }
             __syncwarp();
+            return part;
         };
+        // Row b's loss from what the blocks of the cluster have for it, in rank 0.
+        const auto add_up = [&](int64_t b, float part) {
+            part = warp_sum(lane < S ? part : 0.f);
+            if (lane == 0 && in_range(1606, b, 1, a.B)) a.loss[b] = part;
+        };
+        float part = 0.f;  // of the last finished row
         __syncthreads();
         Peak last_rest = {}, last_whole = {};
         int turn = 0, place = 0;
@@ -553,6 +643,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 if (lane < warps)
                     for (int i = 0; i < S; ++i) st_cluster(&sh.rests[turn][rank][lane], i, make_float2(rest.m, rest.s));
                 if (lane < S) st_cluster(&sh.kepts[turn][rank], lane, make_float2(kept.m, kept.s));
+                if (losses && lane == 0) st_cluster(&sh.parts[turn][rank], 0, make_float2(part, 0.f));
                 cluster_arrive_release();
                 cluster_wait();
                 rest = kept = {-INFINITY, 0.f};
@@ -583,14 +674,27 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 __syncwarp();
                 block_arrive(kAnswered, threads + 32);
             }
+            if (S > 1 && losses && rank == 0 && b - step > first)
+                add_up(b - 2 * step, sh.parts[turn][lane % kMaxCluster].x);
             // everyone's stores of the row before precede this row's sums
-            if (b != first) finish(b - step, (place + kPlaces - 1) % kPlaces, last_rest, last_whole);
+            if (b != first) part = finish(b - step, (place + kPlaces - 1) % kPlaces, last_rest, last_whole);
             block_arrive_turn(kJoined, turn, 64);
             last_rest = rest;
             last_whole = whole;
         }
         if constexpr (GRAD) block_sync(kWritten, threads + 32);
-        finish(first + (a.B - 1 - first) / step * step, (place + kPlaces - 1) % kPlaces, last_rest, last_whole);
+        const int64_t last = first + (a.B - 1 - first) / step * step;
+        const float end = finish(last, (place + kPlaces - 1) % kPlaces, last_rest, last_whole);
+        if (S > 1 && losses) {
+            if (lane == 0) st_cluster(&sh.parts[turn][rank], 0, make_float2(part, end));
+            cluster_arrive_release();
+            cluster_wait();
+            if (rank == 0) {
+                const float2 p = sh.parts[turn][lane % kMaxCluster];
+                if (last != first) add_up(last - step, p.x);
+                add_up(last, p.y);
+            }
+        }
         return;
     }
 
@@ -730,7 +834,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         block_arrive(kWritten, threads + 32);
     else
         block_sync(kSegment, threads + 32);
-    if (S > 1) cluster_wait();
+    leave();
 }
 
 // Blocks a row (a power of two up to 8), segments a block, warps that hold a segment and
@@ -739,7 +843,7 @@ struct Plan {
     int S, Q, seg, warps, items;
 };
 constexpr int kPieces = 4096;    // a segment's most, but where a gradient needs all and 8 blocks do not reach
-constexpr int kEntryBytes = kPlaces * 12 + 12;
+constexpr int kEntryBytes = kPlaces * 12 + 12 + 4;
 constexpr int kMinPieces = 256;  // rows are split further only down to this
 
 template <typename T>
