@@ -618,6 +618,8 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 part = warp_sum(part);
                 if (rank == 0 && p_rest > 0.f)
                     part += p_rest * (logf(p_rest) - ((rest.m - whole.m) * a.inv_tau + logf(rest.s) - ln_s));
+                // z has no distribution (all -inf, a NaN, +inf), or the teacher's sum is no number
+                if (!(whole.s > 0.f) || !(r.mass < INFINITY)) part = NAN;
                 if (!some) part = 0.f;
                 if (S == 1 && lane == 0) a.loss[b] = part;
             }
@@ -668,7 +670,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                     // q_rest·(M - p_rest/q_rest) = M·q_rest - p_rest, shared out by exp2 over the rest's sum
                     const float q_rest = rest.s == 0.f ? 0.f : rest.s * exp2_fast((rest.m - whole.m) * c) / whole.s;
                     const float scale = rest.s != 0.f ? r.w * ((r.mass + p_rest) * q_rest - p_rest) / rest.s
-                                                      : whole.s != 0.f ? 0.f : NAN;
+                                                      : whole.s > 0.f ? 0.f : NAN;
                     sh.out = make_float4(scale, reference(rest.m), r.some ? 1.f : 0.f, 0.f);
                 }
                 __syncwarp();

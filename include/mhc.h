@@ -530,7 +530,8 @@ int mhc_rmsnorm_backward(const mhc_bf16 *dZ, const mhc_bf16 *H, const float *gai
  * entropy.  A row without entries has loss 0 and dz 0, whatever its z (padding).  z may hold
  * -inf (a masked vocabulary); where a kept id with p > 0 has it, the loss is +inf.  Any
  * other row with a NaN or +inf in z, or with z = -inf throughout, has loss and dz NaN.  A NaN
- * or +inf in t makes the row's loss NaN; so may a t_lse that is not finite.
+ * or +inf in t, or a p_k that is +inf in fp32 (x_k far above t_lse), makes the row's loss NaN;
+ * so may a t_lse that is not finite.
  *
  * The backward works from z alone, in one pass: a training step that knows dloss [B] fp32
  * (1/rows, times tau² where that is wanted) needs no forward call.  Its loss may be NULL.
