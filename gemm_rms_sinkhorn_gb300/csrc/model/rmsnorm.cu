@@ -365,7 +365,7 @@ rmsnorm_backward_kernel(const NormBackwardArgs a, int G, int T, float *__restric
         float lo, hi;
         f2_unpack(ss, lo, hi);
         const float sum = group_sum(lo + hi, red[turn], group * warps, warps);
-        const float back = -(rstd * rstd * (sum * inv_C));
+        const float back = -(rstd * (rstd * (sum * inv_C)));  // rstd² alone may be past fp32: tiny rows, eps = 0
         const uint64_t bb = f2_pack(back, back);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
