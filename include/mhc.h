@@ -477,7 +477,8 @@ int mhc_pre_backward(const mhc_bf16 *dX_next, const mhc_bf16 *dF_pre, const uint
  * n = 1 reads it): e4m3 codes, a power-of-two scale for each 32 channels.
  *
  * H and rstd may each be NULL where they are not wanted (the backward needs both).  R may
- * be NULL: the norm of A alone; H then has to be NULL.  H may be exactly A or exactly R.
+ * be NULL: the norm of A alone; H then has to be NULL.  H may be exactly A or
+ * exactly R, or both where they are one.
  * Rules, layouts and status codes otherwise as the calls above, and C <= 16384
  * (MHC_ERR_UNSUPPORTED); eps finite and >= 0 (MHC_ERR_INVALID).  Squares are summed in
  * fp32.  A row of zeros with eps = 0 has rstd = 0 and Z = 0.
