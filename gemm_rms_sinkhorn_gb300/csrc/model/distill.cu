@@ -795,7 +795,14 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             // blocks sum up.  4096 rows of 131072 350 us, 378 as soon as may be, 358 behind the
             // answer; 4096 of 50304 138, 145; 500 of 50001 in fp32 35.8, 37.2; but 4096 of
             // 32000 in fp32 174, 169.
-            if (b + step < a.B) fetch(b + step, 0);
+            if (b + step < a.B) {
+                fetch(b + step, 0);
+                // With few blocks on an SM and none to wait for, a block's reads and writes go better
+                // apart: 4095 rows of 32000 84 us, 94 without; 8192 of 20000 105, 121; in fp32 of 16384
+                // 177, 184.  Not so where 8 warps or fewer hold a row (16384 of 8192 101, 98) and in
+                // clusters (4096 of 50304 140, 135).
+                if (S == 1 && warps > 8) ptx::cp_async_wait_all();
+            }
             block_sync(kAnswered, threads + 32);
             const float4 o = sh.out;
             const uint64_t minus_r = f2_pack(-o.y, -o.y), times = f2_pack(o.x, o.x);
