@@ -109,19 +109,6 @@ __device__ __forceinline__ void st_cluster(float2 *p, uint32_t rank, float2 v)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
 }
-template <int N>  // all copies of this thread have landed but those of its last N groups
-__device__ __forceinline__ void cp_async_wait_but()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void cp_async8(void *dst, const void *src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async16(void *dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
-}
 
 // ---- the logits' types, by pieces of 16 bytes
 template <typename T>
@@ -432,7 +419,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 const float *t = a.t + b * a.K;
 #pragma unroll 4
                 for (int k = lane; k < a.K; k += 32) {
-                    cp_async8(came_ids + k, id + k);
+                    ptx::cp_async8(came_ids + k, id + k);
                     ptx::cp_async4(came_ts + k, t + k);
                 }
                 if (a.t_lse != nullptr) lse = ptx::ld_dep(a.t_lse + b);
@@ -569,9 +556,9 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
                 if (lane == 0) sh.info[place].repeats = all;
             }
             if constexpr (GRAD)
-                cp_async_wait_but<2>();
+                ptx::cp_async_wait_but<2>();
             else
-                cp_async_wait_but<1>();
+                ptx::cp_async_wait_but<1>();
             __syncwarp();
             peak(place);
             block_arrive_turn(kSummed, turn, threads + 64);
@@ -713,7 +700,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j)
             if (j * 32 < left && in_range(1602, lo + q * seg + (at0 + j * 32) * VEC, VEC, a.ld))
-                cp_async16(mine + j * 32, row + j * 32 * VEC);
+                ptx::cp_async16(mine + j * 32, row + j * 32 * VEC);
         ptx::cp_async_commit();
     };
     const auto strike = [&](uint32_t bits, int from) {  // values from + 0..31 that have a bit become -inf

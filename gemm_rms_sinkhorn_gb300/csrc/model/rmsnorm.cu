@@ -78,22 +78,6 @@ __device__ __forceinline__ float inverse_root(float ms)
     return y == 0.f ? 0.f : fmaf(0.5f * y, fmaf(-(ms * y), y, 1.f), y);
 }
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async16(void *dst, const void *src, uint64_t policy)
-{
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(dst)), "l"(src),
-                 "l"(policy)
-                 : "memory");
-}
-template <int N>  // all copies of this thread have landed but those of its last N groups
-__device__ __forceinline__ void cp_async_wait_but()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Chunks that a thread has room for, of P pieces of 16 bytes each: what it has read of one
 // makes room for the one that many on.  More in flight is not better (us, with one / two /
 // four): 4 streams, 16384 tokens of 2048 60 / 63 / 62, 4096 of 16384 121 / 127 / 128; 5
@@ -151,9 +135,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rmsnorm_kernel(const NormArgs 
     const uint64_t policy = Q8 ? ptx::policy_evict_first() : 0;
     const auto copy = [&](uint4 *dst, const uint16_t *src) {
         if constexpr (Q8)
-            cp_async16(dst, src, policy);
+            ptx::cp_async16(dst, src, policy);
         else
-            cp_async16(dst, src);
+            ptx::cp_async16(dst, src);
     };
     const auto fetch = [&](uint4 *slot, uint32_t b, int64_t row, int k) {
         if (b < B && live[k] && in_range(1501, b, 1, a.B)) {
@@ -204,7 +188,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rmsnorm_kernel(const NormArgs 
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             uint4 *const x = slots + k % kSlots * P * stride;
-            cp_async_wait_but<kSlots - 1>();
+            ptx::cp_async_wait_but<kSlots - 1>();
 #pragma unroll
             for (int p = 0; p < 4; ++p) f[k][p] = 0;
             if (have && live[k]) {
@@ -298,9 +282,9 @@ rmsnorm_backward_kernel(const NormBackwardArgs a, int G, int T, float *__restric
     const auto fetch = [&](uint4 *slot, uint32_t b, int64_t row, int k) {
         if (b < B && live[k] && in_range(1511, b, 1, a.B)) {
             const int64_t at = row + (k * G + g) * 8;
-            cp_async16(slot, a.dZ + at);
-            cp_async16(slot + stride, a.H + at);
-            if constexpr (SKIP) cp_async16(slot + 2 * stride, a.dH_skip + at);
+            ptx::cp_async16(slot, a.dZ + at);
+            ptx::cp_async16(slot + stride, a.H + at);
+            if constexpr (SKIP) ptx::cp_async16(slot + 2 * stride, a.dH_skip + at);
         }
         ptx::cp_async_commit();
     };
@@ -344,7 +328,7 @@ rmsnorm_backward_kernel(const NormBackwardArgs a, int G, int T, float *__restric
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             uint4 *const x = slots + k % kSlots * P * stride;
-            cp_async_wait_but<kSlots - 1>();
+            ptx::cp_async_wait_but<kSlots - 1>();
             dz[k] = hv[k] = sk[k] = make_uint4(0, 0, 0, 0);
             if (have && live[k]) {
                 dz[k] = x[0];

@@ -329,15 +329,36 @@ __device__ __forceinline__ void prefetch_l2(const void *p)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// 4-byte asynchronous copy global -> shared (both 4-byte aligned); completes
-// at the issuing thread's next cp_async_wait_all.
+// Asynchronous copies global -> shared of 4, 8 or 16 bytes (both aligned to that); they
+// complete at the issuing thread's next cp_async_wait_all, or by groups.
 __device__ __forceinline__ void cp_async4(void *smem_dst, const void *src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(src)
                  : "memory");
 }
+__device__ __forceinline__ void cp_async8(void *smem_dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem_dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async16(void *smem_dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async16(void *smem_dst, const void *src, uint64_t policy)
+{
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)),
+                 "l"(src), "l"(policy)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+template <int N>  // all but those of the last N groups
+__device__ __forceinline__ void cp_async_wait_but()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ uint4 ld_stream_v4(const void *p)
 {
