@@ -21,13 +21,12 @@
 // ahead: it works out the teacher's sums, fetches the student's logits at those of its own
 // segments and marks the kept ids of a segment in a bit map, a word a thread; the thread
 // overwrites its marked values with -inf before it reads them.  A mark that is there already is
-// an id that came before.  The other warp joins a row's sums, over warps and
-// over the cluster through distributed shared memory, answers with the factor of the gradient,
-// and then has the row before to finish: its loss, and what is due at the kept ids, behind
-// what the row's threads wrote there.  Where ids repeat it makes one entry of all of an id
-// first (merge_repeats): p_k is their sum.  Each block of a cluster has its own ids' part of the loss;
-// rank 0 adds them up, by rank.  dz may be z: a row is written after all of the cluster
-// has summed it up.
+// an id that came before.  The other warp joins a row's sums, over warps and over the cluster
+// through distributed shared memory, answers with the factor of the gradient, and then has the
+// row before to finish: its loss, and what is due at the kept ids, behind what the row's threads
+// wrote there.  Where ids repeat it makes one entry of all of an id first (merge_repeats): p_k is
+// their sum.  Each block of a cluster has its own ids' part of the loss; rank 0 adds them up, by
+// rank.  dz may be z: a row is written after all of the cluster has summed it up.
 //
 // Exponentials are exp2((z - m)·c), c = inv_tau·log2 e, m the largest z seen, two values at
 // a time.  As one fused multiply-add z·c - m·c they would be off by what m·c rounds away:
@@ -35,11 +34,14 @@
 //
 // Bound by memory, all else is kept behind it: 3.6 instructions a value for the sum and 4.4 for
 // the gradient, two exponentials at 32 a clock and SM.  Of the copy rate of 6.78 TB/s: loss of
-// 2048 rows of 131072 bf16, K = 64, 82 us, 0.97; with the gradient 4095 rows of 32000, K = 32,
-// 93.2 us, 0.83 (14 rounds of rows for 13.5); 4096 of 131072, K = 128, 350 us, 0.91 (blocks of a
-// cluster wait for one another); 500 rows of 50001 fp32 35.8 us, 0.82 (7 rounds for 6.6).  Few
+// 2048 rows of 131072 bf16, K = 64, 81 us, 0.98; with the gradient 4095 rows of 32000, K = 32,
+// 84 us, 0.93 (14 rounds of rows for 13.5); 4096 of 131072, K = 128, 348 us, 0.91 (blocks of a
+// cluster wait for one another); 500 rows of 50001 fp32 36.8 us, 0.80 (7 rounds for 6.6).  Few
 // rows: 5.6 us, the call.  Above K = 256 the entries' warp sets the pace: 4096 rows of 32000
-// with the gradient 91 us at K = 128, 96 at 256, 137 at 512, 339 at 1024.
+// with the gradient 90 us at K = 128, 97 at 256, 140 at 512, 335 at 1024.  Repeats cost the
+// joining warp: loss / with the gradient, one repeat in every row 63 / 97 us at K = 128 (53 / 90
+// without), 312 / 343 at 1024 (302 / 335); every id twice 71 / 106 and 589 / 629.
+// All figures here and below are of calls back to back over inputs larger than L2.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -235,7 +237,8 @@ constexpr int kRepeat = 1 << 30, kFirst = 1 << 29;
 // A repeat looks for its first among all entries before it, 128 at once.  Where that would be many, two
 // tables of Kp places each are laid first, one behind the other: an id's entry is at its place in the
 // first unless another has overwritten it, and in that case in the second unless, again, overwritten;
-// so few are left to look.
+// so few are left to look.  4096 rows of 32000, K = 128, loss, us, looking / with tables: 2 repeats a
+// row 62 / 66, 6 64 / 68, 8 67 / 69, 12 79 / 75; K = 1024 6 313 / 318, 16 340 / 330; K = 32 6 54 / 53.
 constexpr int kFewRepeats = 6;
 __device__ __noinline__ void merge_repeats(float *x, int *ids, uint16_t *table, int Kp, float shift, uint32_t chunks)
 {
@@ -766,7 +769,7 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
             else
                 rest = merge(rest, p, c);
             // The next segment (with a gradient: below) behind the sum, not as soon as its place is
-            // free: 2048 rows of 131072 82 us, 84; 16384 of 8192 68, 70.
+            // free: 2048 rows of 131072 81 us, 88; 16384 of 8192 58, 63; 4096 of 32000 42, 47.
             if (q + 1 < Q)
                 fetch(b, q + 1);
             else if (!GRAD && b + step < a.B)
@@ -779,15 +782,16 @@ distill_kernel(const DistillArgs<T> a, int seg, int S, int segments)
         pass(b);
         if constexpr (GRAD) {
             // The next row here, not as soon as its place is free: less is in flight while other
-            // blocks sum up.  4096 rows of 131072 350 us, 378 as soon as may be, 358 behind the
-            // answer; 4096 of 50304 138, 145; 500 of 50001 in fp32 35.8, 37.2; but 4096 of
-            // 32000 in fp32 174, 169.
+            // blocks sum up.  4096 rows of 131072 348 us, 366 as soon as may be, 354 behind the
+            // answer; 4096 of 50304 135, 145, 142; 500 of 50001 in fp32 37, 38, 40; but 4096 of
+            // 32000 in fp32 174, 169, 166.
             if (b + step < a.B) {
                 fetch(b + step, 0);
                 // With few blocks on an SM and none to wait for, a block's reads and writes go better
-                // apart: 4095 rows of 32000 84 us, 94 without; 8192 of 20000 105, 121; in fp32 of 16384
-                // 177, 184.  Not so where 8 warps or fewer hold a row (16384 of 8192 101, 98) and in
-                // clusters (4096 of 50304 140, 135).
+                // apart: 4095 rows of 32000 84 us, 91 without; 8192 of 20000 106, 122; in fp32 of 16384
+                // 176, 184.  Not so where 8 warps or fewer hold a row (16384 of 8192 102, 99; 4096 of
+                // 16000 47, 45) and in clusters (4096 of 50304 140, 135; of 131072 351, 348; but of 32000
+                // in fp32 165, 174).
                 if (S == 1 && warps > 8) ptx::cp_async_wait_all();
             }
             block_sync(kAnswered, threads + 32);

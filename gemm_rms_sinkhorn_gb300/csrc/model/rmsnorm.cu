@@ -9,7 +9,8 @@
 // Bound by memory.  Of the copy rate of 6.78 TB/s: 8 streams, 8191 tokens of 4096 98 us, 1.0; a
 // residual, 16384 tokens of 7168 148 us, 0.94; 4 streams, 16384 of 7168 in 8 bits with the
 // unpacking behind it 209 us, 0.92; the backward of 16384 tokens of 7168 148 us, 0.94.  One
-// token: 3.1 us with the unpacking, in a graph.
+// token: 3.1 us with the unpacking, in a graph.  A alone, 16384 tokens of 7168: 77 us, 0.90, but
+// in 8 bits 91, 0.58.
 //
 // Blocks walk the tokens.  A group of G threads takes a token, a thread chunks of 8 channels
 // g, g + G, ... of it, the same ones in every token.  It copies the chunks of the next tokens
@@ -35,7 +36,7 @@ constexpr int kMaxThreads = 512;
 // How a token of C channels is laid over threads: `items` chunks of 8 channels a thread,
 // `group` threads a token, `tokens` tokens a block of `most` threads.  The backward, where a
 // block ends with its row of the workspace, takes blocks of 512: 16384 tokens of 2048 47 us,
-// 59 with 256.
+// 57 with 256.
 struct Layout {
     int items, group, tokens;
 };
@@ -79,12 +80,16 @@ __device__ __forceinline__ float inverse_root(float ms)
 }
 
 // Chunks that a thread has room for, of P pieces of 16 bytes each: what it has read of one
-// makes room for the one that many on.  More in flight is not better (us, with one / two /
-// four): 4 streams, 16384 tokens of 2048 60 / 63 / 62, 4096 of 16384 121 / 127 / 128; 5
-// streams, 8191 tokens of 4096 68 / 69 / 70; a residual, 16384 tokens of 2048 43 / 46 / 47.
-// Two are where a chunk is small (one stream, 16384 tokens of 4096 68 / 65 / 67; a residual,
-// 16384 of 7168 151 / 148 / 152) and where blocks are few (8 streams, 4096 tokens of 7168
-// 86 / 85).  The backward with a gradient past the norm, 16384 of 7168: 159 / 148.
+// makes room for the one that many on.  More in flight is mostly not better (us back to back,
+// with one / two / four): 3 streams, 16384 tokens of 4096 98 / 104 / 107; 4 streams, 16384 of 2048
+// 50.5 / 50.0 / 50.7; 5 streams, 8191 of 4096 68 / 70 / 70; a residual, 16384 of 2048 43 / 46 / 48;
+// but 4 streams, 4096 of 16384 104 / 102 / 100 and 2 streams, 16384 of 4096 84 / 86 / 88, which
+// have the other's.  Two are where a chunk is small (one stream, 16384 of 4096 69 / 65 / 67; a
+// residual, 16384 of 7168 152 / 148 / 152, in 8 bits 149 / 127 / 140) and where blocks are few (8
+// streams, 8191 of 4096 99.5 / 98.5, 4096 of 7168 86 / 85, of 16384 203 / 197, there with one block
+// an SM).  A norm of A alone goes by the residual's: 16384 of 7168 98 / 77 / 80, 8192 of 16384
+// 118 / 98 / 83, but of 2048 26 / 23 / 23.  The backward, with a gradient past the norm, 16384 of
+// 7168 with one 161, with two 148.
 __host__ __device__ constexpr int slots_of(int P, int items)
 {
     return P == 1 || P == 8 || (P == 2 && items > 1) ? 2 : 1;
@@ -130,8 +135,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) rmsnorm_kernel(const NormArgs 
     const int64_t in_step = static_cast<int64_t>(step) * (n == 0 ? 1 : n) * C;
     // 8 bits: what is read is marked to leave L2 first and the codes are stored plainly, so
     // that the kernel that reads them next finds some there (B = 16384, n = 4, C = 7168, with
-    // the unpacking 224 us without, 213 with).  Not so in bf16: n = 8, 8191 tokens of 4096
-    // took 98.5 us without the mark and 102.6 with it.
+    // the unpacking 221 us without, 209 with).  In bf16 it is all the same: n = 8, 8191 tokens of
+    // 4096 took 99 us either way.
     const uint64_t policy = Q8 ? ptx::policy_evict_first() : 0;
     const auto copy = [&](uint4 *dst, const uint16_t *src) {
         if constexpr (Q8)
